@@ -378,6 +378,195 @@ MOE_W8A8_API moe_status_t moe_w8a8_read_probe(const void *ptr, size_t bytes, voi
 MOE_W8A8_API moe_status_t moe_w8a8_read_write_probe(const void *src, size_t src_bytes, void *dst, size_t dst_bytes,
                                                     void *stream);
 
+/*
+ * moe_w8a8_forward on activations that are quantised already (by
+ * moe_w8a8_norm_quant, or by a program of the caller's own): the block then
+ * skips its own quantisation of x. Results are bit for bit those of
+ * moe_w8a8_forward on any x whose codes and scales these are.
+ *
+ *  q_x      [T, H] codes: int8 (MOE_WEIGHT_INT8) or FP8 E4M3 (MOE_WEIGHT_MXFP4)
+ *  x_scale  fp32 [T] (quant_mode 1) or [T, H / quant_group] (quant_mode 2);
+ *           element i of token t stands for q_x[t][i] * its scale
+ *
+ * Both 16-byte aligned, and required unless T == 0. There are no smooth
+ * scales: they multiply x before its quantisation, by expert, which codes
+ * cannot express. Every other argument, and the errors, are those of
+ * moe_w8a8_forward.
+ */
+MOE_W8A8_API moe_status_t moe_w8a8_forward_quantized(const moe_w8a8_dims_t *dims,
+                              const void *q_x,
+                              const float *x_scale,
+                              const int32_t *expert_ids,
+                              const float *expert_scales,
+                              const int8_t *gmm1_weight,
+                              const float *gmm1_weight_scale,
+                              const int8_t *gmm2_weight,
+                              const float *gmm2_weight_scale,
+                              const int8_t *share_gmm1_weight,
+                              const float *share_gmm1_weight_scale,
+                              const int8_t *share_gmm2_weight,
+                              const float *share_gmm2_weight_scale,
+                              const uint8_t *x_active_mask,
+                              void *output,
+                              void *share_output,
+                              int32_t *expert_token_nums,
+                              void *workspace,
+                              size_t workspace_bytes,
+                              const moe_w8a8_debug_t *dbg,
+                              void *stream);
+
+/* ------------------------------------------------------------------------
+ * Around the expert block: the pre-norm, the router, and the dense products
+ * of the same model with 4-bit weights. The conventions at the top of this
+ * file hold for them too; with num_tokens == 0 a call does nothing, whatever
+ * its pointers.
+ * ------------------------------------------------------------------------ */
+
+/* Element types of the operators below. */
+enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_FP16 = 1, MOE_DTYPE_FP32 = 2, MOE_DTYPE_INT8 = 3 };
+/* 8-bit outputs of moe_w8a8_norm_quant. */
+enum { MOE_QUANT_NONE = 0, MOE_QUANT_INT8 = 1, MOE_QUANT_E4M3 = 2 };
+
+typedef struct {
+    int32_t num_tokens;   /* T in [0, 65536]                                          */
+    int32_t hidden;       /* H in [1, 16384], any size                                */
+    int32_t dtype;        /* of x, residual, residual_out and y: BF16, FP16 or FP32   */
+    int32_t weight_dtype; /* of weight: the same as dtype, or FP32                    */
+    int32_t quant;        /* MOE_QUANT_*: what q holds                                */
+    int32_t quant_group;  /* 0: one scale per row; 64, 128 or 256 (dividing H): one   */
+                          /*   per row and group of that many consecutive elements    */
+    float rms_eps;        /* >= 1e-30: added to the mean square                       */
+    float amax_eps;       /* >= 1e-20: floor of an amax, as in moe_w8a8_dims_t        */
+} moe_w8a8_norm_dims_t;
+
+/*
+ * Residual addition, root-mean-square norm and 8-bit quantisation in one pass:
+ *
+ *   r = x + residual                         (fp32; residual_out = r rounded)
+ *   y = r * weight / sqrt(mean(r^2) + rms_eps)  (fp32; y rounded once)
+ *   codes of y before its rounding, by the block's own rule: a' = max(max|y|,
+ *   amax_eps), scale = a' / 127 (int8) or a' / 448 (E4M3), q = y / scale
+ *   rounded to nearest even
+ *
+ * q and q_scale are what moe_w8a8_forward_quantized (and, one scale per row,
+ * moe_w8a8_linear_w4) take. With p = r * weight, y / max|y| = p / max|p|: the
+ * codes are computed from p, so they do not depend on the order in which the
+ * squares are summed (rows under the amax floor apart).
+ *
+ *  x             [T, H]
+ *  residual      [T, H] or NULL (then r = x, and residual_out must be NULL)
+ *  weight        [H] or NULL (all ones)
+ *  residual_out  [T, H] or NULL
+ *  y             [T, H] or NULL
+ *  q, q_scale    [T, H] bytes, and fp32 [T] or [T, H / quant_group]; both NULL
+ *                iff quant == MOE_QUANT_NONE
+ *
+ * Every pointer is 16-byte aligned (q_scale: 4). residual_out and y may be x
+ * or residual themselves (not both the same one); any other overlap of an
+ * output with anything is refused. At least one of y and q is given. A row
+ * whose values are not finite, or whose squares' sum leaves fp32, is
+ * unspecified; the other rows are not affected by it.
+ */
+MOE_W8A8_API moe_status_t moe_w8a8_norm_quant(const moe_w8a8_norm_dims_t *dims, const void *x, const void *residual,
+                                              const void *weight, void *residual_out, void *y, void *q,
+                                              float *q_scale, void *stream);
+
+/* Scores of the router. */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1, MOE_SCORE_SQRT_SOFTPLUS = 2 };
+
+typedef struct {
+    int32_t num_tokens;     /* T in [0, 65536]                                        */
+    int32_t hidden;         /* H in [1, 16384], any size                              */
+    int32_t moe_expert_num; /* E in [1, 1024]                                         */
+    int32_t topk;           /* K in [1, min(16, E)]                                   */
+    int32_t score;          /* MOE_SCORE_*: softmax over the experts, 1/(1+exp(-l)),  */
+                            /*   or sqrt(log(1 + exp(l)))                             */
+    int32_t normalize;      /* 1: a token's weights are divided by their sum          */
+    int32_t dtype;          /* of x: BF16, FP16 or FP32                               */
+    int32_t weight_dtype;   /* of weight: the same as dtype, or BF16 or FP32          */
+    float route_scale;      /* finite: every weight is multiplied by it at the end    */
+} moe_w8a8_gate_dims_t;
+
+/*
+ * The router: logits, scores and top-k choice of experts, whose results are
+ * moe_w8a8_forward's expert_ids and expert_scales.
+ *
+ *   l[t,e] = sum_h x[t,h] * weight[e,h];  s = score(l)
+ *   the K experts with the largest s + bias (of l where bias is NULL: every
+ *   score rises with l), in falling order, ties to the lowest id
+ *   weight of a chosen expert: s (without bias), over the chosen ones' sum if
+ *   `normalize`, times route_scale; rounded once, to fp32
+ *
+ * Everything up to that rounding is computed in 64 bits, so that the choice
+ * between two experts does not depend on the order of a sum.
+ *
+ *  x              [T, H]
+ *  weight         [E, H]
+ *  bias           fp32 [E] or NULL. -infinity takes an expert out
+ *  expert_ids     int32 [T, K]
+ *  expert_scales  fp32 [T, K]
+ *  workspace      >= moe_w8a8_gate_workspace_size() bytes, 256-byte aligned
+ *
+ * Where fewer than K experts are left (by the bias, or because a logit is
+ * NaN), the places that remain get id -1, which the block drops, and weight 0.
+ * x and weight are 16-byte aligned, the others 4. The outputs overlap nothing.
+ */
+MOE_W8A8_API moe_status_t moe_w8a8_gate_workspace_size(const moe_w8a8_gate_dims_t *dims, size_t *bytes);
+MOE_W8A8_API moe_status_t moe_w8a8_gate(const moe_w8a8_gate_dims_t *dims, const void *x, const void *weight,
+                                        const float *bias, int32_t *expert_ids, float *expert_scales,
+                                        void *workspace, size_t workspace_bytes, void *stream);
+
+typedef struct {
+    int32_t num_tokens;   /* T in [0, 65536]                                          */
+    int32_t out_features; /* N in [1, 2^20]; even when gated                          */
+    int32_t in_features;  /* K in [1, 2^17], a multiple of group; N * K <= about 2^34 */
+    int32_t group;        /* 32, 64 or 128 consecutive k share a scale                */
+    int32_t act_dtype;    /* of x: BF16, FP16 or INT8                                 */
+    int32_t gated;        /* 0: out [T, N]; 1: rows [0, N/2) are the gate, [N/2, N)   */
+                          /*   the up projection, out [T, N/2] = silu(gate) * up      */
+    int32_t has_zeros;    /* 1: zero points per row and group; 0: all of them 8       */
+} moe_w8a8_linear_w4_dims_t;
+
+/*
+ * Dense product with 4-bit weights:
+ *
+ *   o[t,n] = x_scale[t] * sum_k x[t,k] * (code[n,k] - zero[n,k/group]) * scale[n,k/group] + bias[n]
+ *
+ * and out = o, or SwiGLU of its halves (gated), rounded once. A group's sum is
+ * exact for INT8 x and in fp32 otherwise; groups are summed in fp32.
+ *
+ * The weights are re-laid once, at load time, for one (N, K, group, act_dtype
+ * kind, gated, has_zeros); num_tokens may differ from call to call, and BF16
+ * and FP16 share one layout.
+ *
+ *  codes    uint8 [N, K/2]: element k in the low nibble of byte k/2 when k is
+ *           even, the high nibble when odd
+ *  scale    fp32 [N, K/group]
+ *  zero     uint8 [N, K/group], values 0..15; NULL iff has_zeros == 0
+ *  dst      moe_w8a8_packed_w4_bytes() bytes, 16-byte aligned: 1024 bytes of
+ *           codes per 16 rows and 128 k (both padded with zeros), then the
+ *           scales and the zero points of those tiles in the same order. Gated:
+ *           a tile holds 8 gate rows and their 8 up rows in turn
+ */
+MOE_W8A8_API moe_status_t moe_w8a8_packed_w4_bytes(const moe_w8a8_linear_w4_dims_t *dims, size_t *bytes);
+MOE_W8A8_API moe_status_t moe_w8a8_pack_weights_w4(const moe_w8a8_linear_w4_dims_t *dims, const uint8_t *codes,
+                                                   const float *scale, const uint8_t *zero, void *dst,
+                                                   void *stream);
+/*
+ *  x        [T, K], 16-byte aligned
+ *  x_scale  fp32 [T] for INT8 x, else NULL
+ *  weight   from moe_w8a8_pack_weights_w4 with the same dims
+ *  bias     fp32 [N] or NULL
+ *  out      bf16 (BF16 and INT8 x) or fp16 (FP16 x) [T, N] or [T, N/2],
+ *           16-byte aligned, overlapping nothing
+ *
+ * x is taken to be finite, and below 2^100 in magnitude; a token's outputs
+ * depend on no other token's row. No workspace.
+ */
+MOE_W8A8_API moe_status_t moe_w8a8_linear_w4(const moe_w8a8_linear_w4_dims_t *dims, const void *x,
+                                             const float *x_scale, const void *weight, const float *bias, void *out,
+                                             void *stream);
+
 /* Static description of a status code. Never NULL. */
 MOE_W8A8_API const char *moe_w8a8_status_string(moe_status_t status);
 

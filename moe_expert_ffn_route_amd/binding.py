@@ -23,10 +23,19 @@ NOALLOC_SCRATCH_BYTES = 32 << 20  # MOE_W8A8_NOALLOC_SCRATCH_BYTES
 
 EXPORTS = ("moe_w8a8_workspace_size", "moe_w8a8_forward", "moe_w8a8_forward_noalloc", "moe_w8a8_pack_weights",
            "moe_w8a8_packed_mx_bytes", "moe_w8a8_pack_weights_mx", "moe_w8a8_warm", "moe_w8a8_read_probe",
-           "moe_w8a8_read_write_probe", "moe_w8a8_status_string")
+           "moe_w8a8_read_write_probe", "moe_w8a8_status_string", "moe_w8a8_forward_quantized", "moe_w8a8_norm_quant",
+           "moe_w8a8_gate_workspace_size", "moe_w8a8_gate", "moe_w8a8_packed_w4_bytes", "moe_w8a8_pack_weights_w4",
+           "moe_w8a8_linear_w4")
 MOE_WEIGHT_ROW_MAJOR, MOE_WEIGHT_PACKED = 0, 1
 MOE_WEIGHT_INT8, MOE_WEIGHT_MXFP4 = 0, 1
 MOE_PACK_GMM1, MOE_PACK_GMM2 = 1, 2
+MOE_DTYPE_BF16, MOE_DTYPE_FP16, MOE_DTYPE_FP32, MOE_DTYPE_INT8 = 0, 1, 2, 3
+MOE_QUANT_NONE, MOE_QUANT_INT8, MOE_QUANT_E4M3 = 0, 1, 2
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID, MOE_SCORE_SQRT_SOFTPLUS = 0, 1, 2
+_DTYPE_CODE = {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_FP16, torch.float32: MOE_DTYPE_FP32,
+               torch.int8: MOE_DTYPE_INT8}
+_DTYPE_OF = {code: dt for dt, code in _DTYPE_CODE.items()}
+_QUANT_DTYPE = {MOE_QUANT_INT8: torch.int8, MOE_QUANT_E4M3: torch.float8_e4m3fn}
 
 
 class MoeError(RuntimeError):
@@ -47,6 +56,27 @@ class Dims(ctypes.Structure):
     @property
     def e_loc(self) -> int:
         return self.moe_expert_num // self.ep_rank_size
+
+
+class NormDims(ctypes.Structure):
+    """moe_w8a8_norm_dims_t"""
+    _fields_ = [("num_tokens", ctypes.c_int32), ("hidden", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("weight_dtype", ctypes.c_int32), ("quant", ctypes.c_int32), ("quant_group", ctypes.c_int32),
+                ("rms_eps", ctypes.c_float), ("amax_eps", ctypes.c_float)]
+
+
+class GateDims(ctypes.Structure):
+    """moe_w8a8_gate_dims_t"""
+    _fields_ = [("num_tokens", ctypes.c_int32), ("hidden", ctypes.c_int32), ("moe_expert_num", ctypes.c_int32),
+                ("topk", ctypes.c_int32), ("score", ctypes.c_int32), ("normalize", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32), ("route_scale", ctypes.c_float)]
+
+
+class LinearW4Dims(ctypes.Structure):
+    """moe_w8a8_linear_w4_dims_t"""
+    _fields_ = [("num_tokens", ctypes.c_int32), ("out_features", ctypes.c_int32), ("in_features", ctypes.c_int32),
+                ("group", ctypes.c_int32), ("act_dtype", ctypes.c_int32), ("gated", ctypes.c_int32),
+                ("has_zeros", ctypes.c_int32)]
 
 
 DEBUG_FIELDS = ("sorted_pair", "row_of_pair", "group_offset", "shared_token", "num_rows", "q_x", "xs", "acc1",
@@ -90,6 +120,21 @@ def library() -> ctypes.CDLL:
         L.moe_w8a8_read_probe.argtypes = [P, ctypes.c_size_t, P]
         L.moe_w8a8_read_write_probe.restype = ctypes.c_int
         L.moe_w8a8_read_write_probe.argtypes = [P, ctypes.c_size_t, P, ctypes.c_size_t, P]
+        L.moe_w8a8_forward_quantized.restype = ctypes.c_int
+        L.moe_w8a8_forward_quantized.argtypes = ([ctypes.POINTER(Dims)] + [P] * 17
+                                                 + [ctypes.c_size_t, ctypes.POINTER(Debug), P])
+        L.moe_w8a8_norm_quant.restype = ctypes.c_int
+        L.moe_w8a8_norm_quant.argtypes = [ctypes.POINTER(NormDims)] + [P] * 8
+        L.moe_w8a8_gate_workspace_size.restype = ctypes.c_int
+        L.moe_w8a8_gate_workspace_size.argtypes = [ctypes.POINTER(GateDims), ctypes.POINTER(ctypes.c_size_t)]
+        L.moe_w8a8_gate.restype = ctypes.c_int
+        L.moe_w8a8_gate.argtypes = [ctypes.POINTER(GateDims)] + [P] * 6 + [ctypes.c_size_t, P]
+        L.moe_w8a8_packed_w4_bytes.restype = ctypes.c_int
+        L.moe_w8a8_packed_w4_bytes.argtypes = [ctypes.POINTER(LinearW4Dims), ctypes.POINTER(ctypes.c_size_t)]
+        L.moe_w8a8_pack_weights_w4.restype = ctypes.c_int
+        L.moe_w8a8_pack_weights_w4.argtypes = [ctypes.POINTER(LinearW4Dims)] + [P] * 5
+        L.moe_w8a8_linear_w4.restype = ctypes.c_int
+        L.moe_w8a8_linear_w4.argtypes = [ctypes.POINTER(LinearW4Dims)] + [P] * 6
         L.moe_w8a8_status_string.restype = ctypes.c_char_p
         L.moe_w8a8_status_string.argtypes = [ctypes.c_int]
         _lib = L
@@ -243,6 +288,167 @@ def moe_w8a8_forward_noalloc(dims: Dims, x, expert_ids, expert_scales, gmm1_weig
     if check and rc != MOE_OK:
         raise MoeError(rc, "moe_w8a8_forward_noalloc")
     return rc
+
+
+def moe_w8a8_forward_quantized(dims: Dims, q_x, x_scale, expert_ids, expert_scales, gmm1_weight, gmm1_weight_scale,
+                               gmm2_weight, gmm2_weight_scale, share_gmm1_weight=None, share_gmm1_weight_scale=None,
+                               share_gmm2_weight=None, share_gmm2_weight_scale=None, x_active_mask=None, output=None,
+                               share_output=None, expert_token_nums=None, workspace=None,
+                               workspace_bytes: Optional[int] = None, dbg: Optional[Debug] = None, stream=None,
+                               check: bool = True) -> int:
+    """moe_w8a8_forward on codes and scales that moe_w8a8_norm_quant (or the
+    caller) made of x: q_x [T, H] int8 or float8_e4m3fn, x_scale fp32 [T] or
+    [T, H / quant_group]. Returns the status code; raises MoeError on failure
+    when check=True."""
+    if workspace_bytes is None:
+        workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    args = [q_x, x_scale, expert_ids, expert_scales, gmm1_weight, gmm1_weight_scale, gmm2_weight, gmm2_weight_scale,
+            share_gmm1_weight, share_gmm1_weight_scale, share_gmm2_weight, share_gmm2_weight_scale, x_active_mask,
+            output, share_output, expert_token_nums, workspace]
+    rc = library().moe_w8a8_forward_quantized(ctypes.byref(dims), *[_ptr(a) for a in args], workspace_bytes,
+                                              ctypes.byref(dbg) if dbg is not None else None, _stream(stream))
+    if check and rc != MOE_OK:
+        raise MoeError(rc, "moe_w8a8_forward_quantized")
+    return rc
+
+
+# ------------------------------------------- operators around the block
+# These take tensors only, and check their types, sizes and device: a call
+# whose tensors do not fit its dims raises ValueError before the library sees
+# it. They run on the tensors' device, whichever device is current.
+
+def _arg(t, name: str, dtype, numel: int, device: int) -> Optional[int]:
+    """The device pointer of an argument of `numel` elements (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() != numel:
+        raise ValueError(f"{name}: expected {numel} elements of {dtype}, got {tuple(t.shape)} of {t.dtype}")
+    if t.get_device() != device or device < 0:
+        raise ValueError(f"{name}: expected a tensor on the GPU that holds the call's first tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensors passed to libmoe_w8a8 must be contiguous")
+    return t.data_ptr()
+
+
+def _call(where: str, fn, device: int, stream, *args) -> None:
+    """fn(*args, stream) with `device` current; the stream defaults to that
+    device's current one."""
+    if torch.cuda.current_device() != device:
+        with torch.cuda.device(device):
+            return _call(where, fn, device, stream, *args)
+    rc = fn(*args, torch.cuda.current_stream(device).cuda_stream if stream is None else _stream(stream))
+    if rc != MOE_OK:
+        raise MoeError(rc, where)
+
+
+def _code(dt) -> int:
+    if dt not in _DTYPE_CODE:
+        raise ValueError(f"unsupported element type {dt}")
+    return _DTYPE_CODE[dt]
+
+
+def make_norm_dims(num_tokens, hidden, dtype=torch.bfloat16, weight_dtype=None, quant=MOE_QUANT_INT8, quant_group=0,
+                   rms_eps=1e-6, amax_eps=1e-6) -> NormDims:
+    return NormDims(num_tokens, hidden, _code(dtype), _code(dtype if weight_dtype is None else weight_dtype), quant,
+                    quant_group, rms_eps, amax_eps)
+
+
+def moe_w8a8_norm_quant(dims: NormDims, x, weight=None, residual=None, residual_out=None, y=None, q=None,
+                        q_scale=None, stream=None) -> None:
+    """Residual addition, RMS norm and 8-bit quantisation of x [T, H] in one
+    pass; writes those of residual_out, y, q and q_scale that are given (see
+    the header). residual_out and y may be x or residual themselves."""
+    T, H, g = dims.num_tokens, dims.hidden, dims.quant_group
+    dt, n, dev = _DTYPE_OF.get(dims.dtype), dims.num_tokens * dims.hidden, x.get_device()
+    _call("moe_w8a8_norm_quant", library().moe_w8a8_norm_quant, dev, stream, ctypes.byref(dims),
+          _arg(x, "x", dt, n, dev), _arg(residual, "residual", dt, n, dev),
+          _arg(weight, "weight", _DTYPE_OF.get(dims.weight_dtype), H, dev),
+          _arg(residual_out, "residual_out", dt, n, dev), _arg(y, "y", dt, n, dev),
+          _arg(q, "q", _QUANT_DTYPE.get(dims.quant), n, dev),
+          _arg(q_scale, "q_scale", torch.float32, T * (H // g) if g > 0 else T, dev))
+
+
+def make_gate_dims(num_tokens, hidden, moe_expert_num, topk, score=MOE_SCORE_SOFTMAX, normalize=True,
+                   route_scale=1.0, dtype=torch.bfloat16, weight_dtype=None) -> GateDims:
+    return GateDims(num_tokens, hidden, moe_expert_num, topk, score, int(normalize), _code(dtype),
+                    _code(dtype if weight_dtype is None else weight_dtype), route_scale)
+
+
+def moe_w8a8_gate_workspace_size(dims: GateDims) -> int:
+    n = ctypes.c_size_t(0)
+    rc = library().moe_w8a8_gate_workspace_size(ctypes.byref(dims), ctypes.byref(n))
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_w8a8_gate_workspace_size")
+    return int(n.value)
+
+
+def moe_w8a8_gate(dims: GateDims, x, weight, bias=None, expert_ids=None, expert_scales=None, workspace=None,
+                  stream=None):
+    """Router: top-k experts of x [T, H] and their weights. Returns
+    (expert_ids int32 [T, K], expert_scales fp32 [T, K]), allocated if None,
+    as is the workspace."""
+    T, H, E, K = dims.num_tokens, dims.hidden, dims.moe_expert_num, dims.topk
+    dev = x.get_device()
+    if expert_ids is None:
+        expert_ids = torch.empty((T, K), dtype=torch.int32, device=x.device)
+    if expert_scales is None:
+        expert_scales = torch.empty((T, K), dtype=torch.float32, device=x.device)
+    if workspace is None:
+        workspace = torch.empty(max(256, moe_w8a8_gate_workspace_size(dims)), dtype=torch.uint8, device=x.device)
+    n_ws = workspace.numel()
+    _call("moe_w8a8_gate", library().moe_w8a8_gate, dev, stream, ctypes.byref(dims),
+          _arg(x, "x", _DTYPE_OF.get(dims.dtype), T * H, dev),
+          _arg(weight, "weight", _DTYPE_OF.get(dims.weight_dtype), E * H, dev),
+          _arg(bias, "bias", torch.float32, E, dev), _arg(expert_ids, "expert_ids", torch.int32, T * K, dev),
+          _arg(expert_scales, "expert_scales", torch.float32, T * K, dev),
+          _arg(workspace, "workspace", torch.uint8, n_ws, dev), n_ws)
+    return expert_ids, expert_scales
+
+
+def make_linear_w4_dims(num_tokens, out_features, in_features, group=128, act_dtype=torch.bfloat16, gated=False,
+                        has_zeros=False) -> LinearW4Dims:
+    return LinearW4Dims(num_tokens, out_features, in_features, group, _code(act_dtype), int(gated), int(has_zeros))
+
+
+def moe_w8a8_packed_w4_bytes(dims: LinearW4Dims) -> int:
+    b = ctypes.c_size_t(0)
+    rc = library().moe_w8a8_packed_w4_bytes(ctypes.byref(dims), ctypes.byref(b))
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_w8a8_packed_w4_bytes")
+    return int(b.value)
+
+
+def moe_w8a8_pack_weights_w4(dims: LinearW4Dims, codes, scale, zero=None, dst=None, stream=None):
+    """Pack 4-bit weights (codes uint8 [N, K/2], scale fp32 [N, K/group], zero
+    uint8 [N, K/group] if has_zeros) for moe_w8a8_linear_w4 with these dims
+    (num_tokens aside). Returns dst (uint8, allocated if None)."""
+    nbytes, dev = moe_w8a8_packed_w4_bytes(dims), codes.get_device()
+    if dst is None:
+        dst = torch.empty(nbytes, dtype=torch.uint8, device=codes.device)
+    N, K = dims.out_features, dims.in_features
+    groups = N * (K // dims.group)
+    _call("moe_w8a8_pack_weights_w4", library().moe_w8a8_pack_weights_w4, dev, stream, ctypes.byref(dims),
+          _arg(codes, "codes", torch.uint8, N * (K // 2), dev), _arg(scale, "scale", torch.float32, groups, dev),
+          _arg(zero, "zero", torch.uint8, groups, dev), _arg(dst, "dst", torch.uint8, nbytes, dev))
+    return dst
+
+
+def moe_w8a8_linear_w4(dims: LinearW4Dims, x, weight, x_scale=None, bias=None, out=None, stream=None):
+    """Dense product of x [T, K] (bf16, fp16, or int8 with x_scale fp32 [T])
+    with packed 4-bit weights. Returns out (bf16, fp16 for fp16 x; [T, N], or
+    [T, N/2] when gated), allocated if None."""
+    T, N, K = dims.num_tokens, dims.out_features, dims.in_features
+    width = N // 2 if dims.gated else N
+    dt = torch.float16 if dims.act_dtype == MOE_DTYPE_FP16 else torch.bfloat16
+    dev = x.get_device()
+    if out is None:
+        out = torch.empty((T, width), dtype=dt, device=x.device)
+    _call("moe_w8a8_linear_w4", library().moe_w8a8_linear_w4, dev, stream, ctypes.byref(dims),
+          _arg(x, "x", _DTYPE_OF.get(dims.act_dtype), T * K, dev),
+          _arg(x_scale, "x_scale", torch.float32, T, dev),
+          _arg(weight, "weight", torch.uint8, moe_w8a8_packed_w4_bytes(dims), dev),
+          _arg(bias, "bias", torch.float32, N, dev), _arg(out, "out", dt, T * width, dev))
+    return out
 
 
 # ---------------------------------------------------------------- helpers

@@ -224,8 +224,11 @@ static moe_status_t check_call(const moe_w8a8_dims_t *d, const void *x, const in
     return MOE_OK;
 }
 
-// The block on a caller-given workspace (both forward entry points).
-static moe_status_t forward_impl(const moe_w8a8_dims_t *d, const void *x, const int32_t *expert_ids,
+// The block on a caller-given workspace (every forward entry point). x_scale:
+// null when x is bf16; else x holds codes and x_scale their scales, and the
+// routing launch quantises nothing.
+static moe_status_t forward_impl(const moe_w8a8_dims_t *d, const void *x, const float *x_scale,
+                                 const int32_t *expert_ids,
                                  const float *expert_scales, const int8_t *gmm1_weight, const float *gmm1_weight_scale,
                                  const int8_t *gmm2_weight, const float *gmm2_weight_scale,
                                  const int8_t *share_gmm1_weight, const float *share_gmm1_weight_scale,
@@ -302,7 +305,7 @@ static moe_status_t forward_impl(const moe_w8a8_dims_t *d, const void *x, const 
     tq.E_g = d->moe_expert_num;
     tq.E_loc = E;
     tq.base = ra.base;
-    tq.q_tok = (T > 0 && (routed_tok || shared_tok)) ? reinterpret_cast<int8_t *>(ws + L.q_tok) : nullptr;
+    tq.q_tok = (T > 0 && !x_scale && (routed_tok || shared_tok)) ? reinterpret_cast<int8_t *>(ws + L.q_tok) : nullptr;
     tq.s_tok = reinterpret_cast<float *>(ws + L.xs_tok);
     tq.smooth = T > 0 ? expert_smooth_scales : nullptr;
     tq.share_smooth = T > 0 && shared ? share_smooth_scales : nullptr;
@@ -327,11 +330,13 @@ static moe_status_t forward_impl(const moe_w8a8_dims_t *d, const void *x, const 
         g.H = H;
         g.E_loc = E;
         g.row_token = ra.row_token;
-        g.A_r = routed_tok ? tq.q_tok : tq.q_sm;
-        g.a_scale_r = routed_tok ? tq.s_tok : tq.s_sm;
+        const int8_t *q_tok = x_scale ? static_cast<const int8_t *>(x) : tq.q_tok;
+        const float *s_tok = x_scale ? x_scale : tq.s_tok;
+        g.A_r = routed_tok ? q_tok : tq.q_sm;
+        g.a_scale_r = routed_tok ? s_tok : tq.s_sm;
         g.idx_r = routed_tok ? ra.row_token : ra.sorted_pair;
-        g.A_s = shared_tok ? tq.q_tok : tq.q_sm + sh_row0 * H;
-        g.a_scale_s = shared_tok ? tq.s_tok : tq.s_sm + sh_row0 * ngx;
+        g.A_s = shared_tok ? q_tok : tq.q_sm + sh_row0 * H;
+        g.a_scale_s = shared_tok ? s_tok : tq.s_sm + sh_row0 * ngx;
         g.a_ng = ngx;
         g.gsteps = grp ? d->quant_group / 64 : 0;
         return g;
@@ -489,10 +494,27 @@ extern "C" moe_status_t moe_w8a8_forward(const moe_w8a8_dims_t *d, const void *x
                                          void *output, void *share_output, int32_t *expert_token_nums,
                                          void *workspace, size_t workspace_bytes, const moe_w8a8_debug_t *dbg,
                                          void *stream) {
-    return forward_impl(d, x, expert_ids, expert_scales, gmm1_weight, gmm1_weight_scale, gmm2_weight,
+    return forward_impl(d, x, nullptr, expert_ids, expert_scales, gmm1_weight, gmm1_weight_scale, gmm2_weight,
                         gmm2_weight_scale, share_gmm1_weight, share_gmm1_weight_scale, share_gmm2_weight,
                         share_gmm2_weight_scale, expert_smooth_scales, share_smooth_scales, x_active_mask, output,
                         share_output, expert_token_nums, workspace, workspace_bytes, dbg, stream);
+}
+
+extern "C" moe_status_t moe_w8a8_forward_quantized(
+    const moe_w8a8_dims_t *d, const void *q_x, const float *x_scale, const int32_t *expert_ids,
+    const float *expert_scales, const int8_t *gmm1_weight, const float *gmm1_weight_scale, const int8_t *gmm2_weight,
+    const float *gmm2_weight_scale, const int8_t *share_gmm1_weight, const float *share_gmm1_weight_scale,
+    const int8_t *share_gmm2_weight, const float *share_gmm2_weight_scale, const uint8_t *x_active_mask, void *output,
+    void *share_output, int32_t *expert_token_nums, void *workspace, size_t workspace_bytes,
+    const moe_w8a8_debug_t *dbg, void *stream) {
+    const moe_status_t st = check_dims(d);
+    if (st != MOE_OK) return st;
+    if (d->num_tokens > 0 && (!q_x || !x_scale)) return MOE_ERR_INVALID_ARG;
+    if (x_scale && !aligned(x_scale, 16)) return MOE_ERR_INVALID_ARG;
+    return forward_impl(d, q_x, x_scale, expert_ids, expert_scales, gmm1_weight, gmm1_weight_scale, gmm2_weight,
+                        gmm2_weight_scale, share_gmm1_weight, share_gmm1_weight_scale, share_gmm2_weight,
+                        share_gmm2_weight_scale, nullptr, nullptr, x_active_mask, output, share_output,
+                        expert_token_nums, workspace, workspace_bytes, dbg, stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -541,7 +563,7 @@ extern "C" moe_status_t moe_w8a8_forward_noalloc(
     if (make_layout(d).total > static_cast<size_t>(MOE_W8A8_NOALLOC_SCRATCH_BYTES)) return MOE_ERR_SCRATCH_LIMIT;
     void *ws = scratch_on_current_device();
     if (!ws) return MOE_ERR_HIP;
-    return forward_impl(d, x, expert_ids, expert_scales, gmm1_weight, gmm1_weight_scale, gmm2_weight,
+    return forward_impl(d, x, nullptr, expert_ids, expert_scales, gmm1_weight, gmm1_weight_scale, gmm2_weight,
                         gmm2_weight_scale, share_gmm1_weight, share_gmm1_weight_scale, share_gmm2_weight,
                         share_gmm2_weight_scale, expert_smooth_scales, share_smooth_scales, x_active_mask, output,
                         share_output, expert_token_nums, ws, MOE_W8A8_NOALLOC_SCRATCH_BYTES, dbg, stream);

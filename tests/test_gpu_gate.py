@@ -1,0 +1,180 @@
+"""moe_w8a8_gate on the GPU against the formula in 64 bits on the CPU.
+
+Ids are equal: the inputs are random, so two choice values lie within the
+1e-14 that a 64-bit sum may be off only by design (equal rows, checked for the
+lowest id). Weights: everything before the rounding to fp32 is in 64 bits, so
+2^-24 relative, and 1e-10 for the sums and exp."""
+import pytest
+import torch
+
+import moe_expert_ffn_route_amd as moe
+
+pytestmark = pytest.mark.gpu
+BF, FP, F32 = torch.bfloat16, torch.float16, torch.float32
+SOFTMAX, SIGMOID, SQRTSP = moe.MOE_SCORE_SOFTMAX, moe.MOE_SCORE_SIGMOID, moe.MOE_SCORE_SQRT_SOFTPLUS
+
+
+def make(T, H, E, dt=BF, wdt=BF, bias=False, seed=0):
+    g = torch.Generator().manual_seed(seed + 31 * T + 7 * H + E)
+    x = torch.randn(T, H, generator=g).to(dt)
+    w = (torch.randn(E, H, generator=g) * (1.5 / H ** 0.5)).to(wdt)
+    return x, w, torch.randn(E, generator=g) * 0.05 if bias else None
+
+
+def formula(x, w, b, K, score, normalize, route_scale):
+    l = x.double() @ w.double().t()
+    s = {SOFTMAX: lambda: torch.softmax(l, 1), SIGMOID: lambda: torch.sigmoid(l),
+         SQRTSP: lambda: (torch.clamp(l, min=0) + torch.log1p(torch.exp(-l.abs()))).sqrt()}[score]()
+    c = l if b is None else s + b.double()
+    ids = torch.sort(c, dim=1, descending=True, stable=True)[1][:, :K]
+    v = s.gather(1, ids)
+    if normalize:
+        v = v / v.sum(1, keepdim=True)
+    return ids, v * route_scale
+
+
+def run(x, w, b, K, score=SOFTMAX, normalize=True, route_scale=1.0, stream=None):
+    d = moe.make_gate_dims(x.shape[0], x.shape[1], w.shape[0], K, score=score, normalize=normalize,
+                           route_scale=route_scale, dtype=x.dtype, weight_dtype=w.dtype)
+    n = x.shape[0] * K
+    ids = torch.full((n + 64,), -7, dtype=torch.int32, device="cuda")
+    sc = torch.full((n + 64,), -7.0, device="cuda")
+    ws = torch.full((moe.moe_w8a8_gate_workspace_size(d) + 256,), 0xA5, dtype=torch.uint8, device="cuda")
+    need = ws.numel() - 256
+    moe.moe_w8a8_gate(d, x.cuda(), w.cuda(), bias=None if b is None else b.cuda(), expert_ids=ids[:n],
+                      expert_scales=sc[:n], workspace=ws[:need], stream=stream)
+    torch.cuda.synchronize()
+    assert bool((ids[n:] == -7).all()) and bool((sc[n:] == -7).all()) and bool((ws[need:] == 0xA5).all())
+    return ids[:n].view(-1, K).cpu(), sc[:n].view(-1, K).cpu()
+
+
+def check(got, want):
+    assert torch.equal(got[0].long(), want[0])
+    assert bool(((got[1].double() - want[1]).abs() <= (2.0 ** -24 + 1e-10) * want[1].abs() + 1e-45).all())
+
+
+SIZES = [(1, 1, 1, 1), (1, 4096, 256, 8), (8, 4096, 256, 8), (3, 7, 5, 5), (2, 8, 64, 16), (5, 130, 65, 6), (16, 1000, 128, 4),
+         (17, 2501, 72, 6), (33, 512, 256, 8), (64, 7168, 384, 8), (100, 640, 1024, 16), (129, 1024, 257, 9),
+         (300, 2048, 160, 6), (509, 2501, 72, 6), (1000, 333, 30, 3), (1, 16384, 1024, 16), (2, 16383, 511, 2), (700, 4096, 256, 8)]
+
+
+@pytest.mark.parametrize("T,H,E,K", SIZES)
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID, SQRTSP], ids=["softmax", "sigmoid", "sqrtsoftplus"])
+def test_sizes(T, H, E, K, score):
+    for bias in (False, True):
+        x, w, b = make(T, H, E, bias=bias)
+        check(run(x, w, b, K, score, normalize=bias or K > 3, route_scale=2.5),
+              formula(x, w, b, K, score, bias or K > 3, 2.5))
+
+
+@pytest.mark.parametrize("dt,wdt", [(BF, F32), (FP, FP), (FP, BF), (FP, F32), (F32, BF), (F32, F32)], ids=str)
+@pytest.mark.parametrize("T,H,E,K", [(1, 4096, 256, 8), (7, 1001, 40, 4), (64, 2048, 256, 8), (200, 515, 130, 8), (600, 1024, 64, 6)])
+def test_types(T, H, E, K, dt, wdt):
+    x, w, b = make(T, H, E, dt, wdt, bias=True)
+    check(run(x, w, b, K, SIGMOID), formula(x, w, b, K, SIGMOID, True, 1.0))
+
+
+@pytest.mark.parametrize("T", [3, 40, 600])
+def test_ties_go_to_the_lowest_id(T):
+    x, w, _ = make(T, 1024, 200)
+    w[60:120] = w[0:60]     # every expert of 60..119 ties with one of 0..59
+    w[199] = w[3]
+    l = x.double() @ w.double().t()
+    l[:, 60:120], l[:, 199] = l[:, 0:60], l[:, 3]  # whatever order the library sums each column in
+    want = torch.sort(l, dim=1, descending=True, stable=True)[1][:, :8]
+    ids, sc = run(x, w, None, 8)
+    assert torch.equal(ids.long(), want)
+    v = torch.softmax(l.gather(1, want), 1)
+    assert bool(((sc.double() - v).abs() <= (2.0 ** -24 + 1e-10) * v).all())
+    zero = torch.zeros_like(w)
+    ids, sc = run(x, zero, None, 8)
+    assert ids.tolist() == [list(range(8))] * T and bool((sc == 0.125).all())
+
+
+def test_choice_between_values_that_fp32_sums_cannot_tell_apart():
+    # logits of two experts that differ by 2^-40 of their size: large terms
+    # that cancel, and one small one
+    x = torch.ones(4, 2048, dtype=F32)
+    w = torch.zeros(8, 2048, dtype=F32)
+    w[:, 0::2], w[:, 1::2] = 1024.0, -1024.0
+    w[5, 77] += 2.0 ** -13
+    w[2, 1500] += 2.0 ** -12
+    ids, _ = run(x, w, None, 3)
+    assert ids.tolist() == [[2, 5, 0]] * 4
+
+
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID, SQRTSP])
+@pytest.mark.parametrize("T", [2, 300])
+def test_excluded_experts_and_empty_places(score, T):
+    x, w, b = make(T, 512, 64, bias=True)
+    b[:] = -float("inf")
+    b[[5, 9, 40]] = 0.01
+    ids, sc = run(x, w, b, 6, score)
+    want, v = formula(x, w, b, 3, score, True, 1.0)
+    assert torch.equal(ids[:, :3].long(), want) and bool((ids[:, 3:] == -1).all()) and bool((sc[:, 3:] == 0).all())
+    assert bool(((sc[:, :3].double() - v).abs() <= (2.0 ** -24 + 1e-10) * v).all())
+    b[:] = -float("inf")
+    ids, sc = run(x, w, b, 6, score)
+    assert bool((ids == -1).all()) and bool((sc == 0).all())
+
+
+@pytest.mark.parametrize("T", [6, 400])
+def test_non_finite_token_leaves_the_others(T):
+    x, w, b = make(T, 4096, 256, bias=True)
+    ref = run(x, w, b, 8, SIGMOID)
+    x[1, 5], x[4, 4000] = float("nan"), float("inf")
+    ids, sc = run(x, w, b, 8, SIGMOID)
+    rows = [t for t in range(T) if t not in (1, 4)]
+    assert torch.equal(ids[rows], ref[0][rows]) and torch.equal(sc[rows], ref[1][rows])
+    assert ids.min() >= -1 and ids.max() < 256
+    assert bool((ids[1] == -1).all())  # every logit NaN: no expert
+
+
+def test_extreme_logits():
+    # scores that saturate: the choice without bias still goes by the logit
+    x = torch.full((2, 64), 8.0)
+    x[1] = -8.0
+    w = torch.arange(1, 33, dtype=F32).view(32, 1).repeat(1, 64)
+    for score in (SOFTMAX, SIGMOID, SQRTSP):
+        ids, sc = run(x, w, None, 4, score)
+        assert ids.tolist() == [[31, 30, 29, 28], [0, 1, 2, 3]]
+        assert bool(torch.isfinite(sc).all())
+    ids, sc = run(x, w, None, 4, SIGMOID, normalize=False)
+    assert sc[0].tolist() == [1.0] * 4
+
+
+def test_batch_does_not_change_a_token():
+    x, w, b = make(700, 4096, 256, bias=True)
+    ids, sc = run(x, w, b, 8, SQRTSP)
+    for n in (1, 9, 40, 200):
+        i2, s2 = run(x[:n], w, b, 8, SQRTSP)
+        assert torch.equal(i2, ids[:n])
+        # 64-bit sums in another order, then one rounding to fp32
+        assert bool(((s2 - sc[:n]).abs() <= 2.0 ** -23 * sc[:n]).all())
+
+
+def test_defaults_zero_tokens_and_side_stream():
+    x, w, b = make(12, 1024, 64)
+    want = run(x, w, None, 4)
+    st = torch.cuda.Stream()
+    d = moe.make_gate_dims(12, 1024, 64, 4)
+    xs, ws = x.cuda(), w.cuda()
+    torch.cuda.synchronize()
+    ids, sc = torch.empty(12, 4, dtype=torch.int32, device="cuda"), torch.empty(12, 4, device="cuda")
+    work = torch.empty(moe.moe_w8a8_gate_workspace_size(d), dtype=torch.uint8, device="cuda")
+    moe.moe_w8a8_gate(d, xs, ws, expert_ids=ids, expert_scales=sc, workspace=work, stream=st)
+    st.synchronize()
+    assert torch.equal(ids.cpu(), want[0]) and torch.equal(sc.cpu(), want[1])
+    ids, sc = moe.moe_w8a8_gate(d, xs, ws)
+    assert torch.equal(ids.cpu(), want[0]) and torch.equal(sc.cpu(), want[1])
+    ids, sc = moe.moe_w8a8_gate(moe.make_gate_dims(0, 1024, 64, 4), xs[:0], ws)
+    assert ids.shape == (0, 4) and sc.shape == (0, 4)
+
+
+def test_largest_batch():
+    T, H, E = 65536, 64, 1024  # a workspace of 512 MiB
+    x, w, _ = make(T, H, E, F32, F32, seed=3)
+    ids, sc = run(x, w, None, 2)
+    rows = torch.arange(0, T, 1021)
+    want = formula(x[rows], w, None, 2, SOFTMAX, True, 1.0)
+    check((ids[rows], sc[rows]), want)
