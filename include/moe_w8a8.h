@@ -497,8 +497,10 @@ typedef struct {
  *   weight of a chosen expert: s (without bias), over the chosen ones' sum if
  *   `normalize`, times route_scale; rounded once, to fp32
  *
- * Everything up to that rounding is computed in 64 bits, so that the choice
- * between two experts does not depend on the order of a sum.
+ * The choice is that of 64-bit sums, whatever the types, so that it does not
+ * depend on the order of a sum. The weights come from 64-bit logits too, or,
+ * where x and weight are both BF16 or both FP16, from logits whose sums of 128
+ * products are in fp32.
  *
  *  x              [T, H]
  *  weight         [E, H]

@@ -235,7 +235,8 @@ struct GateArgs {
     const float *bias;
     int32_t *ids;
     float *scales;
-    double *logits;  // workspace
+    double *logits;  // workspace: [parts, T, E]
+    float *mags;     // workspace behind them: sums of |x * w|, [parts, T, E]
     int T, H, E, K, score, normalize, dtype, weight_dtype;
     float route_scale;
 };

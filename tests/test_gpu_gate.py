@@ -2,8 +2,18 @@
 
 Ids are equal: the inputs are random, so two choice values lie within the
 1e-14 that a 64-bit sum may be off only by design (equal rows, checked for the
-lowest id). Weights: everything before the rounding to fp32 is in 64 bits, so
-2^-24 relative, and 1e-10 for the sums and exp."""
+lowest id).
+
+Weights. Types that are not both bf16 or both fp16: everything before the
+rounding to fp32 is in 64 bits, so 2^-24 relative, and 1e-10 for the sums and
+exp. Both 16-bit: a logit is a sum of fp32 sums of 128 exact products, each
+addition off by at most 2^-23 of the magnitudes so far, so off by at most
+B = 128 * 2^-23 * sum |x w|. A score moves by at most B relative (softmax 2 B,
+with its sum), the sum of the chosen ones by as much: 4 B, and 2^-24.
+That is with all roundings agreeing. As they do not, the 2-norm is held to
+4e-6: H additions, each off by 2^-24 of a partial sum that for these inputs is
+at most about 6 * 1.5 * sqrt(128 / H), add up to sqrt(H) * 2^-24 * 102 /
+sqrt(H) = 6e-6 in the worst token and under half of it over all."""
 import pytest
 import torch
 
@@ -48,9 +58,14 @@ def run(x, w, b, K, score=SOFTMAX, normalize=True, route_scale=1.0, stream=None)
     return ids[:n].view(-1, K).cpu(), sc[:n].view(-1, K).cpu()
 
 
-def check(got, want):
+def check(got, want, x, w):
     assert torch.equal(got[0].long(), want[0])
-    assert bool(((got[1].double() - want[1]).abs() <= (2.0 ** -24 + 1e-10) * want[1].abs() + 1e-45).all())
+    err = (got[1].double() - want[1]).abs()
+    tol = torch.full((x.shape[0], 1), 2.0 ** -24 + 1e-10, dtype=torch.float64)
+    if x.dtype == w.dtype and x.dtype != F32:
+        tol += 4 * 2.0 ** -16 * (x.double().abs() @ w.double().abs().t()).amax(1, keepdim=True)
+    assert bool((err <= tol * want[1].abs() + 1e-45).all())
+    assert float(err.norm()) <= 4e-6 * float(want[1].norm())
 
 
 SIZES = [(1, 1, 1, 1), (1, 4096, 256, 8), (8, 4096, 256, 8), (3, 7, 5, 5), (2, 8, 64, 16), (5, 130, 65, 6), (16, 1000, 128, 4),
@@ -64,14 +79,14 @@ def test_sizes(T, H, E, K, score):
     for bias in (False, True):
         x, w, b = make(T, H, E, bias=bias)
         check(run(x, w, b, K, score, normalize=bias or K > 3, route_scale=2.5),
-              formula(x, w, b, K, score, bias or K > 3, 2.5))
+              formula(x, w, b, K, score, bias or K > 3, 2.5), x, w)
 
 
 @pytest.mark.parametrize("dt,wdt", [(BF, F32), (FP, FP), (FP, BF), (FP, F32), (F32, BF), (F32, F32)], ids=str)
 @pytest.mark.parametrize("T,H,E,K", [(1, 4096, 256, 8), (7, 1001, 40, 4), (64, 2048, 256, 8), (200, 515, 130, 8), (600, 1024, 64, 6)])
 def test_types(T, H, E, K, dt, wdt):
     x, w, b = make(T, H, E, dt, wdt, bias=True)
-    check(run(x, w, b, K, SIGMOID), formula(x, w, b, K, SIGMOID, True, 1.0))
+    check(run(x, w, b, K, SIGMOID), formula(x, w, b, K, SIGMOID, True, 1.0), x, w)
 
 
 @pytest.mark.parametrize("T", [3, 40, 600])
@@ -84,11 +99,32 @@ def test_ties_go_to_the_lowest_id(T):
     want = torch.sort(l, dim=1, descending=True, stable=True)[1][:, :8]
     ids, sc = run(x, w, None, 8)
     assert torch.equal(ids.long(), want)
-    v = torch.softmax(l.gather(1, want), 1)
-    assert bool(((sc.double() - v).abs() <= (2.0 ** -24 + 1e-10) * v).all())
+    check((ids, sc), (want, torch.softmax(l.gather(1, want), 1)), x, w)
     zero = torch.zeros_like(w)
     ids, sc = run(x, zero, None, 8)
     assert ids.tolist() == [list(range(8))] * T and bool((sc == 0.125).all())
+
+
+@pytest.mark.parametrize("T", [5, 200])
+@pytest.mark.parametrize("bias", [False, True], ids=["logit", "bias"])
+@pytest.mark.parametrize("dt", [BF, FP], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID, SQRTSP])
+def test_close_logits_are_told_apart(T, bias, dt, score):
+    """Experts in pairs and triples whose rows differ in one last bit of one
+    element: logits that fp32 sums cannot order."""
+    x, w, b = make(T, 2048, 96, dt, dt, bias=bias, seed=17)
+    step = 2.0 ** -8 if dt == BF else 2.0 ** -11
+    for e in range(0, 96, 3):
+        w[e + 1], w[e + 2] = w[e], w[e]
+        k = 7 * e + 5
+        w[e + 1, k], w[e + 2, k] = w[e, k] * (1 + 2 * step), w[e, k] * (1 - 4 * step)
+        if bias:
+            b[e + 1] = b[e + 2] = b[e]
+    w[:, 1000:] *= 16  # sums whose terms dwarf the difference
+    l = x.double() @ w.double().t()
+    gaps = torch.sort(l, dim=1)[0].diff(dim=1)
+    assert float(gaps.min()) < 1e-6 and float(gaps.min()) > 0  # close, and no ties
+    check(run(x, w, b, 9, score), formula(x, w, b, 9, score, True, 1.0), x, w)
 
 
 def test_choice_between_values_that_fp32_sums_cannot_tell_apart():
@@ -112,7 +148,7 @@ def test_excluded_experts_and_empty_places(score, T):
     ids, sc = run(x, w, b, 6, score)
     want, v = formula(x, w, b, 3, score, True, 1.0)
     assert torch.equal(ids[:, :3].long(), want) and bool((ids[:, 3:] == -1).all()) and bool((sc[:, 3:] == 0).all())
-    assert bool(((sc[:, :3].double() - v).abs() <= (2.0 ** -24 + 1e-10) * v).all())
+    check((ids[:, :3], sc[:, :3]), (want, v), x, w)
     b[:] = -float("inf")
     ids, sc = run(x, w, b, 6, score)
     assert bool((ids == -1).all()) and bool((sc == 0).all())
@@ -149,7 +185,8 @@ def test_batch_does_not_change_a_token():
     for n in (1, 9, 40, 200):
         i2, s2 = run(x[:n], w, b, 8, SQRTSP)
         assert torch.equal(i2, ids[:n])
-        # 64-bit sums in another order, then one rounding to fp32
+        # fp32 sums over the same 128 products, added in 64 bits in another
+        # order, then one rounding to fp32
         assert bool(((s2 - sc[:n]).abs() <= 2.0 ** -23 * sc[:n]).all())
 
 
@@ -177,4 +214,4 @@ def test_largest_batch():
     ids, sc = run(x, w, None, 2)
     rows = torch.arange(0, T, 1021)
     want = formula(x[rows], w, None, 2, SOFTMAX, True, 1.0)
-    check((ids[rows], sc[rows]), want)
+    check((ids[rows], sc[rows]), want, x[rows], w)
