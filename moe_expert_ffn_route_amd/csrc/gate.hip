@@ -8,9 +8,9 @@
 // depend on its order would make them depend on the tiling, the batch size
 // and the split of H. They are therefore those of 64-bit logits, in one of
 // two ways:
-//   - x and W both bf16, or both fp16: MFMA with fp32 sums over 128 products,
-//     which are added up in fp64. Beside them the MFMA makes the sums of
-//     |x * w|, which bound how far such a logit is off (kGamma). Where the
+//   - x and W both bf16, or both fp16: MFMA with fp32 sums over 32 or 64
+//     products, which are added up in fp64. |x| |w| (2-norms), which is no
+//     less than the sum of |x * w|, bounds how far such a logit is off. Where the
 //     bound leaves open which of two experts comes first, the choice kernel
 //     computes the logits of those experts again, in fp64.
 //   - other types: fp64 MFMA throughout (their products are exact in it).
@@ -19,6 +19,8 @@
 // workspace; and one wave per token, which adds the parts in order, for
 // scores and choice.
 #include "internal.h"
+
+#include <type_traits>
 
 #include "../../include/moe_w8a8.h"
 
@@ -33,20 +35,22 @@ typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 
 constexpr int kVec = 8;      // elements per lane and load
 constexpr int kStep = 32;    // h per load of a 16-row tile
-constexpr int kChunk = 128;  // products per fp32 sum
+constexpr int kChunk = 128;  // h per stage
 constexpr int kBlock = 256;
-constexpr int kMaxSplit = 16;
-// An fp32 sum of 128 products that are themselves exact, in any order, with
+constexpr int kMaxSplit = 8;
+// An fp32 sum of n products that are themselves exact, in any order, with
 // every addition off by at most one unit in the last place (an adder that
-// truncates): 128 * 2^-23 of the sum of magnitudes.
-constexpr double kGamma = 1.0 / 65536.0;
+// truncates): n * 2^-23 of the sum of magnitudes, which Cauchy's inequality
+// bounds by the norms.
+constexpr double kUnit = 0x1p-23;
 // Products under the smallest normal fp32 may be dropped: 16384 of them.
 constexpr double kTiny = 0x1p-110;
 
-// Eight elements from h = k of a row of H.
-template <typename T>
+// Eight elements from h = k of a row of H. WHOLE: they are known to be there
+// (no branch, so that loads can be issued in a row).
+template <bool WHOLE, typename T>
 __device__ __forceinline__ void load8(const T *row, int k, int H, T (&raw)[kVec]) {
-    if (k + kVec <= H) {
+    if (WHOLE || k + kVec <= H) {
         __builtin_memcpy(raw, row + k, sizeof raw);
     } else {
 #pragma unroll
@@ -74,351 +78,629 @@ __device__ __forceinline__ v4f mfma32(v4i a, v4i b, v4f c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
 }
 
+// n += the squares of eight elements.
+template <typename T>
+__device__ __forceinline__ void add_squares(v4i v, float &n) {
+    if constexpr (__is_same(T, Bf16)) {
+        typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const v2bf p = __builtin_bit_cast(v2bf, v[i]);
+            n = __builtin_amdgcn_fdot2_f32_bf16(p, p, n, false);
+        }
+    } else {
+        typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const v2h p = __builtin_bit_cast(v2h, v[i]);
+            n = __builtin_amdgcn_fdot2(p, p, n, false);
+        }
+    }
+}
+
 __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
     for (int d = kWave / 2; d > 0; d >>= 1) v += __shfl_xor(v, d, kWave);
     return v;
 }
-__device__ __forceinline__ double wave_max(double v) {
-#pragma unroll
-    for (int d = kWave / 2; d > 0; d >>= 1) v = fmax(v, __shfl_xor(v, d, kWave));
-    return v;
+// Largest value of the wave, in every lane (a scalar): DPP shifts by 1, 2, 4
+// and 8 within rows of 16 lanes, the row ends to the next row, row 1's end to
+// rows 2 and 3; lane 63 then holds it. `low` is what an absent lane counts as.
+template <typename I>
+__device__ __forceinline__ I wave_max_int(I v, I low) {
+    auto step = [&](auto ctrl) {
+        const I o = static_cast<I>(__builtin_amdgcn_update_dpp(static_cast<int>(low), static_cast<int>(v),
+                                                               decltype(ctrl)::value, 0xF, 0xF, false));
+        v = v > o ? v : o;
+    };
+    step(std::integral_constant<int, 0x111>{});
+    step(std::integral_constant<int, 0x112>{});
+    step(std::integral_constant<int, 0x114>{});
+    step(std::integral_constant<int, 0x118>{});
+    step(std::integral_constant<int, 0x142>{});
+    step(std::integral_constant<int, 0x143>{});
+    return static_cast<I>(__builtin_amdgcn_readlane(static_cast<int>(v), kWave - 1));
+}
+__device__ __forceinline__ int64_t wave_max(int64_t v) {
+    const int32_t hi = wave_max_int<int32_t>(static_cast<int32_t>(v >> 32), INT32_MIN);
+    const uint32_t lo = wave_max_int<uint32_t>(static_cast<int32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u, 0u);
+    return (static_cast<int64_t>(hi) << 32) | lo;
+}
+// A double as an integer of the same order; NaN and -infinity are the least.
+constexpr int64_t kNone = INT64_MIN;
+__device__ __forceinline__ int64_t key_of(double v) {
+    const int64_t b = __builtin_bit_cast(int64_t, v);
+    return v > -__builtin_inf() ? b ^ (b >> 63 & INT64_MAX) : kNone;
+}
+__device__ __forceinline__ double value_of(int64_t k) {
+    return __builtin_bit_cast(double, k ^ (k >> 63 & INT64_MAX));
 }
 
-// Part blockIdx.z of the logits of 16 * TM * WM tokens (A rows) and
-// 16 * TN * WN experts (B columns). The four waves of a workgroup are WM x WN
-// tiles, and WK slices of the part's H, joined in LDS. Lane l loads row
-// l % 16, eight h from 8 * (l / 16) of each step.
-template <typename T, typename W, int TM, int TN, int WM, int WN, int WK>
-__global__ __launch_bounds__(kBlock) void logits_kernel(GateArgs a, int chunks_per_part) {
-    static_assert(WM * WN * WK * kWave == kBlock, "four waves");
-    constexpr bool FAST = kFast<T, W>;
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-    const int r = lane & 15, kq = lane >> 4;
-    const int wk = wave % WK, wn = wave / WK % WN, wm = wave / (WK * WN);
-    const int t0 = (blockIdx.y * WM + wm) * 16 * TM, e0 = (blockIdx.x * WN + wn) * 16 * TN;
-    // rows past the end read the last one; their results are not stored
-    const T *xr[TM];
-    const W *wr[TN];
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-        const int t = t0 + i * 16 + r;
-        xr[i] = static_cast<const T *>(a.x) + static_cast<size_t>(t < a.T ? t : a.T - 1) * a.H;
-    }
-#pragma unroll
-    for (int j = 0; j < TN; ++j) {
-        const int e = e0 + j * 16 + r;
-        wr[j] = static_cast<const W *>(a.weight) + static_cast<size_t>(e < a.E ? e : a.E - 1) * a.H;
-    }
+// Fragments of 32 h, in the two ways that the logits are summed: `sum` += in
+// fp64; fast(): FOLD steps are summed in fp32 first.
+template <typename T, typename W, int TM, int TN>
+struct Tiles {
     v4d sum[TM][TN];
-    v4f mag[TM][TN];
+    __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+        for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            sum[i][j] = v4d{0.0, 0.0, 0.0, 0.0};
-            mag[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-        }
-    const int c_end = min((static_cast<int>(blockIdx.z) + 1) * chunks_per_part, (a.H + kChunk - 1) / kChunk);
-    for (int c = blockIdx.z * chunks_per_part + wk; c < c_end; c += WK) {
-        if constexpr (FAST) {
-            v4i xf[TM][kChunk / kStep], wf[TN][kChunk / kStep];
+            for (int j = 0; j < TN; ++j) sum[i][j] = v4d{0.0, 0.0, 0.0, 0.0};
+    }
+    template <int FOLD>
+    __device__ __forceinline__ void fast(const v4i (&x)[FOLD][TM], const v4i (&w)[FOLD][TN]) {
+        v4f acc[TM][TN];
 #pragma unroll
-            for (int s = 0; s < kChunk / kStep; ++s) {
-                const int k = c * kChunk + s * kStep + kq * kVec;
-#pragma unroll
-                for (int i = 0; i < TM; ++i) {
-                    T raw[kVec];
-                    load8(xr[i], k, a.H, raw);
-                    __builtin_memcpy(&xf[i][s], raw, sizeof raw);
-                }
-#pragma unroll
-                for (int j = 0; j < TN; ++j) {
-                    W raw[kVec];
-                    load8(wr[j], k, a.H, raw);
-                    __builtin_memcpy(&wf[j][s], raw, sizeof raw);
-                }
-            }
-            v4f acc[TM][TN];
-#pragma unroll
-            for (int s = 0; s < kChunk / kStep; ++s)
-#pragma unroll
-                for (int i = 0; i < TM; ++i)
-#pragma unroll
-                    for (int j = 0; j < TN; ++j)
-                        acc[i][j] = mfma32<T>(xf[i][s], wf[j][s], s == 0 ? v4f{0.0f, 0.0f, 0.0f, 0.0f} : acc[i][j]);
-#pragma unroll
-            for (int s = 0; s < kChunk / kStep; ++s) {
-#pragma unroll
-                for (int i = 0; i < TM; ++i) xf[i][s] &= 0x7FFF7FFF;
-#pragma unroll
-                for (int j = 0; j < TN; ++j) wf[j][s] &= 0x7FFF7FFF;
-#pragma unroll
-                for (int i = 0; i < TM; ++i)
-#pragma unroll
-                    for (int j = 0; j < TN; ++j) mag[i][j] = mfma32<T>(xf[i][s], wf[j][s], mag[i][j]);
-            }
+        for (int s = 0; s < FOLD; ++s)
 #pragma unroll
             for (int i = 0; i < TM; ++i)
 #pragma unroll
                 for (int j = 0; j < TN; ++j)
+                    acc[i][j] = mfma32<T>(x[s][i], w[s][j], s == 0 ? v4f{0.0f, 0.0f, 0.0f, 0.0f} : acc[i][j]);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) sum[i][j][q] += static_cast<double>(acc[i][j][q]);
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) sum[i][j][q] += static_cast<double>(acc[i][j][q]);
+    }
+    // the MFMA takes four h, one per lane quarter: h = 8 kq + e for step e
+    __device__ __forceinline__ void full(const T (&x)[TM][kVec], const W (&w)[TN][kVec]) {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e)
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    sum[i][j] = __builtin_amdgcn_mfma_f64_16x16x4f64(static_cast<double>(to_f32(x[i][e])),
+                                                                     static_cast<double>(to_f32(w[j][e])), sum[i][j],
+                                                                     0, 0, 0);
+    }
+    // into part `part` of the workspace; token tiles from t0, expert tiles from e0
+    __device__ __forceinline__ void store(const GateArgs &a, int part, int t0, int e0, int lane) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    // result registers: fp32 D rows 4 * (l / 16) + q, fp64 D rows l / 16 + 4 * q
+                    const int t = t0 + i * 16 + (kFast<T, W> ? 4 * (lane >> 4) + q : (lane >> 4) + 4 * q);
+                    const int e = e0 + j * 16 + (lane & 15);
+                    if (t < a.T && e < a.E) {
+                        const size_t o = (static_cast<size_t>(part) * a.T + t) * a.E + e;
+                        a.logits[o] = sum[i][j][q];
+                    }
+                }
+    }
+};
+
+// Up to 16 tokens: workgroup (expert tile, part), its four waves take every
+// fourth chunk of the part. Lane l loads row l % 16, eight h from 8 * (l / 16)
+// of each step, straight from memory: there is too little of it for LDS to
+// pay. Every step is folded: that keeps the bound, and with it the share of
+// logits that are computed again, small.
+constexpr int kSlices = 4;
+template <typename T, typename W>
+__global__ __launch_bounds__(kBlock) void logits_few_kernel(GateArgs a, int chunks_per_part) {
+    static_assert(kSlices * kWave == kBlock, "one slice per wave");
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int r = lane & 15, kq = lane >> 4;
+    const int e0 = blockIdx.x * 16, part = blockIdx.y;
+    // rows past the end read the last one; their results are not stored
+    const T *x = static_cast<const T *>(a.x) + static_cast<size_t>(min(r, a.T - 1)) * a.H;
+    const W *w = static_cast<const W *>(a.weight) + static_cast<size_t>(min(e0 + r, a.E - 1)) * a.H;
+    Tiles<T, W, 1, 1> tile;
+    tile.clear();
+    float xn = 0.0f, wn = 0.0f;  // squares of the lane's elements
+    const int c_end = min((part + 1) * chunks_per_part, (a.H + kChunk - 1) / kChunk);
+    auto chunk = [&](auto whole, int c) {
+        T xv[kChunk / kStep][1][kVec];
+        W wv[kChunk / kStep][1][kVec];
+#pragma unroll
+        for (int s = 0; s < kChunk / kStep; ++s) {
+            const int k = c * kChunk + s * kStep + kq * kVec;
+            load8<decltype(whole)::value>(x, k, a.H, xv[s][0]);
+            load8<decltype(whole)::value>(w, k, a.H, wv[s][0]);
+        }
+#pragma unroll
+        for (int s = 0; s < kChunk / kStep; ++s) {
+            if constexpr (kFast<T, W>) {
+                v4i xf[1][1], wf[1][1];
+                __builtin_memcpy(&xf[0][0], xv[s][0], 16);
+                __builtin_memcpy(&wf[0][0], wv[s][0], 16);
+                add_squares<T>(xf[0][0], xn);
+                add_squares<T>(wf[0][0], wn);
+                tile.template fast<1>(xf, wf);
+            } else {
+                tile.full(xv[s], wv[s]);
+            }
+        }
+    };
+#pragma unroll 2
+    for (int c = part * chunks_per_part + wave; c < c_end; c += kSlices) {
+        if ((c + 1) * kChunk <= a.H) chunk(std::true_type{}, c);
+        else chunk(std::false_type{}, c);
+    }
+    __shared__ v4d s_sum[kSlices - 1][kWave];
+    __shared__ float s_xn[kSlices][kWave], s_wn[kSlices][kWave];
+    if (wave > 0) s_sum[wave - 1][lane] = tile.sum[0][0];
+    s_xn[wave][lane] = xn;
+    s_wn[wave][lane] = wn;
+    __syncthreads();
+    if (wave > 0) return;
+#pragma unroll
+    for (int i = 0; i < kSlices - 1; ++i) tile.sum[0][0] += s_sum[i][lane];
+    tile.store(a, part, 0, e0, lane);
+    if constexpr (kFast<T, W>) {
+        if (lane < 16) {  // row `lane` lies in lanes lane + 16 q of every wave
+            xn = wn = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kSlices; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    xn += s_xn[i][lane + 16 * q];
+                    wn += s_wn[i][lane + 16 * q];
+                }
+            if (blockIdx.x == 0 && lane < a.T) a.x_norms[part * a.T + lane] = xn;
+            if (e0 + lane < a.E) a.w_norms[part * a.E + e0 + lane] = wn;
+        }
+    }
+}
+
+// More tokens: workgroups of 64 tokens x 64 experts, a wave 32 x 32 of them.
+// Lanes that load MFMA fragments straight from rows touch 16 rows with 16
+// bytes each, four times the requests of whole lines, which is what bound such
+// a kernel (66 us at T 4096, E 256, H 4096); so 128 h of the 128 rows go
+// through LDS, the next ones on their way in registers meanwhile. 16-byte slot
+// c of a row lies at slot c ^ (row % 16): writes of a row and reads of 16
+// rows' fragments both meet every bank once.
+constexpr int kTileRows = 64;
+template <typename T>
+struct Stage {  // kTileRows rows of kChunk elements
+    static constexpr int kSlots = kChunk * sizeof(T) / 16;           // per row
+    static constexpr int kPer = kTileRows * kSlots / kBlock;         // per thread
+    static constexpr int kBytes = kTileRows * kSlots * 16;
+    static constexpr int kElems = 16 / sizeof(T);
+    v4i v[kPer];
+    const T *p[kPer];  // where the thread's slots of the next chunk lie
+    int k;             // and their element (the same for all of them)
+    static_assert(kBlock % kSlots == 0, "a thread's slots are one column");
+    // rows past the end read the last one
+    __device__ __forceinline__ void start(const T *base, int row0, int rows, int H, int c) {
+        k = c * kChunk + static_cast<int>(threadIdx.x) % kSlots * kElems;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int row = min(row0 + static_cast<int>(threadIdx.x + i * kBlock) / kSlots, rows - 1);
+            p[i] = base + static_cast<size_t>(row) * H + k;
+        }
+    }
+    template <bool WHOLE>
+    __device__ __forceinline__ void fetch(int H) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            if (WHOLE || k + kElems <= H) {
+                __builtin_memcpy(&v[i], p[i], 16);
+            } else {
+                T raw[kElems];
+#pragma unroll
+                for (int e = 0; e < kElems; ++e) {
+                    raw[e] = T{};
+                    if (k + e < H) raw[e] = p[i][e];
+                }
+                __builtin_memcpy(&v[i], raw, 16);
+            }
+            p[i] += kChunk;
+        }
+        k += kChunk;
+    }
+    __device__ __forceinline__ void put(char *lds) const {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int slot = threadIdx.x + i * kBlock, row = slot / kSlots, c = slot % kSlots;
+            *reinterpret_cast<v4i *>(lds + (row * kSlots + (c ^ (row & 15))) * 16) = v[i];
+        }
+    }
+    // eight elements of a row from element k (a multiple of 8)
+    static __device__ __forceinline__ void get(const char *lds, int row, int k, T (&out)[kVec]) {
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(kVec * sizeof(T) / 16); ++i) {
+            const int c = k / kElems + i;
+            __builtin_memcpy(&out[i * kElems], lds + (row * kSlots + (c ^ (row & 15))) * 16, 16);
+        }
+    }
+};
+
+// Steps that are summed in fp32 before the fp64 sum: 64 products. At T 4096,
+// E 256, H 4096 (logits, then choice): one step 37.5 + 19.0 us, two 31.2 +
+// 21.6, four 28.8 + 24.5 (a wider bound leaves more tokens open).
+constexpr int kFold = 2;
+
+template <typename T, typename W>
+__global__ __launch_bounds__(kBlock) void logits_many_kernel(GateArgs a, int chunks_per_part, int e_tiles, int units) {
+    __shared__ __attribute__((aligned(16))) char s_x[Stage<T>::kBytes], s_w[Stage<W>::kBytes];
+    // The expert tiles of one unit (token tile, part) read the same x: they
+    // get block numbers that are equal modulo 8, so that one XCD's L2 serves
+    // them all.
+    const int unit = static_cast<int>(blockIdx.x >> 3) / e_tiles * 8 + static_cast<int>(blockIdx.x & 7);
+    if (unit >= units) return;
+    const int t_tiles = (a.T + kTileRows - 1) / kTileRows;
+    const int t0 = unit % t_tiles * kTileRows, part = unit / t_tiles;
+    const int e0 = static_cast<int>(blockIdx.x >> 3) % e_tiles * kTileRows;
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const int r = lane & 15, kq = lane >> 4;
+    const int tm = (wave >> 1) * 32, en = (wave & 1) * 32;
+    Tiles<T, W, 2, 2> tile;
+    tile.clear();
+    Stage<T> sx;
+    Stage<W> sw;
+    auto fetch = [&](int c) {
+        if ((c + 1) * kChunk <= a.H) {
+            sx.template fetch<true>(a.H);
+            sw.template fetch<true>(a.H);
+        } else {
+            sx.template fetch<false>(a.H);
+            sw.template fetch<false>(a.H);
+        }
+    };
+    float xn[Stage<T>::kPer] = {}, wn[Stage<W>::kPer] = {};  // squares of the thread's slots
+    const int c0 = part * chunks_per_part, c_end = min(c0 + chunks_per_part, (a.H + kChunk - 1) / kChunk);
+    sx.start(static_cast<const T *>(a.x), t0, a.T, a.H, c0);
+    sw.start(static_cast<const W *>(a.weight), e0, a.E, a.H, c0);
+    fetch(c0);  // a part has at least one chunk
+    for (int c = c0; c < c_end; ++c) {
+        __syncthreads();
+        sx.put(s_x);
+        sw.put(s_w);
+        if constexpr (kFast<T, W>) {
+#pragma unroll
+            for (int i = 0; i < Stage<T>::kPer; ++i) {
+                add_squares<T>(sx.v[i], xn[i]);
+                add_squares<T>(sw.v[i], wn[i]);
+            }
+        }
+        __syncthreads();
+        if (c + 1 < c_end) fetch(c + 1);
+        if constexpr (kFast<T, W>) {
+#pragma unroll
+            for (int s = 0; s < kChunk / kStep; s += kFold) {
+                v4i xf[kFold][2], wf[kFold][2];
+#pragma unroll
+                for (int f = 0; f < kFold; ++f) {
+                    const int k = (s + f) * kStep + kq * kVec;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        T xv[kVec];
+                        W wv[kVec];
+                        Stage<T>::get(s_x, tm + i * 16 + r, k, xv);
+                        Stage<W>::get(s_w, en + i * 16 + r, k, wv);
+                        __builtin_memcpy(&xf[f][i], xv, 16);
+                        __builtin_memcpy(&wf[f][i], wv, 16);
+                    }
+                }
+                tile.template fast<kFold>(xf, wf);
+            }
         } else {
 #pragma unroll
             for (int s = 0; s < kChunk / kStep; ++s) {
-                const int k = c * kChunk + s * kStep + kq * kVec;
-                T xv[TM][kVec];
-                W wv[TN][kVec];
+                T xv[2][kVec];
+                W wv[2][kVec];
 #pragma unroll
-                for (int i = 0; i < TM; ++i) load8(xr[i], k, a.H, xv[i]);
-#pragma unroll
-                for (int j = 0; j < TN; ++j) load8(wr[j], k, a.H, wv[j]);
-                // the MFMA takes four h, one per lane quarter: h = 8 kq + e for step e
-#pragma unroll
-                for (int e = 0; e < kVec; ++e)
-#pragma unroll
-                    for (int i = 0; i < TM; ++i)
-#pragma unroll
-                        for (int j = 0; j < TN; ++j)
-                            sum[i][j] = __builtin_amdgcn_mfma_f64_16x16x4f64(
-                                static_cast<double>(to_f32(xv[i][e])), static_cast<double>(to_f32(wv[j][e])),
-                                sum[i][j], 0, 0, 0);
-            }
-        }
-    }
-    if constexpr (WK > 1) {
-        __shared__ v4d s_sum[WK - 1][kWave];
-        __shared__ v4f s_mag[WK - 1][kWave];
-        static_assert(WM * WN * TM * TN == 1, "one tile per wave");
-        if (wk > 0) {
-            s_sum[wk - 1][lane] = sum[0][0];
-            s_mag[wk - 1][lane] = mag[0][0];
-        }
-        __syncthreads();
-        if (wk > 0) return;
-#pragma unroll
-        for (int w = 0; w < WK - 1; ++w) {
-            sum[0][0] += s_sum[w][lane];
-            mag[0][0] += s_mag[w][lane];
-        }
-    }
-    const size_t part = static_cast<size_t>(blockIdx.z) * a.T * a.E;
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                // result registers: fp32 D rows 4 * (l / 16) + q, fp64 D rows l / 16 + 4 * q
-                const int t = t0 + i * 16 + (FAST ? 4 * kq + q : kq + 4 * q), e = e0 + j * 16 + r;
-                if (t < a.T && e < a.E) {
-                    const size_t o = part + static_cast<size_t>(t) * a.E + e;
-                    a.logits[o] = sum[i][j][q];
-                    if (FAST) a.mags[o] = mag[i][j][q];
+                for (int i = 0; i < 2; ++i) {
+                    Stage<T>::get(s_x, tm + i * 16 + r, s * kStep + kq * kVec, xv[i]);
+                    Stage<W>::get(s_w, en + i * 16 + r, s * kStep + kq * kVec, wv[i]);
                 }
+                tile.full(xv, wv);
             }
+        }
+    }
+    tile.store(a, part, t0 + tm, e0 + en, lane);
+    if constexpr (kFast<T, W>) {  // a row's slots lie in 16 neighbouring lanes
+        static_assert(Stage<T>::kSlots == 16, "one row per 16 lanes");
+#pragma unroll
+        for (int i = 0; i < Stage<T>::kPer; ++i) {
+#pragma unroll
+            for (int d = 8; d > 0; d >>= 1) {
+                xn[i] += __shfl_xor(xn[i], d, kWave);
+                wn[i] += __shfl_xor(wn[i], d, kWave);
+            }
+            const int row = static_cast<int>(threadIdx.x + i * kBlock) / 16;
+            if (r == 0 && e0 == 0 && t0 + row < a.T) a.x_norms[part * a.T + t0 + row] = xn[i];
+            if (r == 0 && t0 == 0 && e0 + row < a.E) a.w_norms[part * a.E + e0 + row] = wn[i];
+        }
+    }
 }
 
-// The logit of expert e in fp64, by the whole wave.
+// The logits of experts e0 and e1 in fp64, by the whole wave: two at a time,
+// since a doubt is between two as a rule, and both rows' loads overlap.
 template <typename T, typename W>
-__device__ double exact_logit(const GateArgs &a, int t, int e, int lane) {
+__device__ __forceinline__ void exact_logits(const GateArgs &a, int t, int e0, int e1, int lane, double &l0, double &l1) {
     const T *x = static_cast<const T *>(a.x) + static_cast<size_t>(t) * a.H;
-    const W *w = static_cast<const W *>(a.weight) + static_cast<size_t>(e) * a.H;
-    double sum = 0.0;
-    for (int i = lane * kVec; i < a.H; i += kWave * kVec) {
-        T u[kVec];
-        W v[kVec];
-        load8(x, i, a.H, u);
-        load8(w, i, a.H, v);
+    const W *w0 = static_cast<const W *>(a.weight) + static_cast<size_t>(e0) * a.H;
+    const W *w1 = static_cast<const W *>(a.weight) + static_cast<size_t>(e1) * a.H;
+    double s0 = 0.0, s1 = 0.0;
+    constexpr int kBatch = 2;  // loads in flight, written out: a loop that adds as it loads waits for each
+    auto add = [&](auto whole, int i) {
+        T u[kBatch][kVec];
+        W v0[kBatch][kVec], v1[kBatch][kVec];
 #pragma unroll
-        for (int j = 0; j < kVec; ++j)
-            sum = fma(static_cast<double>(to_f32(u[j])), static_cast<double>(to_f32(v[j])), sum);
-    }
-    return wave_sum(sum);
+        for (int b = 0; b < kBatch; ++b) {
+            const int k = i + (b * kWave + lane) * kVec;
+            load8<decltype(whole)::value>(x, k, a.H, u[b]);
+            load8<decltype(whole)::value>(w0, k, a.H, v0[b]);
+            load8<decltype(whole)::value>(w1, k, a.H, v1[b]);
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                const double xv = static_cast<double>(to_f32(u[b][j]));
+                s0 = fma(xv, static_cast<double>(to_f32(v0[b][j])), s0);
+                s1 = fma(xv, static_cast<double>(to_f32(v1[b][j])), s1);
+            }
+    };
+    int i0 = 0;
+    for (; i0 + kBatch * kWave * kVec <= a.H; i0 += kBatch * kWave * kVec) add(std::true_type{}, i0);
+    if (i0 < a.H) add(std::false_type{}, i0);
+    l0 = wave_sum(s0);
+    l1 = wave_sum(s1);
 }
 
 // Score of a logit (softmax: before the division by the sum; m = the largest
 // logit).
-__device__ __forceinline__ double score_of(int score, double l, double m) {
-    if (score == MOE_SCORE_SOFTMAX) return exp(l - m);
-    if (score == MOE_SCORE_SIGMOID) return 1.0 / (1.0 + exp(-l));
+template <int SCORE>
+__device__ __forceinline__ double score_of(double l, double m) {
+    if constexpr (SCORE == MOE_SCORE_SOFTMAX) return exp(l - m);
+    if constexpr (SCORE == MOE_SCORE_SIGMOID) return 1.0 / (1.0 + exp(-l));
     return sqrt(fmax(l, 0.0) + log1p(exp(-fabs(l))));
 }
 
-// Largest value of the wave and its lowest expert (0x7FFFFFFF: all -infinity).
-template <int NPL>
-__device__ __forceinline__ void wave_best(const double (&c)[NPL], int lane, double &best, int &best_e) {
-    best = -__builtin_inf();
-    best_e = 0x7FFFFFFF;
-#pragma unroll
-    for (int j = 0; j < NPL; ++j) {
-        if (c[j] > best) {
-            best = c[j];
-            best_e = j * kWave + lane;
-        }
-    }
-#pragma unroll
-    for (int d = kWave / 2; d > 0; d >>= 1) {
-        const double oc = __shfl_xor(best, d, kWave);
-        const int oe = __shfl_xor(best_e, d, kWave);
-        if (oc > best || (oc == best && oe < best_e)) {
-            best = oc;
-            best_e = oe;
-        }
-    }
-}
-
 // One wave per token; lane l holds experts l, l + 64, ... (NPL of them).
-template <typename T, typename W, int NPL>
-__global__ __launch_bounds__(kBlock) void choose_kernel(GateArgs a, int parts) {
-    constexpr bool FAST = kFast<T, W>;
+// F: the type of x and weight where the logits are bounded fp32 sums, void
+// where they are 64-bit sums.
+//
+// K choices in order. With F, an expert that lies closer than `off` below a
+// choice is marked, and so is that choice; the marked ones' logits are then
+// computed in fp64 and the choice is made again. An unmarked expert is further
+// than `off` from all that it was compared with, so its place stands.
+//
+// A token is a chain of reductions, and few tokens are a single wave's
+// latency, most of it instruction fetches of a kernel that runs once: scores
+// are a template parameter and the second choice shares the first one's code
+// (13 -> 8 us at 8 tokens, 256 experts).
+template <typename F, int SCORE, int NPL>
+__global__ __launch_bounds__(kBlock) void choose_kernel(GateArgs a, int parts, double gamma) {
+    constexpr bool FAST = !__is_same(F, void);
     const int lane = threadIdx.x & (kWave - 1);
     const int t = blockIdx.x * (kBlock / kWave) + threadIdx.x / kWave;
     if (t >= a.T) return;
-    const double none = -__builtin_inf();
-    double l[NPL], s[NPL], c[NPL];  // logits, scores, and what the choice goes by
-    float mag = 0.0f;               // largest sum of |x * w|
+    double l[NPL];  // logits
+    float n[NPL];   // squares of the experts' rows
+    float xn = 0.0f;
+    float bias[NPL];
+    // Loads without branches between them: lanes past the end read the last
+    // expert, and without a bias the workspace's first words are read instead.
+    const float *bp = a.bias ? a.bias : reinterpret_cast<const float *>(a.logits);
+    const size_t row = static_cast<size_t>(t) * a.E, stride = static_cast<size_t>(a.T) * a.E;
+    constexpr int kBatch = NPL > 4 ? 1 : 4;  // parts in flight
 #pragma unroll
     for (int j = 0; j < NPL; ++j) {
-        const int e = j * kWave + lane;
-        double v = 0.0;
-        float b = 0.0f;
-        if (e < a.E) {
-            for (int p = 0; p < parts; ++p) {
-                const size_t o = (static_cast<size_t>(p) * a.T + t) * a.E + e;
-                v += a.logits[o];
-                if (FAST) b += a.mags[o];
+        l[j] = 0.0;
+        n[j] = 0.0f;
+        bias[j] = bp[min(j * kWave + lane, a.E - 1)];
+    }
+    for (int p = 0; p < parts; p += kBatch) {
+        double lv[kBatch][NPL];
+        float nv[kBatch][NPL], xv[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int q = min(p + b, parts - 1);  // past the last part: read it again, add nothing
+            const size_t o = q * stride + row;
+            if (FAST) xv[b] = a.x_norms[q * a.T + t];
+#pragma unroll
+            for (int j = 0; j < NPL; ++j) {
+                const int e = min(j * kWave + lane, a.E - 1);
+                lv[b][j] = a.logits[o + e];
+                if (FAST) nv[b][j] = a.w_norms[q * a.E + e];
             }
         }
-        l[j] = e < a.E ? v : none;
-        mag = fmaxf(mag, b);
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            if (p + b >= parts) continue;
+            if (FAST) xn += xv[b];
+#pragma unroll
+            for (int j = 0; j < NPL; ++j) {
+                l[j] += lv[b][j];
+                if (FAST) n[j] += nv[b][j];
+            }
+        }
     }
-    // choice values of every expert, from the logits
-    auto values = [&] {
-        double m = none, total = 0.0;
-        if (a.score == MOE_SCORE_SOFTMAX) {
-#pragma unroll
-            for (int j = 0; j < NPL; ++j) m = fmax(m, l[j]);
-            m = wave_max(m);
-        }
-#pragma unroll
-        for (int j = 0; j < NPL; ++j) {
-            s[j] = j * kWave + lane < a.E ? score_of(a.score, l[j], m) : 0.0;
-            total += s[j];
-        }
-        if (a.score == MOE_SCORE_SOFTMAX) {
-            total = wave_sum(total);
-#pragma unroll
-            for (int j = 0; j < NPL; ++j) s[j] = s[j] / total;
-        }
-#pragma unroll
-        for (int j = 0; j < NPL; ++j) {
-            const int e = j * kWave + lane;
-            c[j] = a.bias && e < a.E ? s[j] + static_cast<double>(a.bias[e]) : l[j];
-            if (e >= a.E || !(c[j] > none)) c[j] = none;  // NaN is never chosen
-        }
-    };
-    values();
+    // How far two choice values may be off together. Slopes: sigmoid 1/4,
+    // sqrt(softplus) under 1/3; a softmax share moves by at most twice its
+    // logits' error.
+    double off = 0.0;
     if constexpr (FAST) {
-        // How far two choice values may be off together. Slopes: sigmoid 1/4,
-        // sqrt(softplus) under 1/3; a softmax share moves by at most twice its
-        // logits' error.
-        double off = 2.0 * (kGamma * 1.01 * wave_max(static_cast<double>(mag)) + kTiny);
-        if (a.bias) off *= a.score == MOE_SCORE_SOFTMAX ? 2.5 : a.score == MOE_SCORE_SIGMOID ? 0.25 : 0.34;
+        float wn = 0.0f;  // squares order like their bits; a NaN is the largest, and marks all
+#pragma unroll
+        for (int j = 0; j < NPL; ++j) wn = n[j] <= wn ? wn : n[j];
+        wn = __uint_as_float(wave_max_int<uint32_t>(__float_as_uint(wn), 0u));
+        off = 2.0 * (gamma * 1.01 * sqrt(static_cast<double>(xn) * static_cast<double>(wn)) + kTiny);
+        if (a.bias) off *= SCORE == MOE_SCORE_SOFTMAX ? 2.5 : SCORE == MOE_SCORE_SIGMOID ? 0.25 : 0.34;
         off += 1e-13;
-        // K + 1 choices in order; an expert that is closer than `off` to one of
-        // them is marked, and so is that one
-        double left[NPL];
-        uint32_t marked = 0;  // bit j: expert j * 64 + lane
-#pragma unroll
-        for (int j = 0; j < NPL; ++j) left[j] = c[j];
-        for (int k = 0; k < a.K; ++k) {
-            double best;
-            int best_e;
-            wave_best(left, lane, best, best_e);
-            if (!(best > none)) break;
-            bool close = false;
-#pragma unroll
-            for (int j = 0; j < NPL; ++j) {
-                if (j * kWave + lane == best_e) {
-                    left[j] = none;
-                } else if (left[j] > best - off) {
-                    marked |= 1u << j;
-                    close = true;
-                }
-            }
-            if (__ballot(close)) {
-#pragma unroll
-                for (int j = 0; j < NPL; ++j)
-                    if (j * kWave + lane == best_e) marked |= 1u << j;
-            }
-        }
-        if (__ballot(marked != 0)) {
-#pragma unroll
-            for (int j = 0; j < NPL; ++j) {
-                unsigned long long todo = __ballot((marked >> j) & 1u);
-                while (todo) {
-                    const int who = __builtin_ctzll(todo);
-                    todo &= todo - 1;
-                    const double v = exact_logit<T, W>(a, t, j * kWave + who, lane);
-                    if (lane == who) l[j] = v;
-                }
-            }
-            values();
-        }
     }
-    double w_mine = 0.0, w_sum = 0.0;  // lane k keeps the k-th choice
-    int id_mine = -1;
-    for (int k = 0; k < a.K; ++k) {
-        double best;
-        int best_e;
-        wave_best(c, lane, best, best_e);
-        if (!(best > none)) break;  // uniform: nothing is left
-        double v = 0.0;
+    double s[NPL], total;  // scores (softmax: undivided, `total` their sum)
+    int id_mine;           // lane k keeps the k-th choice
+    for (bool again = false;; again = true) {
+        double top = 0.0;
+        total = 1.0;
+        if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
+            int64_t k = kNone;
+#pragma unroll
+            for (int j = 0; j < NPL; ++j) {
+                if (j * kWave + lane >= a.E) l[j] = -__builtin_inf();
+                k = max(k, key_of(l[j]));
+            }
+            top = value_of(wave_max(k));
+            total = 0.0;
+        }
+        int64_t c[NPL];  // what the choice goes by
 #pragma unroll
         for (int j = 0; j < NPL; ++j) {
-            if (best_e / kWave == j) v = s[j];
-            if (j * kWave + lane == best_e) c[j] = none;
+            s[j] = score_of<SCORE>(l[j], top);
+            if (SCORE == MOE_SCORE_SOFTMAX) total += s[j];
         }
-        v = __shfl(v, best_e & (kWave - 1), kWave);
-        w_sum += v;
-        if (lane == k) {
-            w_mine = v;
-            id_mine = best_e;
+        if (SCORE == MOE_SCORE_SOFTMAX) total = wave_sum(total);
+#pragma unroll
+        for (int j = 0; j < NPL; ++j) {
+            double v = l[j];
+            if (a.bias) v = (SCORE == MOE_SCORE_SOFTMAX ? s[j] / total : s[j]) + static_cast<double>(bias[j]);
+            c[j] = j * kWave + lane < a.E ? key_of(v) : kNone;
         }
+        id_mine = -1;
+        int64_t c_mine = kNone;
+        for (int k = 0; k < a.K; ++k) {
+            int64_t best = c[0];
+#pragma unroll
+            for (int j = 1; j < NPL; ++j) best = max(best, c[j]);
+            best = wave_max(best);
+            if (best == kNone) break;  // nothing is left
+            int id = 0;                // its lowest expert
+#pragma unroll
+            for (int j = NPL - 1; j >= 0; --j) {
+                const unsigned long long equal = __ballot(c[j] == best);
+                if (equal) id = j * kWave + __builtin_ctzll(equal);
+            }
+#pragma unroll
+            for (int j = 0; j < NPL; ++j)
+                if (j * kWave + lane == id) c[j] = kNone;
+            if (lane == k) {
+                c_mine = best;
+                id_mine = id;
+            }
+        }
+        if constexpr (!FAST) {
+            break;
+        } else {
+            if (again) break;
+            // neighbours in the order that are closer than `off`: lane k
+            // against lane k + 1, the last choice against all that are left
+            const double mine = value_of(c_mine);
+            const bool chosen = id_mine >= 0;
+            const int count = __popcll(__ballot(chosen));
+            if (count == 0) break;
+            const double next = value_of(__shfl_down(c_mine, 1, kWave));
+            const double last = value_of(__shfl(c_mine, count - 1, kWave));
+            uint32_t marked = 0;  // bit j: expert j * 64 + lane
+#pragma unroll
+            for (int j = 0; j < NPL; ++j)
+                if (c[j] != kNone && !(last - value_of(c[j]) > off)) marked |= 1u << j;
+            const unsigned long long left = __ballot(marked != 0);
+            const unsigned long long near =
+                __ballot(chosen && lane + 1 < count && !(mine - next > off)) | (left ? 1ull << (count - 1) : 0);
+            if (!near) break;
+            unsigned long long todo = near | near << 1;  // both of a pair
+            if (count < kWave) todo &= (1ull << count) - 1;
+            while (todo) {
+                const int id = __builtin_amdgcn_readlane(id_mine, __builtin_ctzll(todo));
+                todo &= todo - 1;
+                if (lane == (id & (kWave - 1))) marked |= 1u << (id / kWave);
+            }
+            for (;;) {
+                int e[2] = {-1, -1};  // the next two marked experts
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const unsigned long long some = __ballot(marked != 0);
+                    if (!some) continue;  // uniform
+                    const int lo = __builtin_ctzll(some);
+                    const int j = __builtin_ctz(__builtin_amdgcn_readlane(marked, lo));
+                    e[i] = j * kWave + lo;
+                    if (lane == lo) marked &= ~(1u << j);
+                }
+                if (e[0] < 0) break;
+                double v[2];
+                exact_logits<F, F>(a, t, e[0], e[1] < 0 ? e[0] : e[1], lane, v[0], v[1]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < NPL; ++j)
+                        if (j * kWave + lane == e[i]) l[j] = v[i];
+            }
+        }
+    }
+    double w = 0.0;  // the score of lane k's choice
+#pragma unroll
+    for (int j = 0; j < NPL; ++j) {
+        const double v = __shfl(s[j], id_mine & (kWave - 1), kWave);
+        if (id_mine >= 0 && id_mine / kWave == j) w = v;
+    }
+    if (a.normalize) {
+        double sum = w;
+#pragma unroll
+        for (int d = kMaxTopK / 2; d > 0; d >>= 1) sum += __shfl_xor(sum, d, kWave);
+        if (sum > 0.0) w = w / sum;
+    } else if (SCORE == MOE_SCORE_SOFTMAX) {
+        w = w / total;
     }
     if (lane < a.K) {
-        double w = w_mine;
-        if (a.normalize && w_sum > 0.0) w = w / w_sum;
-        w = w * static_cast<double>(a.route_scale);
         const size_t o = static_cast<size_t>(t) * a.K + lane;
         a.ids[o] = id_mine;
-        a.scales[o] = id_mine < 0 ? 0.0f : static_cast<float>(w);
+        a.scales[o] = id_mine < 0 ? 0.0f : static_cast<float>(w * static_cast<double>(a.route_scale));
     }
 }
 
-// Parts of H: enough workgroups to give every CU one, of at least two chunks
-// per wave slice each.
+template <typename F, int SCORE>
+void choose_score(const GateArgs &a, int parts, double gamma, hipStream_t s) {
+    const dim3 grid((a.T + kBlock / kWave - 1) / (kBlock / kWave)), blk(kBlock);
+    if (a.E <= kWave) hipLaunchKernelGGL((choose_kernel<F, SCORE, 1>), grid, blk, 0, s, a, parts, gamma);
+    else if (a.E <= 2 * kWave) hipLaunchKernelGGL((choose_kernel<F, SCORE, 2>), grid, blk, 0, s, a, parts, gamma);
+    else if (a.E <= 4 * kWave) hipLaunchKernelGGL((choose_kernel<F, SCORE, 4>), grid, blk, 0, s, a, parts, gamma);
+    else hipLaunchKernelGGL((choose_kernel<F, SCORE, 16>), grid, blk, 0, s, a, parts, gamma);
+}
+template <typename F>
+void choose(const GateArgs &a, int parts, double gamma, hipStream_t s) {
+    if (a.score == MOE_SCORE_SOFTMAX) choose_score<F, MOE_SCORE_SOFTMAX>(a, parts, gamma, s);
+    else if (a.score == MOE_SCORE_SIGMOID) choose_score<F, MOE_SCORE_SIGMOID>(a, parts, gamma, s);
+    else choose_score<F, MOE_SCORE_SQRT_SOFTPLUS>(a, parts, gamma, s);
+}
+
+// Parts of H: two workgroups per CU where that takes no more than kMaxSplit
+// parts (T 4096: 31 us, one workgroup per CU 38 us), of at least two chunks per
+// wave (few tokens) or workgroup.
 struct Plan {
-    int small;  // up to 16 tokens: one 16 x 16 tile per workgroup, its waves split H
-    dim3 grid;
-    int chunks_per_part, parts;
+    bool few;
+    int t_tiles, e_tiles, parts, chunks_per_part;
 };
 Plan plan_of(int T, int E, int H) {
     Plan p;
-    p.small = T <= 16;
-    const int tile = p.small ? 16 : 64, slices = p.small ? 4 : 1;
-    p.grid = dim3((E + tile - 1) / tile, (T + tile - 1) / tile);
-    const int chunks = (H + kChunk - 1) / kChunk;
-    const int blocks = static_cast<int>(p.grid.x * p.grid.y);
-    int parts = (256 + blocks - 1) / blocks;
-    if (parts > kMaxSplit) parts = kMaxSplit;
-    if (parts > chunks / (2 * slices)) parts = chunks / (2 * slices);
-    if (parts < 1) parts = 1;
+    p.few = T <= 16;
+    const int rows = p.few ? 16 : kTileRows, chunks = (H + kChunk - 1) / kChunk;
+    p.t_tiles = (T + rows - 1) / rows;
+    p.e_tiles = (E + rows - 1) / rows;
+    int parts = (512 + p.t_tiles * p.e_tiles - 1) / (p.t_tiles * p.e_tiles);
+    parts = min(min(parts, kMaxSplit), chunks / (p.few ? 2 * kSlices : 2));
+    parts = max(parts, 1);
     p.chunks_per_part = (chunks + parts - 1) / parts;
     p.parts = (chunks + p.chunks_per_part - 1) / p.chunks_per_part;
-    p.grid.z = p.parts;
     return p;
 }
 
@@ -426,17 +708,21 @@ template <typename T, typename W>
 hipError_t launch(const GateArgs &a, hipStream_t s) {
     const Plan p = plan_of(a.T, a.E, a.H);
     GateArgs g = a;
-    g.mags = reinterpret_cast<float *>(a.logits + static_cast<size_t>(p.parts) * a.T * a.E);
-    if (p.small)
-        hipLaunchKernelGGL((logits_kernel<T, W, 1, 1, 1, 1, 4>), p.grid, dim3(kBlock), 0, s, g, p.chunks_per_part);
-    else
-        hipLaunchKernelGGL((logits_kernel<T, W, 2, 2, 2, 2, 1>), p.grid, dim3(kBlock), 0, s, g, p.chunks_per_part);
+    g.x_norms = reinterpret_cast<float *>(a.logits + static_cast<size_t>(p.parts) * a.T * a.E);
+    g.w_norms = g.x_norms + static_cast<size_t>(p.parts) * a.T;
+    if (p.few) {
+        hipLaunchKernelGGL((logits_few_kernel<T, W>), dim3(p.e_tiles, p.parts), dim3(kBlock), 0, s, g,
+                           p.chunks_per_part);
+    } else {
+        const int units = p.t_tiles * p.parts;
+        hipLaunchKernelGGL((logits_many_kernel<T, W>), dim3((units + 7) / 8 * 8 * p.e_tiles), dim3(kBlock), 0, s, g,
+                           p.chunks_per_part, p.e_tiles, units);
+    }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const dim3 grid((a.T + kBlock / kWave - 1) / (kBlock / kWave)), blk(kBlock);
-    if (a.E <= kWave) hipLaunchKernelGGL((choose_kernel<T, W, 1>), grid, blk, 0, s, g, p.parts);
-    else if (a.E <= 4 * kWave) hipLaunchKernelGGL((choose_kernel<T, W, 4>), grid, blk, 0, s, g, p.parts);
-    else hipLaunchKernelGGL((choose_kernel<T, W, 16>), grid, blk, 0, s, g, p.parts);
+    const double gamma = kStep * (p.few ? 1 : kFold) * kUnit;
+    if constexpr (kFast<T, W>) choose<T>(g, p.parts, gamma, s);
+    else choose<void>(g, p.parts, gamma, s);
     return hipGetLastError();
 }
 
@@ -444,7 +730,8 @@ hipError_t launch(const GateArgs &a, hipStream_t s) {
 
 size_t gate_workspace(int T, int E, int H) {
     if (T == 0) return 0;
-    return static_cast<size_t>(plan_of(T, E, H).parts) * T * E * (sizeof(double) + sizeof(float));
+    return static_cast<size_t>(plan_of(T, E, H).parts) *
+           (static_cast<size_t>(T) * E * sizeof(double) + (static_cast<size_t>(T) + E) * sizeof(float));
 }
 
 hipError_t launch_gate(const GateArgs &a, hipStream_t s) {

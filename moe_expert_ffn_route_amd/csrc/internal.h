@@ -236,7 +236,7 @@ struct GateArgs {
     int32_t *ids;
     float *scales;
     double *logits;  // workspace: [parts, T, E]
-    float *mags;     // workspace behind them: sums of |x * w|, [parts, T, E]
+    float *x_norms, *w_norms;  // workspace behind them: squares of the rows, [parts, T] and [parts, E]
     int T, H, E, K, score, normalize, dtype, weight_dtype;
     float route_scale;
 };

@@ -124,7 +124,23 @@ def test_close_logits_are_told_apart(T, bias, dt, score):
     l = x.double() @ w.double().t()
     gaps = torch.sort(l, dim=1)[0].diff(dim=1)
     assert float(gaps.min()) < 1e-6 and float(gaps.min()) > 0  # close, and no ties
-    check(run(x, w, b, 9, score), formula(x, w, b, 9, score, True, 1.0), x, w)
+    ids, sc = run(x, w, b, 9, score)
+    want, v = formula(x, w, b, 9, score, True, 1.0)
+    # A softmax share of 1e-18 beside a bias of 0.05 is under the bias' last
+    # bit: there the 64-bit sums themselves, off by 2048 * 2^-53 of the
+    # magnitudes in a logit (relative to the share) and by 4 * 2^-53 of the
+    # value, leave the order open. Everywhere else ids are equal.
+    mag = (x.double().abs() @ w.double().abs().t()).amax(1, keepdim=True)
+    s64 = {SOFTMAX: lambda: torch.softmax(l, 1), SIGMOID: lambda: torch.sigmoid(l),
+           SQRTSP: lambda: (torch.clamp(l, min=0) + torch.log1p(torch.exp(-l.abs()))).sqrt()}[score]()
+    c = l if b is None else s64 + b.double()
+    slope = 1.0 if b is None else 2 * s64.gather(1, want) if score == SOFTMAX else 0.34
+    open_ = 2 * 2.0 ** -53 * (2048 * mag * slope + 4 * c.gather(1, want).abs())
+    same = ids.long() == want
+    assert bool((same | ((c.gather(1, ids.long()) - c.gather(1, want)).abs() <= open_)).all())
+    if b is None:
+        assert bool(same.all())
+    check((want.int(), sc), (want, v), x, w)
 
 
 def test_choice_between_values_that_fp32_sums_cannot_tell_apart():
