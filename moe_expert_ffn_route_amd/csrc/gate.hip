@@ -85,14 +85,16 @@ __device__ __forceinline__ void add_squares(v4i v, float &n) {
         typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const v2bf p = __builtin_bit_cast(v2bf, v[i]);
+            const int e = v[i];  // a vector's element has no address to cast from
+            const v2bf p = __builtin_bit_cast(v2bf, e);
             n = __builtin_amdgcn_fdot2_f32_bf16(p, p, n, false);
         }
     } else {
         typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const v2h p = __builtin_bit_cast(v2h, v[i]);
+            const int e = v[i];
+            const v2h p = __builtin_bit_cast(v2h, e);
             n = __builtin_amdgcn_fdot2(p, p, n, false);
         }
     }

@@ -106,31 +106,35 @@ def test_ties_go_to_the_lowest_id(T):
 
 
 @pytest.mark.parametrize("T", [5, 200])
+@pytest.mark.parametrize("keep", [None, 0, 3, 7], ids=lambda k: "all" if k is None else f"element{k}")
 @pytest.mark.parametrize("bias", [False, True], ids=["logit", "bias"])
 @pytest.mark.parametrize("dt", [BF, FP], ids=["bf16", "fp16"])
 @pytest.mark.parametrize("score", [SOFTMAX, SIGMOID, SQRTSP])
-def test_close_logits_are_told_apart(T, bias, dt, score):
+def test_close_logits_are_told_apart(T, bias, dt, score, keep):
     """Experts in pairs and triples whose rows differ in one last bit of one
-    element: logits that fp32 sums cannot order."""
+    element: logits that fp32 sums cannot order. `keep`: only that one of every
+    eight elements of x is not zero, so that a bound that misses it is zero."""
     x, w, b = make(T, 2048, 96, dt, dt, bias=bias, seed=17)
+    if keep is not None:
+        x = torch.where(torch.arange(2048) % 8 == keep, 3 * x.float(), torch.zeros(1)).to(dt)
     step = 2.0 ** -8 if dt == BF else 2.0 ** -11
     for e in range(0, 96, 3):
         w[e + 1], w[e + 2] = w[e], w[e]
-        k = 7 * e + 5
+        k = 7 * e + 5 if keep is None else 8 * e + keep
         w[e + 1, k], w[e + 2, k] = w[e, k] * (1 + 2 * step), w[e, k] * (1 - 4 * step)
         if bias:
             b[e + 1] = b[e + 2] = b[e]
     w[:, 1000:] *= 16  # sums whose terms dwarf the difference
     l = x.double() @ w.double().t()
     gaps = torch.sort(l, dim=1)[0].diff(dim=1)
-    assert float(gaps.min()) < 1e-6 and float(gaps.min()) > 0  # close, and no ties
+    mag = (x.double().abs() @ w.double().abs().t()).amax(1, keepdim=True)
+    assert float(gaps.min()) < 2.0 ** -23 * float(mag.max()) and float(gaps.min()) > 0  # under fp32's last bit; no ties
     ids, sc = run(x, w, b, 9, score)
     want, v = formula(x, w, b, 9, score, True, 1.0)
     # A softmax share of 1e-18 beside a bias of 0.05 is under the bias' last
     # bit: there the 64-bit sums themselves, off by 2048 * 2^-53 of the
     # magnitudes in a logit (relative to the share) and by 4 * 2^-53 of the
     # value, leave the order open. Everywhere else ids are equal.
-    mag = (x.double().abs() @ w.double().abs().t()).amax(1, keepdim=True)
     s64 = {SOFTMAX: lambda: torch.softmax(l, 1), SIGMOID: lambda: torch.sigmoid(l),
            SQRTSP: lambda: (torch.clamp(l, min=0) + torch.log1p(torch.exp(-l.abs()))).sqrt()}[score]()
     c = l if b is None else s64 + b.double()

@@ -99,7 +99,10 @@ def check(c, G, gated, out, tokens=None):
 SHAPES = [(1, 1, 32, 32), (1, 16, 128, 128), (2, 17, 64, 64), (3, 33, 96, 32), (1, 4096, 4096, 128), (5, 100, 320, 64),
           (16, 256, 1152, 128), (17, 48, 2048, 64), (31, 130, 544, 32), (33, 200, 4256, 32), (64, 64, 1024, 128),
           (65, 1000, 512, 64), (128, 96, 256, 32), (130, 520, 1408, 128), (200, 2000, 640, 64), (300, 1024, 1024, 128),
-          (515, 272, 192, 32), (1, 8, 16384, 128), (4, 12000, 256, 64)]
+          (515, 272, 192, 32), (1, 8, 16384, 128), (4, 12000, 256, 64),
+          # over 1024 pairs of 16 rows and 64 tokens: the kernel for many tokens; one, two, three k tiles and more
+          (33, 16500, 128, 128), (1030, 1100, 96, 32), (65, 8300, 320, 64), (600, 1999, 1152, 128), (515, 2320, 160, 32),
+          (128, 8208, 256, 128), (700, 1600, 1088, 64), (64, 16400, 544, 32)]
 
 
 @pytest.mark.parametrize("T,N,K,G", SHAPES)
@@ -111,7 +114,8 @@ def test_shapes(T, N, K, G, act):
 
 
 @pytest.mark.parametrize("T,N,K,G", [(1, 2, 32, 32), (1, 4096, 1024, 128), (7, 34, 192, 64), (20, 512, 2048, 128),
-                                     (64, 258, 416, 32), (100, 1040, 512, 128), (260, 640, 768, 64)])
+                                     (64, 258, 416, 32), (100, 1040, 512, 128), (260, 640, 768, 64),
+                                     (514, 1270, 320, 64), (100, 4500, 416, 32), (40, 9000, 384, 128)])
 @pytest.mark.parametrize("act", [BF, FP, I8], ids=["bf16", "fp16", "int8"])
 @pytest.mark.parametrize("zeros", [False, True], ids=["sym", "zeros"])
 def test_gated(T, N, K, G, act, zeros):
@@ -122,9 +126,10 @@ def test_gated(T, N, K, G, act, zeros):
 
 @pytest.mark.parametrize("act", [BF, I8], ids=["bf16", "int8"])
 @pytest.mark.parametrize("G", [32, 64, 128])
-def test_every_code_and_position(act, G):
+@pytest.mark.parametrize("N", [40, 4120], ids=["few", "many"])
+def test_every_code_and_position(act, G, N):
     """x = unit vectors: every element of W comes out by itself, exactly rounded once."""
-    N, K = 40, 256
+    K = 256
     c = make(K, N, K, G, act, True, False)
     c["x"] = torch.eye(K).to(act)
     c["xs"] = torch.ones(K) if act == I8 else None
