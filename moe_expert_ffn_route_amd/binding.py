@@ -321,22 +321,22 @@ def _arg(t, name: str, dtype, numel: int, device: int) -> Optional[int]:
     """The device pointer of an argument of `numel` elements (None: NULL)."""
     if t is None:
         return None
+    if t.dtype is dtype and t.numel() == numel and t.get_device() == device >= 0 and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype or t.numel() != numel:
         raise ValueError(f"{name}: expected {numel} elements of {dtype}, got {tuple(t.shape)} of {t.dtype}")
     if t.get_device() != device or device < 0:
         raise ValueError(f"{name}: expected a tensor on the GPU that holds the call's first tensor")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: tensors passed to libmoe_w8a8 must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name}: tensors passed to libmoe_w8a8 must be contiguous")
 
 
 def _call(where: str, fn, device: int, stream, *args) -> None:
     """fn(*args, stream) with `device` current; the stream defaults to that
-    device's current one."""
+    device's current one (its handle: the stream object costs a microsecond)."""
     if torch.cuda.current_device() != device:
         with torch.cuda.device(device):
             return _call(where, fn, device, stream, *args)
-    rc = fn(*args, torch.cuda.current_stream(device).cuda_stream if stream is None else _stream(stream))
+    rc = fn(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream))
     if rc != MOE_OK:
         raise MoeError(rc, where)
 

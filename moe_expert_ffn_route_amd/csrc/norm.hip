@@ -11,8 +11,15 @@
 // which the squares are summed. rstd enters only the scale, and the codes of
 // rows (or groups) whose amax lies under the floor.
 //
-// A row (of up to 16384 elements) is held as fp32 p in the registers of its
-// kTPR threads between the one read of x, residual and w and the writes.
+// A row (of up to 16384 elements) is held as fp32 p in the registers of one
+// workgroup between the one read of x, residual and w and the writes. What
+// that costs is set by memory: T 8192, H 4096, bf16 with residual, y and int8
+// codes (302 MB) takes 60 us, against 61 us for a copy of as many bytes.
+//
+// Every load is issued before anything waits for one: none stands behind a
+// branch. Lanes past the row's end read its last chunk again and count nothing.
+// A row whose length is no multiple of kVec ends in up to seven elements more,
+// one per thread.
 #include "internal.h"
 #include "rowquant.h"
 
@@ -40,90 +47,117 @@ __device__ __forceinline__ void store8(T *p, const float (&v)[kVec]) {
     for (int e = 0; e < kVec; ++e) from_f32(v[e], raw[e]);
     __builtin_memcpy(p, raw, sizeof raw);
 }
-// The last chunk of a row whose length is no multiple of kVec: n < kVec.
-template <typename T>
-__device__ __forceinline__ void load_tail(const T *p, int n, float (&v)[kVec]) {
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) v[e] = e < n ? to_f32(p[e]) : 0.0f;
+// Sum and maximum over the wave: DPP shifts within rows of 16 lanes, then the
+// row ends to the following rows; lane 63 holds the result.
+template <int CTRL>
+__device__ __forceinline__ float dpp_or(float v, float absent) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(absent), __float_as_int(v), CTRL, 0xF, 0xF, false));
 }
-template <typename T>
-__device__ __forceinline__ void store_tail(T *p, int n, const float (&v)[kVec]) {
-#pragma unroll
-    for (int e = 0; e < kVec; ++e)
-        if (e < n) from_f32(v[e], p[e]);
+__device__ __forceinline__ float last_lane_sum(float v) {
+    v += dpp_or<0x111>(v, 0.0f);
+    v += dpp_or<0x112>(v, 0.0f);
+    v += dpp_or<0x114>(v, 0.0f);
+    v += dpp_or<0x118>(v, 0.0f);
+    // lanes 15, 31, 47, 63 hold their rows' sums; rows 1 and 3, then 2 and 3, take what is before them
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x142, 0xA, 0xF, false));
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x143, 0xC, 0xF, false));
+    return v;
 }
-
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int d = kWave / 2; d > 0; d >>= 1) v += __shfl_xor(v, d, kWave);
+__device__ __forceinline__ float last_lane_max(float v) {  // of magnitudes
+    v = fmaxf(v, dpp_or<0x111>(v, 0.0f));
+    v = fmaxf(v, dpp_or<0x112>(v, 0.0f));
+    v = fmaxf(v, dpp_or<0x114>(v, 0.0f));
+    v = fmaxf(v, dpp_or<0x118>(v, 0.0f));
+    v = fmaxf(v, dpp_or<0x142>(v, 0.0f));
+    v = fmaxf(v, dpp_or<0x143>(v, 0.0f));
     return v;
 }
 
-// One workgroup of TPR threads per row, CH chunks of kVec elements per
-// thread: H <= TPR * CH * kVec.
-template <typename T, typename W, int TPR, int CH>
-__global__ __launch_bounds__(TPR) void norm_kernel(NormArgs a) {
+// TPR threads per row, CH chunks of kVec elements per thread: H <= TPR * CH *
+// kVec. A workgroup is one row, or four rows of one wave each. TAIL: H is no
+// multiple of kVec.
+template <int TPR>
+constexpr int kRows = TPR == kWave ? 4 : 1;
+template <typename T, typename W, int TPR, int CH, bool TAIL>
+__global__ __launch_bounds__(TPR *kRows<TPR>) void norm_kernel(NormArgs a) {
     constexpr int kWaves = TPR / kWave;
-    __shared__ float s_sum[kWaves], s_max[kWaves];
-    const int tr = threadIdx.x;
-    const size_t base = static_cast<size_t>(blockIdx.x) * a.H;
+    const int tr = threadIdx.x % TPR, row = blockIdx.x * kRows<TPR> + threadIdx.x / TPR;
+    if (kRows<TPR> > 1 && row >= a.T) return;  // whole waves, and such a row has no barrier
+    const size_t base = static_cast<size_t>(row) * a.H;
     const T *x = static_cast<const T *>(a.x) + base;
-    const T *res = a.residual ? static_cast<const T *>(a.residual) + base : nullptr;
+    const T *res = static_cast<const T *>(a.residual) + base;
     const W *w = static_cast<const W *>(a.weight);
-    T *res_out = a.residual_out ? static_cast<T *>(a.residual_out) + base : nullptr;
+    T *res_out = static_cast<T *>(a.residual_out) + base;
+    const int chunks = a.H / kVec, rest = a.H % kVec;  // whole chunks, and the elements after them
+    const bool tail = TAIL && tr < rest;
+    const int it = TAIL ? chunks * kVec + min(tr, rest - 1) : 0;
 
-    float p[CH][kVec];
+    // chunk j of the thread, or the row's last one (a row without a whole chunk: nothing is read)
+    auto at = [&](int j) { return min(tr + j * TPR, chunks - 1) * kVec; };
+    float p[CH][kVec], g[CH][kVec], pt = 0.0f, gt = 1.0f;
+    if (!TAIL || chunks > 0) {
+        float r[CH][kVec];
+#pragma unroll
+        for (int j = 0; j < CH; ++j) load8(x + at(j), p[j]);
+        if (a.residual) {
+#pragma unroll
+            for (int j = 0; j < CH; ++j) load8(res + at(j), r[j]);
+        }
+        if (w) {
+#pragma unroll
+            for (int j = 0; j < CH; ++j) load8(w + at(j), g[j]);
+        }
+        if (a.residual) {
+#pragma unroll
+            for (int j = 0; j < CH; ++j)
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) p[j][e] = p[j][e] + r[j][e];
+        }
+    }
+    if (TAIL) {
+        pt = to_f32(x[it]);
+        if (a.residual) pt = pt + to_f32(res[it]);
+        if (w) gt = to_f32(w[it]);
+    }
     float sum = 0.0f, mx = 0.0f;
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-        const int i = (tr + j * TPR) * kVec, left = a.H - i;
-        if (left <= 0) {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) p[j][e] = 0.0f;
-            continue;
-        }
-        float g[kVec];
-        if (left >= kVec) {
-            load8(x + i, p[j]);
-            if (res) {
-                load8(res + i, g);
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) p[j][e] = p[j][e] + g[e];
-            }
-            if (w) load8(w + i, g);
-        } else {
-            load_tail(x + i, left, p[j]);
-            if (res) {
-                load_tail(res + i, left, g);
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) p[j][e] = p[j][e] + g[e];
-            }
-            if (w) load_tail(w + i, left, g);
-        }
-        if (res_out) {
-            if (left >= kVec) store8(res_out + i, p[j]);
-            else store_tail(res_out + i, left, p[j]);
-        }
+        const bool in = tr + j * TPR < chunks;
+        if (in && a.residual_out) store8(res_out + at(j), p[j]);
 #pragma unroll
         for (int e = 0; e < kVec; ++e) {
+            if (!in) p[j][e] = 0.0f;
             sum += p[j][e] * p[j][e];
-            if (w) p[j][e] = p[j][e] * g[e];
+            if (in && w) p[j][e] = p[j][e] * g[j][e];
             mx = fmaxf(mx, fabsf(p[j][e]));
         }
     }
-    sum = wave_sum(sum);
-    mx = wave_max(mx);
-    if ((tr & (kWave - 1)) == 0) {
-        s_sum[tr / kWave] = sum;
-        s_max[tr / kWave] = mx;
+    if (TAIL) {
+        if (tail && a.residual_out) from_f32(pt, res_out[it]);
+        if (!tail) pt = 0.0f;
+        sum += pt * pt;
+        if (tail && w) pt = pt * gt;
+        mx = fmaxf(mx, fabsf(pt));
     }
-    __syncthreads();
-    sum = 0.0f;
-    mx = 0.0f;
+    sum = last_lane_sum(sum);
+    mx = last_lane_max(mx);
+    if constexpr (kWaves == 1) {  // the wave has read every element: y may lie where x or residual did
+        sum = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(sum), kWave - 1));
+        mx = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(mx), kWave - 1));
+    } else {
+        __shared__ float s_sum[kWaves], s_max[kWaves];
+        if ((tr & (kWave - 1)) == kWave - 1) {
+            s_sum[tr / kWave] = sum;
+            s_max[tr / kWave] = mx;
+        }
+        __syncthreads();  // the same, for the workgroup
+        sum = 0.0f;
+        mx = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) {
-        sum += s_sum[i];
-        mx = fmaxf(mx, s_max[i]);
+        for (int i = 0; i < kWaves; ++i) {
+            sum += s_sum[i];
+            mx = fmaxf(mx, s_max[i]);
+        }
     }
     const float rstd = 1.0f / sqrtf(sum / static_cast<float>(a.H) + a.rms_eps);
 
@@ -131,64 +165,79 @@ __global__ __launch_bounds__(TPR) void norm_kernel(NormArgs a) {
         T *y = static_cast<T *>(a.y) + base;
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
-            const int i = (tr + j * TPR) * kVec, left = a.H - i;
-            if (left <= 0) break;
+            if (tr + j * TPR >= chunks) break;
             float v[kVec];
 #pragma unroll
             for (int e = 0; e < kVec; ++e) v[e] = p[j][e] * rstd;
-            if (left >= kVec) store8(y + i, v);
-            else store_tail(y + i, left, v);
+            store8(y + at(j), v);
         }
+        if (tail) from_f32(pt * rstd, y[it]);
     }
     if (!a.q) return;
     const bool fp8 = a.quant == MOE_QUANT_E4M3;
     const float top_inv = fp8 ? 1.0f / kQMax<true> : 1.0f / kQMax<false>;
     uint8_t *q = static_cast<uint8_t *>(a.q) + base;
-    const int gl = a.group / kVec;  // lanes per group
-    float *scale = a.q_scale + static_cast<size_t>(blockIdx.x) * (a.group ? a.H / a.group : 1);
+    float *scale = a.q_scale + static_cast<size_t>(row) * (a.group ? a.H / a.group : 1);
+    auto inv_of = [&](float pm, float am) {
+        return am >= a.amax_eps ? 1.0f / pm : rstd * (1.0f / a.amax_eps);
+    };
+    auto quant8 = [&](const float (&v)[kVec], float inv) -> uint64_t {
+        uint32_t lo, hi;
+        if (fp8) {
+            lo = quant4<true>(v[0], v[1], v[2], v[3], inv);
+            hi = quant4<true>(v[4], v[5], v[6], v[7], inv);
+        } else {
+            lo = quant4<false>(v[0], v[1], v[2], v[3], inv);
+            hi = quant4<false>(v[4], v[5], v[6], v[7], inv);
+        }
+        return lo | (static_cast<uint64_t>(hi) << 32);
+    };
+    if (a.group) {  // a group is gl neighbouring lanes' chunks; groups divide H, so there is no tail
+        const int gl = a.group / kVec;
 #pragma unroll
-    for (int j = 0; j < CH; ++j) {
-        const int i = (tr + j * TPR) * kVec, left = a.H - i;
-        if (j * TPR * kVec >= a.H) break;  // uniform
-        float pm = mx;
-        if (gl) {  // a group is gl neighbouring lanes' chunks and never straddles the row's end
-            pm = 0.0f;
+        for (int j = 0; j < CH; ++j) {
+            if (j * TPR >= chunks) break;  // uniform
+            float pm = 0.0f;
 #pragma unroll
             for (int e = 0; e < kVec; ++e) pm = fmaxf(pm, fabsf(p[j][e]));
             for (int d = gl / 2; d > 0; d >>= 1) pm = fmaxf(pm, __shfl_xor(pm, d, kWave));
+            if (tr + j * TPR >= chunks) continue;
+            const float am = pm * rstd;
+            const uint64_t code = quant8(p[j], inv_of(pm, am));
+            __builtin_memcpy(q + at(j), &code, sizeof code);
+            if ((tr & (gl - 1)) == 0) scale[at(j) / a.group] = fmaxf(am, a.amax_eps) * top_inv;
         }
-        if (left <= 0) continue;
-        const float am = pm * rstd;
-        const float inv = am >= a.amax_eps ? 1.0f / pm : rstd * (1.0f / a.amax_eps);
-        uint32_t lo, hi;
-        if (fp8) {
-            lo = quant4<true>(p[j][0], p[j][1], p[j][2], p[j][3], inv);
-            hi = quant4<true>(p[j][4], p[j][5], p[j][6], p[j][7], inv);
-        } else {
-            lo = quant4<false>(p[j][0], p[j][1], p[j][2], p[j][3], inv);
-            hi = quant4<false>(p[j][4], p[j][5], p[j][6], p[j][7], inv);
-        }
-        const uint64_t code = lo | (static_cast<uint64_t>(hi) << 32);
-        if (left >= kVec) {
-            __builtin_memcpy(q + i, &code, sizeof code);
-        } else {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e)
-                if (e < left) q[i + e] = static_cast<uint8_t>(code >> (8 * e));
-        }
-        if (gl ? (tr & (gl - 1)) == 0 : (j == 0 && tr == 0))
-            scale[gl ? i / a.group : 0] = fmaxf(am, a.amax_eps) * top_inv;
+        return;
     }
+    const float am = mx * rstd, inv = inv_of(mx, am);
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+        if (tr + j * TPR >= chunks) break;
+        const uint64_t code = quant8(p[j], inv);
+        __builtin_memcpy(q + at(j), &code, sizeof code);
+    }
+    if (tail) q[it] = static_cast<uint8_t>(fp8 ? quant4<true>(pt, 0.0f, 0.0f, 0.0f, inv) : quant4<false>(pt, 0.0f, 0.0f, 0.0f, inv));
+    if (tr == 0) *scale = fmaxf(am, a.amax_eps) * top_inv;
 }
 
+template <typename T, typename W, int TPR, int CH>
+hipError_t launch_rows(const NormArgs &a, hipStream_t s) {
+    const dim3 grid((a.T + kRows<TPR> - 1) / kRows<TPR>), blk(TPR * kRows<TPR>);
+    if (a.H % kVec) hipLaunchKernelGGL((norm_kernel<T, W, TPR, CH, true>), grid, blk, 0, s, a);
+    else hipLaunchKernelGGL((norm_kernel<T, W, TPR, CH, false>), grid, blk, 0, s, a);
+    return hipGetLastError();
+}
+
+// Short rows: one wave. Else 256 threads, or for long rows 1024 while they are
+// few: T 64, H 7168, groups of 128: 6.5 us against 8.3 with 256 threads; T 300,
+// H 16384: 16.8 against 18.7; but T 2000, H 7168: 40 against 34.
 template <typename T, typename W>
 hipError_t launch(const NormArgs &a, hipStream_t s) {
-    const dim3 grid(a.T), blk(256);
-    if (a.H <= 256 * kVec * 2)
-        hipLaunchKernelGGL((norm_kernel<T, W, 256, 2>), grid, blk, 0, s, a);
-    else
-        hipLaunchKernelGGL((norm_kernel<T, W, 256, 8>), grid, blk, 0, s, a);
-    return hipGetLastError();
+    if (a.H <= 64 * kVec) return launch_rows<T, W, 64, 1>(a, s);
+    if (a.H <= 256 * kVec) return launch_rows<T, W, 256, 1>(a, s);
+    if (a.H <= 512 * kVec) return launch_rows<T, W, 256, 2>(a, s);
+    if (a.T < 512) return a.H <= 1024 * kVec ? launch_rows<T, W, 1024, 1>(a, s) : launch_rows<T, W, 1024, 2>(a, s);
+    return a.H <= 1024 * kVec ? launch_rows<T, W, 256, 4>(a, s) : launch_rows<T, W, 256, 8>(a, s);
 }
 
 }  // namespace
