@@ -8,11 +8,12 @@
 // depend on its order would make them depend on the tiling, the batch size
 // and the split of H. They are therefore those of 64-bit logits, in one of
 // two ways:
-//   - x and W both bf16, or both fp16: MFMA with fp32 sums over 32 or 64
-//     products, which are added up in fp64. |x| |w| (2-norms), which is no
-//     less than the sum of |x * w|, bounds how far such a logit is off. Where the
-//     bound leaves open which of two experts comes first, the choice kernel
-//     computes the logits of those experts again, in fp64.
+//   - x and W both bf16, or both fp16, or bf16 x and fp32 W (large products;
+//     W is split into three bf16 parts, which hold its 24 bits): MFMA with
+//     fp32 sums over 32 or 64 h, which are added up in fp64. |x| |w| (2-norms),
+//     which is no less than the sum of |x * w|, bounds how far such a logit is
+//     off. Where the bound leaves open which of two experts comes first, the
+//     choice kernel computes the logits of those experts again, in fp64.
 //   - other types: fp64 MFMA throughout (their products are exact in it).
 //
 // Two launches: the logits, in up to kMaxSplit parts of H, into the
@@ -43,8 +44,9 @@ constexpr int kMaxSplit = 8;
 // truncates): n * 2^-23 of the sum of magnitudes, which Cauchy's inequality
 // bounds by the norms.
 constexpr double kUnit = 0x1p-23;
-// Products under the smallest normal fp32 may be dropped: 16384 of them.
-constexpr double kTiny = 0x1p-110;
+// Inputs and products under the smallest normal fp32 may be dropped: 16384 of
+// them, the other factor up to 2^20.
+constexpr double kTiny = 0x1p-90;
 
 // Eight elements from h = k of a row of H. WHOLE: they are known to be there
 // (no branch, so that loads can be issued in a row).
@@ -69,6 +71,15 @@ template <>
 constexpr bool kFast<Bf16, Bf16> = true;
 template <>
 constexpr bool kFast<Fp16, Fp16> = true;
+// Planes of W that the fp32 sums may be made of, else 0.
+template <typename T, typename W>
+constexpr int kPlanes = kFast<T, W> ? 1 : 0;
+template <>
+constexpr int kPlanes<Bf16, float> = 3;
+// Three planes pay where the fp64 MFMA is the time: bf16 x, fp32 W, E 256, H
+// 4096, logits and choice together, planes / fp64: T 4096 92 / 177 us, T 512
+// 30 / 28, and T 509, E 72, H 2501 25 / 23 (the doubtful choices cost 6 us).
+constexpr int64_t kPlanesFrom = int64_t(1) << 29;  // products
 
 template <typename T>
 __device__ __forceinline__ v4f mfma32(v4i a, v4i b, v4f c) {
@@ -78,10 +89,13 @@ __device__ __forceinline__ v4f mfma32(v4i a, v4i b, v4f c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
 }
 
-// n += the squares of eight elements.
+// n += the squares of 16 bytes of elements.
 template <typename T>
 __device__ __forceinline__ void add_squares(v4i v, float &n) {
-    if constexpr (__is_same(T, Bf16)) {
+    if constexpr (__is_same(T, float)) {  // four elements
+#pragma unroll
+        for (int i = 0; i < 4; ++i) n = __builtin_fmaf(__int_as_float(v[i]), __int_as_float(v[i]), n);
+    } else if constexpr (__is_same(T, Bf16)) {
         typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -140,7 +154,7 @@ __device__ __forceinline__ double value_of(int64_t k) {
 
 // Fragments of 32 h, in the two ways that the logits are summed: `sum` += in
 // fp64; fast(): FOLD steps are summed in fp32 first.
-template <typename T, typename W, int TM, int TN>
+template <typename T, typename W, bool FAST, int TM, int TN>
 struct Tiles {
     v4d sum[TM][TN];
     __device__ __forceinline__ void clear() {
@@ -149,16 +163,22 @@ struct Tiles {
 #pragma unroll
             for (int j = 0; j < TN; ++j) sum[i][j] = v4d{0.0, 0.0, 0.0, 0.0};
     }
-    template <int FOLD>
-    __device__ __forceinline__ void fast(const v4i (&x)[FOLD][TM], const v4i (&w)[FOLD][TN]) {
+    // The planes of W come smallest first: what their sums are off by is then
+    // 2^-7 of a plane's, and with a plane more or less the bound stays n * kUnit
+    // (times 1.05, which the choice takes).
+    template <int FOLD, int PLANES>
+    __device__ __forceinline__ void fast(const v4i (&x)[FOLD][TM], const v4i (&w)[PLANES][FOLD][TN]) {
         v4f acc[TM][TN];
 #pragma unroll
-        for (int s = 0; s < FOLD; ++s)
+        for (int p = PLANES - 1; p >= 0; --p)
 #pragma unroll
-            for (int i = 0; i < TM; ++i)
+            for (int s = 0; s < FOLD; ++s)
 #pragma unroll
-                for (int j = 0; j < TN; ++j)
-                    acc[i][j] = mfma32<T>(x[s][i], w[s][j], s == 0 ? v4f{0.0f, 0.0f, 0.0f, 0.0f} : acc[i][j]);
+                for (int i = 0; i < TM; ++i)
+#pragma unroll
+                    for (int j = 0; j < TN; ++j)
+                        acc[i][j] = mfma32<T>(x[s][i], w[p][s][j],
+                                              p == PLANES - 1 && s == 0 ? v4f{0.0f, 0.0f, 0.0f, 0.0f} : acc[i][j]);
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -187,7 +207,7 @@ struct Tiles {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     // result registers: fp32 D rows 4 * (l / 16) + q, fp64 D rows l / 16 + 4 * q
-                    const int t = t0 + i * 16 + (kFast<T, W> ? 4 * (lane >> 4) + q : (lane >> 4) + 4 * q);
+                    const int t = t0 + i * 16 + (FAST ? 4 * (lane >> 4) + q : (lane >> 4) + 4 * q);
                     const int e = e0 + j * 16 + (lane & 15);
                     if (t < a.T && e < a.E) {
                         const size_t o = (static_cast<size_t>(part) * a.T + t) * a.E + e;
@@ -212,7 +232,7 @@ __global__ __launch_bounds__(kBlock) void logits_few_kernel(GateArgs a, int chun
     // rows past the end read the last one; their results are not stored
     const T *x = static_cast<const T *>(a.x) + static_cast<size_t>(min(r, a.T - 1)) * a.H;
     const W *w = static_cast<const W *>(a.weight) + static_cast<size_t>(min(e0 + r, a.E - 1)) * a.H;
-    Tiles<T, W, 1, 1> tile;
+    Tiles<T, W, kFast<T, W>, 1, 1> tile;
     tile.clear();
     float xn = 0.0f, wn = 0.0f;  // squares of the lane's elements
     const int c_end = min((part + 1) * chunks_per_part, (a.H + kChunk - 1) / kChunk);
@@ -228,12 +248,12 @@ __global__ __launch_bounds__(kBlock) void logits_few_kernel(GateArgs a, int chun
 #pragma unroll
         for (int s = 0; s < kChunk / kStep; ++s) {
             if constexpr (kFast<T, W>) {
-                v4i xf[1][1], wf[1][1];
+                v4i xf[1][1], wf[1][1][1];
                 __builtin_memcpy(&xf[0][0], xv[s][0], 16);
-                __builtin_memcpy(&wf[0][0], wv[s][0], 16);
+                __builtin_memcpy(&wf[0][0][0], wv[s][0], 16);
                 add_squares<T>(xf[0][0], xn);
-                add_squares<T>(wf[0][0], wn);
-                tile.template fast<1>(xf, wf);
+                add_squares<T>(wf[0][0][0], wn);
+                tile.template fast<1, 1>(xf, wf);
             } else {
                 tile.full(xv[s], wv[s]);
             }
@@ -323,6 +343,29 @@ struct Stage {  // kTileRows rows of kChunk elements
             *reinterpret_cast<v4i *>(lds + (row * kSlots + (c ^ (row & 15))) * 16) = v[i];
         }
     }
+    // fp32 slots as three planes of bf16: the upper 8 of the 24 bits, the next
+    // and the last (a truncation and an exact difference each)
+    static constexpr int kPlaneBytes = kTileRows * kChunk * 2;
+    __device__ __forceinline__ void put_planes(char *lds) const {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int slot = threadIdx.x + i * kBlock, row = slot / kSlots, c = slot % kSlots;
+            float f[4];
+            __builtin_memcpy(f, &v[i], 16);
+#pragma unroll
+            for (int p = 0; p < 3; ++p) {
+                uint32_t b[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    b[e] = __float_as_uint(f[e]);
+                    f[e] = f[e] - __uint_as_float(b[e] & 0xFFFF0000u);
+                }
+                const uint64_t pair = __builtin_amdgcn_perm(b[1], b[0], 0x07060302) |
+                                      static_cast<uint64_t>(__builtin_amdgcn_perm(b[3], b[2], 0x07060302)) << 32;
+                *reinterpret_cast<uint64_t *>(lds + p * kPlaneBytes + (row * 16 + ((c / 2) ^ (row & 15))) * 16 + c % 2 * 8) = pair;
+            }
+        }
+    }
     // eight elements of a row from element k (a multiple of 8)
     static __device__ __forceinline__ void get(const char *lds, int row, int k, T (&out)[kVec]) {
 #pragma unroll
@@ -338,9 +381,11 @@ struct Stage {  // kTileRows rows of kChunk elements
 // 21.6, four 28.8 + 24.5 (a wider bound leaves more tokens open).
 constexpr int kFold = 2;
 
-template <typename T, typename W>
+template <typename T, typename W, int PLANES>
 __global__ __launch_bounds__(kBlock) void logits_many_kernel(GateArgs a, int chunks_per_part, int e_tiles, int units) {
-    __shared__ __attribute__((aligned(16))) char s_x[Stage<T>::kBytes], s_w[Stage<W>::kBytes];
+    constexpr bool FAST = PLANES > 0;
+    __shared__ __attribute__((aligned(16))) char s_x[Stage<T>::kBytes];
+    __shared__ __attribute__((aligned(16))) char s_w[PLANES > 1 ? PLANES * Stage<T>::kBytes : Stage<W>::kBytes];
     // The expert tiles of one unit (token tile, part) read the same x: they
     // get block numbers that are equal modulo 8, so that one XCD's L2 serves
     // them all.
@@ -352,7 +397,7 @@ __global__ __launch_bounds__(kBlock) void logits_many_kernel(GateArgs a, int chu
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int r = lane & 15, kq = lane >> 4;
     const int tm = (wave >> 1) * 32, en = (wave & 1) * 32;
-    Tiles<T, W, 2, 2> tile;
+    Tiles<T, W, FAST, 2, 2> tile;
     tile.clear();
     Stage<T> sx;
     Stage<W> sw;
@@ -373,34 +418,36 @@ __global__ __launch_bounds__(kBlock) void logits_many_kernel(GateArgs a, int chu
     for (int c = c0; c < c_end; ++c) {
         __syncthreads();
         sx.put(s_x);
-        sw.put(s_w);
-        if constexpr (kFast<T, W>) {
+        if constexpr (PLANES > 1) sw.put_planes(s_w);
+        else sw.put(s_w);
+        if constexpr (FAST) {
 #pragma unroll
-            for (int i = 0; i < Stage<T>::kPer; ++i) {
-                add_squares<T>(sx.v[i], xn[i]);
-                add_squares<T>(sw.v[i], wn[i]);
-            }
+            for (int i = 0; i < Stage<T>::kPer; ++i) add_squares<T>(sx.v[i], xn[i]);
+#pragma unroll
+            for (int i = 0; i < Stage<W>::kPer; ++i) add_squares<W>(sw.v[i], wn[i]);
         }
         __syncthreads();
         if (c + 1 < c_end) fetch(c + 1);
-        if constexpr (kFast<T, W>) {
+        if constexpr (FAST) {
 #pragma unroll
             for (int s = 0; s < kChunk / kStep; s += kFold) {
-                v4i xf[kFold][2], wf[kFold][2];
+                v4i xf[kFold][2], wf[PLANES][kFold][2];
 #pragma unroll
                 for (int f = 0; f < kFold; ++f) {
                     const int k = (s + f) * kStep + kq * kVec;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        T xv[kVec];
-                        W wv[kVec];
-                        Stage<T>::get(s_x, tm + i * 16 + r, k, xv);
-                        Stage<W>::get(s_w, en + i * 16 + r, k, wv);
-                        __builtin_memcpy(&xf[f][i], xv, 16);
-                        __builtin_memcpy(&wf[f][i], wv, 16);
+                        T v[kVec];
+                        Stage<T>::get(s_x, tm + i * 16 + r, k, v);
+                        __builtin_memcpy(&xf[f][i], v, 16);
+#pragma unroll
+                        for (int p = 0; p < PLANES; ++p) {  // a plane lies as 16-bit elements do
+                            Stage<T>::get(s_w + p * Stage<T>::kBytes, en + i * 16 + r, k, v);
+                            __builtin_memcpy(&wf[p][f][i], v, 16);
+                        }
                     }
                 }
-                tile.template fast<kFold>(xf, wf);
+                tile.template fast<kFold, PLANES>(xf, wf);
             }
         } else {
 #pragma unroll
@@ -417,19 +464,16 @@ __global__ __launch_bounds__(kBlock) void logits_many_kernel(GateArgs a, int chu
         }
     }
     tile.store(a, part, t0 + tm, e0 + en, lane);
-    if constexpr (kFast<T, W>) {  // a row's slots lie in 16 neighbouring lanes
-        static_assert(Stage<T>::kSlots == 16, "one row per 16 lanes");
+    if constexpr (FAST) {  // a row's slots lie in neighbouring lanes, 16 of them or 32
+        auto put = [&](float n, int lanes, int i, bool mine, int row0, int rows, float *out) {
+            for (int d = lanes / 2; d > 0; d >>= 1) n += __shfl_xor(n, d, kWave);
+            const int row = row0 + static_cast<int>(threadIdx.x + i * kBlock) / lanes;
+            if (mine && (lane & (lanes - 1)) == 0 && row < rows) out[part * rows + row] = n;
+        };
 #pragma unroll
-        for (int i = 0; i < Stage<T>::kPer; ++i) {
+        for (int i = 0; i < Stage<T>::kPer; ++i) put(xn[i], Stage<T>::kSlots, i, e0 == 0, t0, a.T, a.x_norms);
 #pragma unroll
-            for (int d = 8; d > 0; d >>= 1) {
-                xn[i] += __shfl_xor(xn[i], d, kWave);
-                wn[i] += __shfl_xor(wn[i], d, kWave);
-            }
-            const int row = static_cast<int>(threadIdx.x + i * kBlock) / 16;
-            if (r == 0 && e0 == 0 && t0 + row < a.T) a.x_norms[part * a.T + t0 + row] = xn[i];
-            if (r == 0 && t0 == 0 && e0 + row < a.E) a.w_norms[part * a.E + e0 + row] = wn[i];
-        }
+        for (int i = 0; i < Stage<W>::kPer; ++i) put(wn[i], Stage<W>::kSlots, i, t0 == 0, e0, a.E, a.w_norms);
     }
 }
 
@@ -478,10 +522,10 @@ __device__ __forceinline__ double score_of(double l, double m) {
 }
 
 // One wave per token; lane l holds experts l, l + 64, ... (NPL of them).
-// F: the type of x and weight where the logits are bounded fp32 sums, void
-// where they are 64-bit sums.
+// FAST: the logits are bounded fp32 sums of T and W; else they are 64-bit sums,
+// and T and W do not matter.
 //
-// K choices in order. With F, an expert that lies closer than `off` below a
+// K choices in order. FAST, an expert that lies closer than `off` below a
 // choice is marked, and so is that choice; the marked ones' logits are then
 // computed in fp64 and the choice is made again. An unmarked expert is further
 // than `off` from all that it was compared with, so its place stands.
@@ -490,9 +534,8 @@ __device__ __forceinline__ double score_of(double l, double m) {
 // latency, most of it instruction fetches of a kernel that runs once: scores
 // are a template parameter and the second choice shares the first one's code
 // (13 -> 8 us at 8 tokens, 256 experts).
-template <typename F, int SCORE, int NPL>
+template <bool FAST, typename T, typename W, int SCORE, int NPL>
 __global__ __launch_bounds__(kBlock) void choose_kernel(GateArgs a, int parts, double gamma) {
-    constexpr bool FAST = !__is_same(F, void);
     const int lane = threadIdx.x & (kWave - 1);
     const int t = blockIdx.x * (kBlock / kWave) + threadIdx.x / kWave;
     if (t >= a.T) return;
@@ -546,9 +589,14 @@ __global__ __launch_bounds__(kBlock) void choose_kernel(GateArgs a, int parts, d
 #pragma unroll
         for (int j = 0; j < NPL; ++j) wn = n[j] <= wn ? wn : n[j];
         wn = __uint_as_float(wave_max_int<uint32_t>(__float_as_uint(wn), 0u));
-        off = 2.0 * (gamma * 1.01 * sqrt(static_cast<double>(xn) * static_cast<double>(wn)) + kTiny);
+        off = 2.0 * (gamma * 1.05 * sqrt(static_cast<double>(xn) * static_cast<double>(wn)) + kTiny);
         if (a.bias) off *= SCORE == MOE_SCORE_SOFTMAX ? 2.5 : SCORE == MOE_SCORE_SIGMOID ? 0.25 : 0.34;
-        off += 1e-13;
+        // and the 64-bit roundings of score + bias
+        float bm = 1.0f;
+#pragma unroll
+        for (int j = 0; j < NPL; ++j) bm = a.bias && fabsf(bias[j]) < __builtin_inff() ? fmaxf(bm, fabsf(bias[j])) : bm;
+        bm = __uint_as_float(wave_max_int<uint32_t>(__float_as_uint(bm), 0u));
+        off += 0x1p-50 * static_cast<double>(bm);
     }
     double s[NPL], total;  // scores (softmax: undivided, `total` their sum)
     int id_mine;           // lane k keeps the k-th choice
@@ -640,7 +688,7 @@ __global__ __launch_bounds__(kBlock) void choose_kernel(GateArgs a, int parts, d
                 }
                 if (e[0] < 0) break;
                 double v[2];
-                exact_logits<F, F>(a, t, e[0], e[1] < 0 ? e[0] : e[1], lane, v[0], v[1]);
+                exact_logits<T, W>(a, t, e[0], e[1] < 0 ? e[0] : e[1], lane, v[0], v[1]);
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -670,19 +718,19 @@ __global__ __launch_bounds__(kBlock) void choose_kernel(GateArgs a, int parts, d
     }
 }
 
-template <typename F, int SCORE>
+template <bool FAST, typename T, typename W, int SCORE>
 void choose_score(const GateArgs &a, int parts, double gamma, hipStream_t s) {
     const dim3 grid((a.T + kBlock / kWave - 1) / (kBlock / kWave)), blk(kBlock);
-    if (a.E <= kWave) hipLaunchKernelGGL((choose_kernel<F, SCORE, 1>), grid, blk, 0, s, a, parts, gamma);
-    else if (a.E <= 2 * kWave) hipLaunchKernelGGL((choose_kernel<F, SCORE, 2>), grid, blk, 0, s, a, parts, gamma);
-    else if (a.E <= 4 * kWave) hipLaunchKernelGGL((choose_kernel<F, SCORE, 4>), grid, blk, 0, s, a, parts, gamma);
-    else hipLaunchKernelGGL((choose_kernel<F, SCORE, 16>), grid, blk, 0, s, a, parts, gamma);
+    if (a.E <= kWave) hipLaunchKernelGGL((choose_kernel<FAST, T, W, SCORE, 1>), grid, blk, 0, s, a, parts, gamma);
+    else if (a.E <= 2 * kWave) hipLaunchKernelGGL((choose_kernel<FAST, T, W, SCORE, 2>), grid, blk, 0, s, a, parts, gamma);
+    else if (a.E <= 4 * kWave) hipLaunchKernelGGL((choose_kernel<FAST, T, W, SCORE, 4>), grid, blk, 0, s, a, parts, gamma);
+    else hipLaunchKernelGGL((choose_kernel<FAST, T, W, SCORE, 16>), grid, blk, 0, s, a, parts, gamma);
 }
-template <typename F>
+template <bool FAST, typename T, typename W>
 void choose(const GateArgs &a, int parts, double gamma, hipStream_t s) {
-    if (a.score == MOE_SCORE_SOFTMAX) choose_score<F, MOE_SCORE_SOFTMAX>(a, parts, gamma, s);
-    else if (a.score == MOE_SCORE_SIGMOID) choose_score<F, MOE_SCORE_SIGMOID>(a, parts, gamma, s);
-    else choose_score<F, MOE_SCORE_SQRT_SOFTPLUS>(a, parts, gamma, s);
+    if (a.score == MOE_SCORE_SOFTMAX) choose_score<FAST, T, W, MOE_SCORE_SOFTMAX>(a, parts, gamma, s);
+    else if (a.score == MOE_SCORE_SIGMOID) choose_score<FAST, T, W, MOE_SCORE_SIGMOID>(a, parts, gamma, s);
+    else choose_score<FAST, T, W, MOE_SCORE_SQRT_SOFTPLUS>(a, parts, gamma, s);
 }
 
 // Parts of H: two workgroups per CU where that takes no more than kMaxSplit
@@ -712,19 +760,29 @@ hipError_t launch(const GateArgs &a, hipStream_t s) {
     GateArgs g = a;
     g.x_norms = reinterpret_cast<float *>(a.logits + static_cast<size_t>(p.parts) * a.T * a.E);
     g.w_norms = g.x_norms + static_cast<size_t>(p.parts) * a.T;
+    // whether the logits are bounded fp32 sums
+    const bool fast = p.few || kPlanes<T, W> == 1 ? kFast<T, W>
+                                                  : kPlanes<T, W> > 1 && static_cast<int64_t>(a.T) * a.E * a.H > kPlanesFrom;
     if (p.few) {
         hipLaunchKernelGGL((logits_few_kernel<T, W>), dim3(p.e_tiles, p.parts), dim3(kBlock), 0, s, g,
                            p.chunks_per_part);
     } else {
         const int units = p.t_tiles * p.parts;
-        hipLaunchKernelGGL((logits_many_kernel<T, W>), dim3((units + 7) / 8 * 8 * p.e_tiles), dim3(kBlock), 0, s, g,
-                           p.chunks_per_part, p.e_tiles, units);
+        const dim3 grid((units + 7) / 8 * 8 * p.e_tiles);
+        if (fast)
+            hipLaunchKernelGGL((logits_many_kernel<T, W, kPlanes<T, W>>), grid, dim3(kBlock), 0, s, g,
+                               p.chunks_per_part, p.e_tiles, units);
+        else if constexpr (!kFast<T, W>)
+            hipLaunchKernelGGL((logits_many_kernel<T, W, 0>), grid, dim3(kBlock), 0, s, g, p.chunks_per_part,
+                               p.e_tiles, units);
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const double gamma = kStep * (p.few ? 1 : kFold) * kUnit;
-    if constexpr (kFast<T, W>) choose<T>(g, p.parts, gamma, s);
-    else choose<void>(g, p.parts, gamma, s);
+    if constexpr (kPlanes<T, W> > 0) {
+        if (fast) choose<true, T, W>(g, p.parts, gamma, s);
+    }
+    if (!fast) choose<false, float, float>(g, p.parts, gamma, s);
     return hipGetLastError();
 }
 

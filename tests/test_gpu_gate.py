@@ -4,7 +4,8 @@ Ids are equal: the inputs are random, so two choice values lie within the
 1e-14 that a 64-bit sum may be off only by design (equal rows, checked for the
 lowest id).
 
-Weights. Types that are not both bf16 or both fp16: everything before the
+Weights. Types that are not both bf16, both fp16, or bf16 x and fp32 weights:
+everything before the
 rounding to fp32 is in 64 bits, so 2^-24 relative, and 1e-10 for the sums and
 exp. Both 16-bit: a logit is a sum of fp32 sums of 128 exact products, each
 addition off by at most 2^-23 of the magnitudes so far, so off by at most
@@ -62,7 +63,7 @@ def check(got, want, x, w):
     assert torch.equal(got[0].long(), want[0])
     err = (got[1].double() - want[1]).abs()
     tol = torch.full((x.shape[0], 1), 2.0 ** -24 + 1e-10, dtype=torch.float64)
-    if x.dtype == w.dtype and x.dtype != F32:
+    if (x.dtype == w.dtype and x.dtype != F32) or (x.dtype == BF and w.dtype == F32):
         tol += 4 * 2.0 ** -16 * (x.double().abs() @ w.double().abs().t()).amax(1, keepdim=True)
     assert bool((err <= tol * want[1].abs() + 1e-45).all())
     assert float(err.norm()) <= 4e-6 * float(want[1].norm())
@@ -145,6 +146,47 @@ def test_close_logits_are_told_apart(T, bias, dt, score, keep):
     if b is None:
         assert bool(same.all())
     check((want.int(), sc), (want, v), x, w)
+
+
+@pytest.mark.parametrize("T", [7, 150, 3000])
+@pytest.mark.parametrize("dt,wdt", [(BF, BF), (FP, FP), (BF, F32)], ids=["bf16", "fp16", "bf16-fp32"])
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID, SQRTSP])
+def test_large_biases(T, dt, wdt, score):
+    """score + bias is rounded at the bias' size: 64-bit values that tie there go to the lowest id."""
+    x, w, b = make(T, 1500, 130, dt, wdt, bias=True, seed=5)
+    for size in (1e3, 1e6):
+        bb = (torch.randint(0, 3, (130,)).float() + 1) * size
+        bb[7] = -float("inf")
+        check(run(x, w, bb, 8, score), formula(x, w, bb, 8, score, True, 1.0), x, w)
+
+
+@pytest.mark.parametrize("T", [7, 150])
+def test_subnormal_and_tiny_inputs(T):
+    x, w, _ = make(T, 1024, 64, FP, FP, seed=6)
+    x = (x.float() * 2.0 ** -20).to(FP)  # fp16 subnormals
+    assert 0 < float(x.abs().max()) < torch.finfo(FP).smallest_normal
+    check(run(x, w, None, 6), formula(x, w, None, 6, SOFTMAX, True, 1.0), x, w)
+    x, w, _ = make(T, 1024, 64, BF, F32, seed=7)
+    x = x.repeat(1 + 60 * (T > 100), 8)
+    w = torch.cat([w.roll(i, 1) for i in range(8)], 1)  # 9150 x 64 x 8192 products: the split
+    check(run(x, (w * 2.0 ** -60), None, 6), formula(x, w * 2.0 ** -60, None, 6, SOFTMAX, True, 1.0), x, w * 2.0 ** -60)
+    check(run((x.float() * 2.0 ** -50).to(BF), w, None, 6), formula((x.float() * 2.0 ** -50).to(BF), w, None, 6, SOFTMAX, True, 1.0), x, w)
+
+
+@pytest.mark.parametrize("T", [60, 2900])
+@pytest.mark.parametrize("bias", [False, True], ids=["logit", "bias"])
+def test_fp32_weights_to_their_last_bit(T, bias):
+    """bf16 x and fp32 weights whose rows differ in one last bit of 24: every part of the split counts."""
+    x, w, b = make(T, 2048, 96, BF, F32, bias=bias, seed=21)
+    for e in range(0, 96, 2):
+        w[e + 1] = w[e]
+        k = 5 * e + 3
+        w[e + 1, k] = torch.nextafter(w[e, k], torch.tensor(9.0))
+        if bias:
+            b[e + 1] = b[e]
+    l = x.double() @ w.double().t()
+    assert float((l[:, 0::2] - l[:, 1::2]).abs().min()) > 0
+    check(run(x, w, b, 10, SIGMOID), formula(x, w, b, 10, SIGMOID, True, 1.0), x, w)
 
 
 def test_choice_between_values_that_fp32_sums_cannot_tell_apart():
