@@ -641,16 +641,25 @@ hipError_t launch_few(const LinearW4Args &a, hipStream_t s) {
 //   T 256, N 4096: 34 / 34      T 300, N 4096: 40 / 34    T 512, N 8192: 129 / 53
 // so it goes by 16-row tiles x 64-token tiles. (int8 x: 26 / 41 at T 256, 23 /
 // 24 at T 300; groups of 32: 52 / 43 at T 300.)
-// Two row tiles per workgroup halve what x costs, where there are enough of
-// them: T 16, N 28672, K 8192 46 -> 38 us; N 4096 would fill half the chip.
+// Two row tiles per workgroup halve what x costs, and four halve it again,
+// where there are enough of them and registers hold their scales: T 16, N
+// 28672, K 8192, one / two / four 46 / 39 / 33 us; T 64, N 8192, K 4096, int8
+// x, one / two 12 / 9.5 (bf16 19 / 25). N 4096 would fill half the chip.
 template <int X, int G, bool Z>
 hipError_t launch_tokens(const LinearW4Args &a, hipStream_t s) {
-    const bool wide = a.n_tiles >= 512;
+    const bool wide = G != 32 && a.n_tiles >= 512;
     if (a.T > 32 && a.n_tiles * static_cast<int64_t>((a.T + 63) / 64) > 1024) return launch_many<X, G, Z>(a, s);
-    if (a.T <= 4) return wide ? launch_few<X, G, Z, 4, 2, 8>(a, s) : launch_few<X, G, Z, 4, 1, 8>(a, s);
-    if (a.T <= 8) return wide ? launch_few<X, G, Z, 8, 2, 8>(a, s) : launch_few<X, G, Z, 8, 1, 8>(a, s);
-    if (a.T <= 16) return wide ? launch_few<X, G, Z, 16, 2, 8>(a, s) : launch_few<X, G, Z, 16, 1, 8>(a, s);
-    if (a.T <= 32) return wide ? launch_few<X, G, Z, 32, 2, 8>(a, s) : launch_few<X, G, Z, 32, 1, 8>(a, s);
+    constexpr int kTwo = G != 32 ? 2 : 1;
+    if (a.T <= 4) return wide ? launch_few<X, G, Z, 4, kTwo, 8>(a, s) : launch_few<X, G, Z, 4, 1, 8>(a, s);
+    if (a.T <= 8) return wide ? launch_few<X, G, Z, 8, kTwo, 8>(a, s) : launch_few<X, G, Z, 8, 1, 8>(a, s);
+    if constexpr (G == 128 && !(X == 1 && Z)) {
+        if (a.T <= 16 && a.n_tiles >= 1024) return launch_few<X, G, Z, 16, 4, 8>(a, s);
+    }
+    if (a.T <= 16) return wide ? launch_few<X, G, Z, 16, kTwo, 8>(a, s) : launch_few<X, G, Z, 16, 1, 8>(a, s);
+    if (a.T <= 32) return wide ? launch_few<X, G, Z, 32, kTwo, 8>(a, s) : launch_few<X, G, Z, 32, 1, 8>(a, s);
+    if constexpr (X == 2 && G != 32) {
+        if (wide) return a.T <= 48 ? launch_few<X, G, Z, 48, 2, 8>(a, s) : launch_few<X, G, Z, 64, 2, 8>(a, s);
+    }
     if (a.T <= 48) return launch_few<X, G, Z, 48, 1, 4>(a, s);
     return launch_few<X, G, Z, 64, 1, 4>(a, s);
 }

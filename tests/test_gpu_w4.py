@@ -102,7 +102,10 @@ SHAPES = [(1, 1, 32, 32), (1, 16, 128, 128), (2, 17, 64, 64), (3, 33, 96, 32), (
           (515, 272, 192, 32), (1, 8, 16384, 128), (4, 12000, 256, 64),
           # over 1024 pairs of 16 rows and 64 tokens: the kernel for many tokens; one, two, three k tiles and more
           (33, 16500, 128, 128), (1030, 1100, 96, 32), (65, 8300, 320, 64), (600, 1999, 1152, 128), (515, 2320, 160, 32),
-          (128, 8208, 256, 128), (700, 1600, 1088, 64), (64, 16400, 544, 32)]
+          (128, 8208, 256, 128), (700, 1600, 1088, 64), (64, 16400, 544, 32),
+          # two and four row tiles per workgroup, their last ones past the end
+          (3, 8200, 256, 128), (6, 8210, 320, 32), (12, 8200, 320, 64), (12, 16400, 1280, 128), (30, 8201, 256, 128),
+          (40, 8200, 384, 128), (60, 8205, 320, 64)]
 
 
 @pytest.mark.parametrize("T,N,K,G", SHAPES)
