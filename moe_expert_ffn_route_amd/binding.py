@@ -297,9 +297,26 @@ def moe_w8a8_forward_quantized(dims: Dims, q_x, x_scale, expert_ids, expert_scal
                                workspace_bytes: Optional[int] = None, dbg: Optional[Debug] = None, stream=None,
                                check: bool = True) -> int:
     """moe_w8a8_forward on codes and scales that moe_w8a8_norm_quant (or the
-    caller) made of x: q_x [T, H] int8 or float8_e4m3fn, x_scale fp32 [T] or
-    [T, H / quant_group]. Returns the status code; raises MoeError on failure
-    when check=True."""
+    caller) made of x: q_x [T, H] int8 (float8_e4m3fn for FP4 weights), x_scale
+    fp32 [T] or [T, H / quant_group]. Runs on q_x's device. Returns the status
+    code; raises MoeError on failure when check=True."""
+    T, H = dims.num_tokens, dims.hidden
+    if isinstance(q_x, torch.Tensor):
+        want = torch.float8_e4m3fn if dims.weight_format == MOE_WEIGHT_MXFP4 else torch.int8
+        if q_x.numel() != T * H or q_x.dtype not in (want, torch.uint8, torch.int8):
+            raise ValueError(f"q_x: expected {T * H} codes of {want}, got {tuple(q_x.shape)} of {q_x.dtype}")
+        if q_x.is_cuda and q_x.get_device() != torch.cuda.current_device():
+            with torch.cuda.device(q_x.get_device()):
+                return moe_w8a8_forward_quantized(
+                    dims, q_x, x_scale, expert_ids, expert_scales, gmm1_weight, gmm1_weight_scale, gmm2_weight,
+                    gmm2_weight_scale, share_gmm1_weight, share_gmm1_weight_scale, share_gmm2_weight,
+                    share_gmm2_weight_scale, x_active_mask, output, share_output, expert_token_nums, workspace,
+                    workspace_bytes, dbg, stream, check)
+    if isinstance(x_scale, torch.Tensor):
+        n = T * (H // dims.quant_group if dims.quant_mode == 2 and dims.quant_group > 0 else 1)
+        if x_scale.dtype is not torch.float32 or x_scale.numel() != n:
+            raise ValueError(f"x_scale: expected {n} elements of torch.float32, got {tuple(x_scale.shape)} of "
+                             f"{x_scale.dtype}")
     if workspace_bytes is None:
         workspace_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     args = [q_x, x_scale, expert_ids, expert_scales, gmm1_weight, gmm1_weight_scale, gmm2_weight, gmm2_weight_scale,
@@ -339,6 +356,18 @@ def _call(where: str, fn, device: int, stream, *args) -> None:
     rc = fn(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream))
     if rc != MOE_OK:
         raise MoeError(rc, where)
+
+
+def _empty(shape, dtype, device, stream):
+    """A tensor that the call allocates: from the pool of the stream that the
+    call runs on, so that memory freed after the call is not handed to another
+    stream while the kernels still use it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _code(dt) -> int:
@@ -390,11 +419,11 @@ def moe_w8a8_gate(dims: GateDims, x, weight, bias=None, expert_ids=None, expert_
     T, H, E, K = dims.num_tokens, dims.hidden, dims.moe_expert_num, dims.topk
     dev = x.get_device()
     if expert_ids is None:
-        expert_ids = torch.empty((T, K), dtype=torch.int32, device=x.device)
+        expert_ids = _empty((T, K), torch.int32, x.device, stream)
     if expert_scales is None:
-        expert_scales = torch.empty((T, K), dtype=torch.float32, device=x.device)
+        expert_scales = _empty((T, K), torch.float32, x.device, stream)
     if workspace is None:
-        workspace = torch.empty(max(256, moe_w8a8_gate_workspace_size(dims)), dtype=torch.uint8, device=x.device)
+        workspace = _empty(max(256, moe_w8a8_gate_workspace_size(dims)), torch.uint8, x.device, stream)
     n_ws = workspace.numel()
     _call("moe_w8a8_gate", library().moe_w8a8_gate, dev, stream, ctypes.byref(dims),
           _arg(x, "x", _DTYPE_OF.get(dims.dtype), T * H, dev),
@@ -424,7 +453,7 @@ def moe_w8a8_pack_weights_w4(dims: LinearW4Dims, codes, scale, zero=None, dst=No
     (num_tokens aside). Returns dst (uint8, allocated if None)."""
     nbytes, dev = moe_w8a8_packed_w4_bytes(dims), codes.get_device()
     if dst is None:
-        dst = torch.empty(nbytes, dtype=torch.uint8, device=codes.device)
+        dst = _empty(nbytes, torch.uint8, codes.device, stream)
     N, K = dims.out_features, dims.in_features
     groups = N * (K // dims.group)
     _call("moe_w8a8_pack_weights_w4", library().moe_w8a8_pack_weights_w4, dev, stream, ctypes.byref(dims),
@@ -442,7 +471,7 @@ def moe_w8a8_linear_w4(dims: LinearW4Dims, x, weight, x_scale=None, bias=None, o
     dt = torch.float16 if dims.act_dtype == MOE_DTYPE_FP16 else torch.bfloat16
     dev = x.get_device()
     if out is None:
-        out = torch.empty((T, width), dtype=dt, device=x.device)
+        out = _empty((T, width), dt, x.device, stream)
     _call("moe_w8a8_linear_w4", library().moe_w8a8_linear_w4, dev, stream, ctypes.byref(dims),
           _arg(x, "x", _DTYPE_OF.get(dims.act_dtype), T * K, dev),
           _arg(x_scale, "x_scale", torch.float32, T, dev),

@@ -243,6 +243,35 @@ def test_two_layers_at_once_on_two_streams():
             assert torch.equal(got.view(torch.uint8), x.view(torch.uint8))
 
 
+def test_buffers_that_a_call_allocates_belong_to_its_stream():
+    """On a stream of their own, with the current stream taking and filling
+    memory as fast as it can: a workspace freed to the wrong pool would be
+    overwritten under the kernels."""
+    g = torch.Generator().manual_seed(12)
+    x, w = torch.randn(700, 2048, generator=g).to(BF).cuda(), torch.randn(128, 2048, generator=g).to(BF).cuda()
+    d = moe.make_gate_dims(700, 2048, 128, 6)
+    want = moe.moe_w8a8_gate(d, x, w)
+    n = moe.moe_w8a8_gate_workspace_size(d)
+    torch.cuda.synchronize()
+    for stream in (torch.cuda.Stream(), torch.cuda.Stream().cuda_stream):
+        for _ in range(10):
+            ids, sc = moe.moe_w8a8_gate(d, x, w, stream=stream)
+            junk = [torch.empty(n, dtype=torch.uint8, device="cuda").fill_(0xFF) for _ in range(3)]
+            torch.cuda.synchronize()
+            assert torch.equal(ids, want[0]) and torch.equal(sc, want[1])
+            del junk
+    ld = moe.make_linear_w4_dims(5, 64, 256)
+    codes = torch.randint(0, 256, (64, 128), dtype=torch.uint8, generator=g).cuda()
+    scale = torch.rand(64, 2, generator=g).cuda()
+    x5 = torch.randn(5, 256, generator=g).to(BF).cuda()
+    ref = moe.moe_w8a8_linear_w4(ld, x5, moe.moe_w8a8_pack_weights_w4(ld, codes, scale))
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    out = moe.moe_w8a8_linear_w4(ld, x5, moe.moe_w8a8_pack_weights_w4(ld, codes, scale, stream=st), stream=st)
+    st.synchronize()
+    assert torch.equal(out, ref)
+
+
 def test_binding_refuses_tensors_that_do_not_fit():
     x = torch.zeros(4, 64, dtype=BF, device="cuda")
     d = moe.make_norm_dims(4, 64, quant=moe.MOE_QUANT_NONE)
@@ -267,3 +296,13 @@ def test_binding_refuses_tensors_that_do_not_fit():
         ld8 = moe.make_linear_w4_dims(4, 32, 64, group=64, act_dtype=torch.int8)
         w = torch.zeros(moe.moe_w8a8_packed_w4_bytes(ld8), dtype=torch.uint8, device="cuda")
         moe.moe_w8a8_linear_w4(ld8, x.to(torch.int8), w, x_scale=torch.ones(3, device="cuda"))
+    bd = moe.make_dims(num_tokens=4, hidden=512, inter=256, topk=2, moe_expert_num=8)
+    q, s = torch.zeros(4, 512, dtype=torch.int8, device="cuda"), torch.ones(4, device="cuda")
+    with ERR(ValueError, match="q_x: expected"):
+        moe.moe_w8a8_forward_quantized(bd, q[:3], s, *[None] * 6)
+    with ERR(ValueError, match="q_x: expected"):
+        moe.moe_w8a8_forward_quantized(bd, q.to(BF), s, *[None] * 6)
+    with ERR(ValueError, match="x_scale: expected"):
+        moe.moe_w8a8_forward_quantized(bd, q, s[:3], *[None] * 6)
+    with ERR(moe.MoeError):
+        moe.moe_w8a8_forward_quantized(bd, q, s, *[None] * 6)
