@@ -1,4 +1,5 @@
-"""MI355X (gfx950) fused W8A8 MoE expert block.
+"""MI355X (gfx950) fused W8A8 MoE expert block, and the pre-norm, router and
+4-bit dense products around it.
 
 The compute lives in libmoe_w8a8.so (hand-written HIP kernels behind the C ABI
 of include/moe_w8a8.h); `binding` is its ctypes front end and `synth` draws
