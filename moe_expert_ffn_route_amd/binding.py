@@ -34,8 +34,6 @@ MOE_QUANT_NONE, MOE_QUANT_INT8, MOE_QUANT_E4M3 = 0, 1, 2
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID, MOE_SCORE_SQRT_SOFTPLUS = 0, 1, 2
 _DTYPE_CODE = {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_FP16, torch.float32: MOE_DTYPE_FP32,
                torch.int8: MOE_DTYPE_INT8}
-_DTYPE_OF = {code: dt for dt, code in _DTYPE_CODE.items()}
-_QUANT_DTYPE = {MOE_QUANT_INT8: torch.int8, MOE_QUANT_E4M3: torch.float8_e4m3fn}
 
 
 class MoeError(RuntimeError):
@@ -332,30 +330,50 @@ def moe_w8a8_forward_quantized(dims: Dims, q_x, x_scale, expert_ids, expert_scal
 # ------------------------------------------- operators around the block
 # These take tensors only, and check their types, sizes and device: a call
 # whose tensors do not fit its dims raises ValueError before the library sees
-# it. They run on the tensors' device, whichever device is current.
+# it. They run on the tensors' device, whichever device is current. The checks
+# and the call are in csrc/pycall.cpp.
+
+_pycall = None
+
+
+def _native():
+    """The compiled argument checks (raises if they have not been built)."""
+    global _pycall
+    if _pycall is None:
+        library()
+        from . import _pycall as module
+        _pycall = module
+    return _pycall
+
+
+def _call(where: str, fn, first, stream, *args) -> None:
+    """fn(*args, stream handle) with the device of tensor `first` current; the
+    stream defaults to that device's current one (its handle: the stream
+    object costs a microsecond)."""
+    device = first.get_device()
+    if device < 0:  # refused by fn
+        handle = 0
+    elif device != torch._C._cuda_getDevice():
+        with torch.cuda.device(device):
+            return _call(where, fn, first, stream, *args)
+    else:
+        handle = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+    rc = fn(*args, handle)
+    if rc != MOE_OK:
+        raise MoeError(rc, where)
+
 
 def _arg(t, name: str, dtype, numel: int, device: int) -> Optional[int]:
     """The device pointer of an argument of `numel` elements (None: NULL)."""
     if t is None:
         return None
-    if t.dtype is dtype and t.numel() == numel and t.get_device() == device >= 0 and t.is_contiguous():
-        return t.data_ptr()
     if t.dtype is not dtype or t.numel() != numel:
         raise ValueError(f"{name}: expected {numel} elements of {dtype}, got {tuple(t.shape)} of {t.dtype}")
     if t.get_device() != device or device < 0:
         raise ValueError(f"{name}: expected a tensor on the GPU that holds the call's first tensor")
-    raise ValueError(f"{name}: tensors passed to libmoe_w8a8 must be contiguous")
-
-
-def _call(where: str, fn, device: int, stream, *args) -> None:
-    """fn(*args, stream) with `device` current; the stream defaults to that
-    device's current one (its handle: the stream object costs a microsecond)."""
-    if torch.cuda.current_device() != device:
-        with torch.cuda.device(device):
-            return _call(where, fn, device, stream, *args)
-    rc = fn(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream))
-    if rc != MOE_OK:
-        raise MoeError(rc, where)
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensors passed to libmoe_w8a8 must be contiguous")
+    return t.data_ptr()
 
 
 def _empty(shape, dtype, device, stream):
@@ -387,14 +405,8 @@ def moe_w8a8_norm_quant(dims: NormDims, x, weight=None, residual=None, residual_
     """Residual addition, RMS norm and 8-bit quantisation of x [T, H] in one
     pass; writes those of residual_out, y, q and q_scale that are given (see
     the header). residual_out and y may be x or residual themselves."""
-    T, H, g = dims.num_tokens, dims.hidden, dims.quant_group
-    dt, n, dev = _DTYPE_OF.get(dims.dtype), dims.num_tokens * dims.hidden, x.get_device()
-    _call("moe_w8a8_norm_quant", library().moe_w8a8_norm_quant, dev, stream, ctypes.byref(dims),
-          _arg(x, "x", dt, n, dev), _arg(residual, "residual", dt, n, dev),
-          _arg(weight, "weight", _DTYPE_OF.get(dims.weight_dtype), H, dev),
-          _arg(residual_out, "residual_out", dt, n, dev), _arg(y, "y", dt, n, dev),
-          _arg(q, "q", _QUANT_DTYPE.get(dims.quant), n, dev),
-          _arg(q_scale, "q_scale", torch.float32, T * (H // g) if g > 0 else T, dev))
+    _call("moe_w8a8_norm_quant", _native().norm_quant, x, stream, dims, x, residual, weight, residual_out, y, q,
+          q_scale)
 
 
 def make_gate_dims(num_tokens, hidden, moe_expert_num, topk, score=MOE_SCORE_SOFTMAX, normalize=True,
@@ -416,21 +428,14 @@ def moe_w8a8_gate(dims: GateDims, x, weight, bias=None, expert_ids=None, expert_
     """Router: top-k experts of x [T, H] and their weights. Returns
     (expert_ids int32 [T, K], expert_scales fp32 [T, K]), allocated if None,
     as is the workspace."""
-    T, H, E, K = dims.num_tokens, dims.hidden, dims.moe_expert_num, dims.topk
-    dev = x.get_device()
     if expert_ids is None:
-        expert_ids = _empty((T, K), torch.int32, x.device, stream)
+        expert_ids = _empty((dims.num_tokens, dims.topk), torch.int32, x.device, stream)
     if expert_scales is None:
-        expert_scales = _empty((T, K), torch.float32, x.device, stream)
+        expert_scales = _empty((dims.num_tokens, dims.topk), torch.float32, x.device, stream)
     if workspace is None:
         workspace = _empty(max(256, moe_w8a8_gate_workspace_size(dims)), torch.uint8, x.device, stream)
-    n_ws = workspace.numel()
-    _call("moe_w8a8_gate", library().moe_w8a8_gate, dev, stream, ctypes.byref(dims),
-          _arg(x, "x", _DTYPE_OF.get(dims.dtype), T * H, dev),
-          _arg(weight, "weight", _DTYPE_OF.get(dims.weight_dtype), E * H, dev),
-          _arg(bias, "bias", torch.float32, E, dev), _arg(expert_ids, "expert_ids", torch.int32, T * K, dev),
-          _arg(expert_scales, "expert_scales", torch.float32, T * K, dev),
-          _arg(workspace, "workspace", torch.uint8, n_ws, dev), n_ws)
+    _call("moe_w8a8_gate", _native().gate, x, stream, dims, x, weight, bias, expert_ids, expert_scales, workspace,
+          workspace.numel())
     return expert_ids, expert_scales
 
 
@@ -456,7 +461,7 @@ def moe_w8a8_pack_weights_w4(dims: LinearW4Dims, codes, scale, zero=None, dst=No
         dst = _empty(nbytes, torch.uint8, codes.device, stream)
     N, K = dims.out_features, dims.in_features
     groups = N * (K // dims.group)
-    _call("moe_w8a8_pack_weights_w4", library().moe_w8a8_pack_weights_w4, dev, stream, ctypes.byref(dims),
+    _call("moe_w8a8_pack_weights_w4", library().moe_w8a8_pack_weights_w4, codes, stream, ctypes.byref(dims),
           _arg(codes, "codes", torch.uint8, N * (K // 2), dev), _arg(scale, "scale", torch.float32, groups, dev),
           _arg(zero, "zero", torch.uint8, groups, dev), _arg(dst, "dst", torch.uint8, nbytes, dev))
     return dst
@@ -466,17 +471,11 @@ def moe_w8a8_linear_w4(dims: LinearW4Dims, x, weight, x_scale=None, bias=None, o
     """Dense product of x [T, K] (bf16, fp16, or int8 with x_scale fp32 [T])
     with packed 4-bit weights. Returns out (bf16, fp16 for fp16 x; [T, N], or
     [T, N/2] when gated), allocated if None."""
-    T, N, K = dims.num_tokens, dims.out_features, dims.in_features
-    width = N // 2 if dims.gated else N
-    dt = torch.float16 if dims.act_dtype == MOE_DTYPE_FP16 else torch.bfloat16
-    dev = x.get_device()
     if out is None:
-        out = _empty((T, width), dt, x.device, stream)
-    _call("moe_w8a8_linear_w4", library().moe_w8a8_linear_w4, dev, stream, ctypes.byref(dims),
-          _arg(x, "x", _DTYPE_OF.get(dims.act_dtype), T * K, dev),
-          _arg(x_scale, "x_scale", torch.float32, T, dev),
-          _arg(weight, "weight", torch.uint8, moe_w8a8_packed_w4_bytes(dims), dev),
-          _arg(bias, "bias", torch.float32, N, dev), _arg(out, "out", dt, T * width, dev))
+        width = dims.out_features // 2 if dims.gated else dims.out_features
+        out = _empty((dims.num_tokens, width), torch.float16 if dims.act_dtype == MOE_DTYPE_FP16 else torch.bfloat16,
+                     x.device, stream)
+    _call("moe_w8a8_linear_w4", _native().linear_w4, x, stream, dims, x, x_scale, weight, bias, out)
     return out
 
 

@@ -1,5 +1,6 @@
 """Build libmoe_w8a8.so (gfx950) in-tree with hipcc (one compile per source,
-in parallel, then a link).
+in parallel, then a link), and _pycall.so, the Python entry of the operators
+around the block (host code, against the installed torch).
 
     python -m moe_expert_ffn_route_amd.build
 
@@ -19,6 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmoe_w8a8.so")
 SOURCES = ["abi.hip", "route.hip", "quant.hip", "gemm.hip", "gemm_wide.hip", "gemm_tall.hip", "gemm_mx.hip", "combine.hip",
            "pack.hip", "warm.hip", "abi_ops.hip", "norm.hip", "gate.hip", "linear_w4.hip"]
+PYCALL = os.path.join(PKG, "_pycall.so")
 ARCH = os.environ.get("MOE_OFFLOAD_ARCH", "gfx950")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -27,13 +29,28 @@ FLAGS = ["-O3", "-std=c++17", "-fPIC", "-shared", f"--offload-arch={ARCH}", "-ff
          "-fvisibility=hidden", "-I", os.path.join(ROOT, "include"), "-I", CSRC]
 
 
+def _pycall_cmd(out):
+    """g++ on csrc/pycall.cpp: links the library beside it and torch's, which
+    the process has loaded when the module is imported."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    inc = [f for d in (*cpp_extension.include_paths(), sysconfig.get_paths()["include"]) for f in ("-isystem", d)]
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc,
+            os.path.join(CSRC, "pycall.cpp"), "-o", out, "-L", PKG, "-l:libmoe_w8a8.so", "-L", lib, "-ltorch_python",
+            "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN", "-Wl,--allow-shlib-undefined"]
+
+
 def _run(cmd, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     errs = "\n".join(l for l in r.stderr.splitlines() if "packed-fp32-ops" not in l)
     if r.returncode != 0:
-        raise RuntimeError(f"hipcc failed ({r.returncode}):\n{errs}")
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed ({r.returncode}):\n{errs}")
     if errs.strip() and verbose:
         print(errs, file=sys.stderr)
 
@@ -57,6 +74,9 @@ def build(verbose: bool = False, jobs: int = 0) -> str:
         tmp = LIB + f".tmp{os.getpid()}"
         _run([HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", *objs, "-o", tmp], verbose)
         os.replace(tmp, LIB)
+        tmp = PYCALL + f".tmp{os.getpid()}"
+        _run(_pycall_cmd(tmp), verbose)
+        os.replace(tmp, PYCALL)
     finally:
         shutil.rmtree(obj_dir, ignore_errors=True)
     return LIB

@@ -259,7 +259,6 @@ __global__ __launch_bounds__(kBlock) void logits_few_kernel(GateArgs a, int chun
             }
         }
     };
-#pragma unroll 2
     for (int c = part * chunks_per_part + wave; c < c_end; c += kSlices) {
         if ((c + 1) * kChunk <= a.H) chunk(std::true_type{}, c);
         else chunk(std::false_type{}, c);
