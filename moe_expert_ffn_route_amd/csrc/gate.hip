@@ -44,9 +44,11 @@ constexpr int kMaxSplit = 8;
 // truncates): n * 2^-23 of the sum of magnitudes, which Cauchy's inequality
 // bounds by the norms.
 constexpr double kUnit = 0x1p-23;
-// Inputs and products under the smallest normal fp32 may be dropped: 16384 of
-// them, the other factor up to 2^20.
-constexpr double kTiny = 0x1p-90;
+// Numbers under the smallest normal fp32 may be dropped. Products: at most
+// 16384 of them. Squares: the norms' (8192 sums of two at a time) may lack as
+// much, which also covers inputs that are dropped: 2^-126 of each is under
+// kUnit * 2^-56.
+constexpr double kTiny = 0x1p-112, kTinySquares = 0x1p-112;
 
 // Eight elements from h = k of a row of H. WHOLE: they are known to be there
 // (no branch, so that loads can be issued in a row).
@@ -511,6 +513,18 @@ __device__ __forceinline__ void exact_logits(const GateArgs &a, int t, int e0, i
     l1 = wave_sum(s1);
 }
 
+template <typename T>
+__device__ __forceinline__ bool row_is_zero(const GateArgs &a, const T *x, int lane) {
+    uint32_t any = 0;
+    for (int k = lane * kVec; k < a.H; k += kWave * kVec) {
+        T u[kVec];
+        load8<false>(x, k, a.H, u);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) any |= u[e].bits & 0x7FFFu;
+    }
+    return __ballot(any != 0) == 0;
+}
+
 // Score of a logit (softmax: before the division by the sum; m = the largest
 // logit).
 template <int SCORE>
@@ -588,7 +602,7 @@ __global__ __launch_bounds__(kBlock) void choose_kernel(GateArgs a, int parts, d
 #pragma unroll
         for (int j = 0; j < NPL; ++j) wn = n[j] <= wn ? wn : n[j];
         wn = __uint_as_float(wave_max_int<uint32_t>(__float_as_uint(wn), 0u));
-        off = 2.0 * (gamma * 1.05 * sqrt(static_cast<double>(xn) * static_cast<double>(wn)) + kTiny);
+        off = 2.0 * (gamma * 1.05 * sqrt((xn + kTinySquares) * (wn + kTinySquares)) + kTiny);
         if (a.bias) off *= SCORE == MOE_SCORE_SOFTMAX ? 2.5 : SCORE == MOE_SCORE_SIGMOID ? 0.25 : 0.34;
         // and the 64-bit roundings of score + bias
         float bm = 1.0f;
@@ -596,6 +610,10 @@ __global__ __launch_bounds__(kBlock) void choose_kernel(GateArgs a, int parts, d
         for (int j = 0; j < NPL; ++j) bm = a.bias && fabsf(bias[j]) < __builtin_inff() ? fmaxf(bm, fabsf(bias[j])) : bm;
         bm = __uint_as_float(wave_max_int<uint32_t>(__float_as_uint(bm), 0u));
         off += 0x1p-50 * static_cast<double>(bm);
+        // A row of zeros (a padded batch): its logits are 0, all of them equal
+        // and right. Without this 243 us instead of 10 for two such rows of 8.
+        if (xn == 0.0f && row_is_zero(a, static_cast<const T *>(a.x) + static_cast<size_t>(t) * a.H, lane))
+            off = -__builtin_inf();
     }
     double s[NPL], total;  // scores (softmax: undivided, `total` their sum)
     int id_mine;           // lane k keeps the k-th choice

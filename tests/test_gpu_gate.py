@@ -7,7 +7,7 @@ lowest id).
 Weights. Types that are not both bf16, both fp16, or bf16 x and fp32 weights:
 everything before the
 rounding to fp32 is in 64 bits, so 2^-24 relative, and 1e-10 for the sums and
-exp. Both 16-bit: a logit is a sum of fp32 sums of 128 exact products, each
+exp. Both 16-bit: a logit is a sum of fp32 sums of at most 128 exact products, each
 addition off by at most 2^-23 of the magnitudes so far, so off by at most
 B = 128 * 2^-23 * sum |x w|. A score moves by at most B relative (softmax 2 B,
 with its sum), the sum of the chosen ones by as much: 4 B, and 2^-24.
@@ -173,6 +173,39 @@ def test_subnormal_and_tiny_inputs(T):
     check(run((x.float() * 2.0 ** -50).to(BF), w, None, 6), formula((x.float() * 2.0 ** -50).to(BF), w, None, 6, SOFTMAX, True, 1.0), x, w)
 
 
+@pytest.mark.parametrize("T", [7, 150])
+@pytest.mark.parametrize("dt,wdt,xs,ws", [(BF, BF, -82, 60), (BF, BF, 56, -76), (FP, FP, -20, 4), (BF, F32, -82, 60)],
+                         ids=["bf16-x", "bf16-w", "fp16", "fp32-w"])
+def test_close_logits_of_inputs_whose_squares_vanish(T, dt, wdt, xs, ws):
+    """Pairs of experts with the same products in another order, and one small
+    element's last bit more: fp32 sums order them by their roundings. The
+    elements are fp16 subnormals, or so small that their squares are not even
+    fp32 subnormals: the bound still has to see them."""
+    g = torch.Generator().manual_seed(23 + T)
+    x, w, _ = make(T, 2048, 96, dt, wdt, seed=23)
+    x, w = (x.float() * 2.0 ** xs).to(dt), (w.float() * 2.0 ** ws).to(wdt)
+    x[x == 0] = 2.0 ** (xs - 4)  # a zero would tie
+    x = x[:, :16].repeat(1 if wdt == dt else 1 + 2900 // T, 128)  # fp32 w: products enough for the split
+    for e in range(0, 96, 2):
+        w[e, 5] *= {BF: 2.0 ** -14, FP: 2.0 ** -7, F32: 1.0}[wdt]
+        w[e + 1] = w[e].view(128, 16)[torch.randperm(128, generator=g)].view(-1)
+        w[e, 5] *= 1 + {BF: 2.0 ** -7, FP: 2.0 ** -10, F32: 2.0 ** -23}[wdt]
+    want, v = formula(x, w, None, 9, SIGMOID, True, 1.0)
+    check(run(x, w, None, 9, SIGMOID), (want, v), x, w)
+
+
+@pytest.mark.parametrize("T", [9, 130, 3000])
+@pytest.mark.parametrize("bias", [False, True], ids=["logit", "bias"])
+@pytest.mark.parametrize("dt,wdt", [(BF, BF), (FP, FP), (BF, F32)], ids=["bf16", "fp16", "fp32-w"])
+def test_padded_batch(T, dt, wdt, bias):
+    """Rows of zeros (both signs) among others: every logit is 0, so the bias or the ids decide."""
+    x, w, b = make(T, 2047, 90, dt, wdt, bias=bias, seed=29)
+    x[T // 2:] = 0.0
+    x[T // 2, ::3] = -0.0
+    x[T - 1, 2046] = 2.0 ** -24  # not quite zero
+    check(run(x, w, b, 7, SIGMOID), formula(x, w, b, 7, SIGMOID, True, 1.0), x, w)
+
+
 @pytest.mark.parametrize("T", [60, 2900])
 @pytest.mark.parametrize("bias", [False, True], ids=["logit", "bias"])
 def test_fp32_weights_to_their_last_bit(T, bias):
@@ -247,8 +280,7 @@ def test_batch_does_not_change_a_token():
     for n in (1, 9, 40, 200):
         i2, s2 = run(x[:n], w, b, 8, SQRTSP)
         assert torch.equal(i2, ids[:n])
-        # fp32 sums over the same 128 products, added in 64 bits in another
-        # order, then one rounding to fp32
+        # fp32 sums of 32 products or of 64, which is the whole difference
         assert bool(((s2 - sc[:n]).abs() <= 2.0 ** -23 * sc[:n]).all())
 
 
