@@ -466,8 +466,8 @@ typedef struct {
  * Every pointer is 16-byte aligned (q_scale: 4). residual_out and y may be x
  * or residual themselves (not both the same one); any other overlap of an
  * output with anything is refused. At least one of y and q is given. A row
- * whose values are not finite, or whose squares' sum leaves fp32, is
- * unspecified; the other rows are not affected by it.
+ * whose values are not finite, or whose squares' sum or r * weight * 448 leaves
+ * fp32, is unspecified; the other rows are not affected by it.
  */
 MOE_W8A8_API moe_status_t moe_w8a8_norm_quant(const moe_w8a8_norm_dims_t *dims, const void *x, const void *residual,
                                               const void *weight, void *residual_out, void *y, void *q,
@@ -501,8 +501,8 @@ typedef struct {
  *
  * The choice is that of 64-bit sums, whatever the types, so that it does not
  * depend on the order of a sum. The weights come from 64-bit logits too, or,
- * where x and weight are both BF16 or both FP16, from logits whose sums of 128
- * products are in fp32.
+ * where x and weight are both BF16 or both FP16 (or x BF16 and weight FP32 in
+ * large products), from logits whose sums of up to 64 products are in fp32.
  *
  *  x              [T, H]
  *  weight         [E, H]

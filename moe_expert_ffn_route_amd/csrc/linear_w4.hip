@@ -289,7 +289,6 @@ __device__ __forceinline__ void finish(const LinearW4Args &a, int nt, int kq, in
 // Few tokens (MT tiles of 16): the weight stream is what counts. A workgroup
 // takes 16 weight rows, its WAVES waves every WAVES-th tile of 128 k, whose
 // codes and scales are loaded DEPTH tiles ahead; the waves' sums meet in LDS.
-
 //
 // MFMA operands are one row per lane, so loading x straight into them is 64
 // requests of 16 bytes per instruction, and four instructions per tile kept
@@ -675,7 +674,7 @@ hipError_t launch_act(const LinearW4Args &a, hipStream_t s) {
 
 hipError_t launch_pack_w4(const uint8_t *codes, const float *scale, const uint8_t *zero, uint8_t *dst_codes,
                           float *dst_scale, uint8_t *dst_zero, const LinearW4Args &a, hipStream_t s) {
-    const int64_t tiles = static_cast<int64_t>(a.n_tiles) * a.k_tiles;  // <= 2^26: the grid below fits
+    const int64_t tiles = static_cast<int64_t>(a.n_tiles) * a.k_tiles;  // <= 2^23: the grid below fits
     const int64_t n = tiles * (kTileK / a.group) * 16;
     hipLaunchKernelGGL(pack_codes_kernel, dim3(static_cast<unsigned>(tiles)), dim3(256), 0, s, codes,
                        reinterpret_cast<uint32_t *>(dst_codes), a);
