@@ -350,6 +350,8 @@ def _call(where: str, fn, first, stream, *args) -> None:
     """fn(*args, stream handle) with the device of tensor `first` current; the
     stream defaults to that device's current one (its handle: the stream
     object costs a microsecond)."""
+    if not isinstance(first, torch.Tensor):
+        raise ValueError(f"{where}: expected a tensor, got {type(first).__name__}")
     device = first.get_device()
     if device < 0:  # refused by fn
         handle = 0

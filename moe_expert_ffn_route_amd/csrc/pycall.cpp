@@ -1,7 +1,7 @@
 // Python entry of the operators around the block: checks tensors against a
 // call's dims and calls the C ABI with their pointers. In Python these checks
 // and the ctypes conversion cost 4 us a call, more than the kernels that a
-// decode batch launches; here they cost 0.4.
+// decode batch launches; here they cost 0.6.
 //
 // Every function takes the dims structure (anything with the buffer
 // interface), the tensors (or None) and the stream handle, raises ValueError
@@ -70,6 +70,16 @@ void *handle_of(PyObject *o) {
     return p;
 }
 
+// The library's call, without the interpreter's lock: a launch may wait for
+// room in the queue, and what empties it for another Python thread.
+template <typename F>
+moe_status_t unlocked(F f) {
+    PyThreadState *state = PyEval_SaveThread();
+    const moe_status_t st = f();
+    PyEval_RestoreThread(state);
+    return st;
+}
+
 // Runs f, which may refuse; no C++ exception reaches Python.
 template <typename F>
 PyObject *guarded(Py_ssize_t n, Py_ssize_t want, F f) {
@@ -98,7 +108,8 @@ PyObject *norm_quant(PyObject *, PyObject *const *a, Py_ssize_t n) {
         void *ro = ts.get(a[4], "residual_out", t, T * H), *y = ts.get(a[5], "y", t, T * H);
         void *q = ts.get(a[6], "q", d.quant == MOE_QUANT_E4M3 ? at::kFloat8_e4m3fn : at::kChar, T * H);
         void *s = ts.get(a[7], "q_scale", at::kFloat, d.quant_group > 0 ? T * (H / d.quant_group) : T);
-        return moe_w8a8_norm_quant(&d, x, res, w, ro, y, q, static_cast<float *>(s), handle_of(a[8]));
+        void *stream = handle_of(a[8]);
+        return unlocked([&] { return moe_w8a8_norm_quant(&d, x, res, w, ro, y, q, static_cast<float *>(s), stream); });
     });
 }
 
@@ -113,8 +124,11 @@ PyObject *gate(PyObject *, PyObject *const *a, Py_ssize_t n) {
         void *x = ts.get(a[1], "x", type_of(d.dtype), T * H), *w = ts.get(a[2], "weight", type_of(d.weight_dtype), E * H);
         void *b = ts.get(a[3], "bias", at::kFloat, E), *ids = ts.get(a[4], "expert_ids", at::kInt, TK);
         void *s = ts.get(a[5], "expert_scales", at::kFloat, TK), *ws = ts.get(a[6], "workspace", at::kByte, bytes);
-        return moe_w8a8_gate(&d, x, w, static_cast<float *>(b), static_cast<int32_t *>(ids), static_cast<float *>(s), ws,
-                             static_cast<size_t>(bytes), handle_of(a[8]));
+        void *stream = handle_of(a[8]);
+        return unlocked([&] {
+            return moe_w8a8_gate(&d, x, w, static_cast<float *>(b), static_cast<int32_t *>(ids), static_cast<float *>(s),
+                                 ws, static_cast<size_t>(bytes), stream);
+        });
     });
 }
 
@@ -131,7 +145,9 @@ PyObject *linear_w4(PyObject *, PyObject *const *a, Py_ssize_t n) {
         void *xs = ts.get(a[2], "x_scale", at::kFloat, T), *w = ts.get(a[3], "weight", at::kByte, packed);
         void *b = ts.get(a[4], "bias", at::kFloat, N);
         void *out = ts.get(a[5], "out", d.act_dtype == MOE_DTYPE_FP16 ? at::kHalf : at::kBFloat16, T * (d.gated ? N / 2 : N));
-        return moe_w8a8_linear_w4(&d, x, static_cast<float *>(xs), w, static_cast<float *>(b), out, handle_of(a[6]));
+        void *stream = handle_of(a[6]);
+        return unlocked(
+            [&] { return moe_w8a8_linear_w4(&d, x, static_cast<float *>(xs), w, static_cast<float *>(b), out, stream); });
     });
 }
 

@@ -3,6 +3,8 @@ and 8-bit output) -> router -> expert block on the norm's codes, and the norm's
 codes through a dense gated pair of 4-bit products. Also
 moe_w8a8_forward_quantized by itself: bit for bit moe_w8a8_forward on an x
 whose codes it is given."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -239,6 +241,37 @@ def test_two_layers_at_once_on_two_streams():
                 L()
     torch.cuda.synchronize()
     for L, w in zip((a, b), want):
+        for got, x in zip(L.outputs(), w):
+            assert torch.equal(got.view(torch.uint8), x.view(torch.uint8))
+
+
+def test_two_threads_call_at_once():
+    """A thread and a stream each: the calls release the interpreter's lock."""
+    layers = [Layer(40, seed=3), Layer(9, seed=4)]
+    want = []
+    for L in layers:
+        L()
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in L.outputs()])
+        L.clear()
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(L):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    L()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=(L,)) for L in layers]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    torch.cuda.synchronize()
+    assert not errors and not any(t.is_alive() for t in threads)
+    for L, w in zip(layers, want):
         for got, x in zip(L.outputs(), w):
             assert torch.equal(got.view(torch.uint8), x.view(torch.uint8))
 

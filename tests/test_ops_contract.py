@@ -214,3 +214,7 @@ def test_binding_refuses_host_tensors_and_misfits(lib):
         moe.moe_w8a8_packed_w4_bytes(moe.make_linear_w4_dims(2, 16, 64, group=0))
     with pytest.raises(moe.MoeError):
         moe.moe_w8a8_gate(moe.make_gate_dims(2, 64, 4, 5), x, x)
+    with pytest.raises(ValueError, match="expected a tensor"):
+        moe.moe_w8a8_norm_quant(d, x.data_ptr(), y=x)
+    with pytest.raises(ValueError, match="dims"):
+        moe.moe_w8a8_norm_quant(moe.make_gate_dims(2, 64, 4, 2), x, y=x)
