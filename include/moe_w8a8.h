@@ -514,6 +514,8 @@ typedef struct {
  * Where fewer than K experts are left (by the bias, or because a logit is
  * NaN), the places that remain get id -1, which the block drops, and weight 0.
  * x and weight are 16-byte aligned, the others 4. The outputs overlap nothing.
+ * The workspace's size does not fall as T or E grows: one that is made for the
+ * largest batch serves every smaller one.
  */
 MOE_W8A8_API moe_status_t moe_w8a8_gate_workspace_size(const moe_w8a8_gate_dims_t *dims, size_t *bytes);
 MOE_W8A8_API moe_status_t moe_w8a8_gate(const moe_w8a8_gate_dims_t *dims, const void *x, const void *weight,

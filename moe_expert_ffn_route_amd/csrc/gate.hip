@@ -805,10 +805,14 @@ hipError_t launch(const GateArgs &a, hipStream_t s) {
 
 }  // namespace
 
+// What plan_of's parts take, or more, so that the size never falls as T grows
+// (a workspace for the largest batch serves all): parts are at most kMaxSplit
+// and chunks / 2, and there is one, or parts * t_tiles * e_tiles < 2 * 512.
 size_t gate_workspace(int T, int E, int H) {
     if (T == 0) return 0;
-    return static_cast<size_t>(plan_of(T, E, H).parts) *
-           (static_cast<size_t>(T) * E * sizeof(double) + (static_cast<size_t>(T) + E) * sizeof(float));
+    const size_t parts = max(1, min(kMaxSplit, (H + kChunk - 1) / kChunk / 2)), logits = static_cast<size_t>(T) * E;
+    const size_t split = min(parts * logits, size_t(2 * 512) * kTileRows * kTileRows);
+    return max(logits, split) * sizeof(double) + parts * (static_cast<size_t>(T) + E) * sizeof(float);
 }
 
 hipError_t launch_gate(const GateArgs &a, hipStream_t s) {

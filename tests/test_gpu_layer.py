@@ -305,6 +305,32 @@ def test_buffers_that_a_call_allocates_belong_to_its_stream():
     assert torch.equal(out, ref)
 
 
+def test_allocating_calls_captured_and_on_the_null_stream():
+    """Outputs and workspaces that calls allocate under capture are the graph's own; handle 0 is a stream."""
+    g = torch.Generator().manual_seed(14)
+    x, w = torch.randn(70, 1024, generator=g).to(BF).cuda(), torch.randn(128, 1024, generator=g).to(BF).cuda()
+    d, ld = moe.make_gate_dims(70, 1024, 128, 6), moe.make_linear_w4_dims(70, 64, 1024)
+    codes = torch.randint(0, 256, (64, 512), dtype=torch.uint8, generator=g).cuda()
+    packed = moe.moe_w8a8_pack_weights_w4(ld, codes, torch.rand(64, 8, generator=g).cuda())
+    call = lambda **kw: [*moe.moe_w8a8_gate(d, x, w, **kw), moe.moe_w8a8_linear_w4(ld, x, packed, **kw)]  # noqa: E731
+    want = call()
+    torch.cuda.synchronize()
+    got = call(stream=0)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = call()
+    for _ in range(4):
+        for t in got:
+            t.fill_(1)
+        call()  # eager work in between
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_binding_refuses_tensors_that_do_not_fit():
     x = torch.zeros(4, 64, dtype=BF, device="cuda")
     d = moe.make_norm_dims(4, 64, quant=moe.MOE_QUANT_NONE)

@@ -122,6 +122,22 @@ def test_gate_workspace_size(lib):
     assert moe.moe_w8a8_gate_workspace_size(moe.make_gate_dims(0, 4096, 256, 8)) >= 0
 
 
+@pytest.mark.parametrize("H,E", [(1, 1), (4096, 256), (2501, 72), (16384, 1024), (700, 1024)])
+def test_gate_workspace_for_the_largest_batch_serves_all(lib, H, E):
+    """Its size grows with T, and holds plan_of's parts of the logits and norms."""
+    last = 0
+    for T in [*range(0, 5000), *range(5000, 65537, 53), 65536]:
+        n = moe.moe_w8a8_gate_workspace_size(moe.make_gate_dims(T, H, E, 1))
+        assert n >= last
+        rows, chunks = 16 if T <= 16 else 64, -(-H // 128)
+        tiles = -(-T // rows) * -(-E // rows)
+        if T:
+            parts = max(1, min(8, -(-512 // tiles), chunks // (8 if T <= 16 else 2)))
+            parts = -(-chunks // -(-chunks // parts))
+            assert n >= parts * (8 * T * E + 4 * (T + E))
+        last = n
+
+
 # ------------------------------------------------------------- 4-bit linear
 
 def w4_dims(**over):
