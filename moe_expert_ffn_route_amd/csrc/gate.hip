@@ -80,7 +80,7 @@ template <>
 constexpr int kPlanes<Bf16, float> = 3;
 // Three planes pay where the fp64 MFMA is the time: bf16 x, fp32 W, E 256, H
 // 4096, logits and choice together, planes / fp64: T 4096 92 / 177 us, T 512
-// 30 / 28, and T 509, E 72, H 2501 25 / 23 (the doubtful choices cost 6 us).
+// 30 / 28 (the doubtful choices cost 6 us).
 constexpr int64_t kPlanesFrom = int64_t(1) << 29;  // products
 
 template <typename T>
@@ -219,20 +219,21 @@ struct Tiles {
     }
 };
 
-// Up to 16 tokens: workgroup (expert tile, part), its four waves take every
-// fourth chunk of the part. Lane l loads row l % 16, eight h from 8 * (l / 16)
-// of each step, straight from memory: there is too little of it for LDS to
-// pay. Every step is folded: that keeps the bound, and with it the share of
-// logits that are computed again, small.
+// Small products: workgroup (16 experts, part, 16 tokens), its four waves take
+// every fourth chunk of the part. Lane l loads row l % 16, eight h from 8 * (l
+// / 16) of each step, straight from memory: there is too little of it for LDS
+// to pay, and 16 x 16 tiles are enough workgroups. Every step is folded: that
+// keeps the bound, and with it the share of logits that are computed again,
+// small.
 constexpr int kSlices = 4;
 template <typename T, typename W>
 __global__ __launch_bounds__(kBlock) void logits_few_kernel(GateArgs a, int chunks_per_part) {
     static_assert(kSlices * kWave == kBlock, "one slice per wave");
     const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
     const int r = lane & 15, kq = lane >> 4;
-    const int e0 = blockIdx.x * 16, part = blockIdx.y;
+    const int e0 = blockIdx.x * 16, part = blockIdx.y, t0 = blockIdx.z * 16;
     // rows past the end read the last one; their results are not stored
-    const T *x = static_cast<const T *>(a.x) + static_cast<size_t>(min(r, a.T - 1)) * a.H;
+    const T *x = static_cast<const T *>(a.x) + static_cast<size_t>(min(t0 + r, a.T - 1)) * a.H;
     const W *w = static_cast<const W *>(a.weight) + static_cast<size_t>(min(e0 + r, a.E - 1)) * a.H;
     Tiles<T, W, kFast<T, W>, 1, 1> tile;
     tile.clear();
@@ -274,7 +275,7 @@ __global__ __launch_bounds__(kBlock) void logits_few_kernel(GateArgs a, int chun
     if (wave > 0) return;
 #pragma unroll
     for (int i = 0; i < kSlices - 1; ++i) tile.sum[0][0] += s_sum[i][lane];
-    tile.store(a, part, 0, e0, lane);
+    tile.store(a, part, t0, e0, lane);
     if constexpr (kFast<T, W>) {
         if (lane < 16) {  // row `lane` lies in lanes lane + 16 q of every wave
             xn = wn = 0.0f;
@@ -285,13 +286,13 @@ __global__ __launch_bounds__(kBlock) void logits_few_kernel(GateArgs a, int chun
                     xn += s_xn[i][lane + 16 * q];
                     wn += s_wn[i][lane + 16 * q];
                 }
-            if (blockIdx.x == 0 && lane < a.T) a.x_norms[part * a.T + lane] = xn;
-            if (e0 + lane < a.E) a.w_norms[part * a.E + e0 + lane] = wn;
+            if (e0 == 0 && t0 + lane < a.T) a.x_norms[part * a.T + t0 + lane] = xn;
+            if (t0 == 0 && e0 + lane < a.E) a.w_norms[part * a.E + e0 + lane] = wn;
         }
     }
 }
 
-// More tokens: workgroups of 64 tokens x 64 experts, a wave 32 x 32 of them.
+// Large products: workgroups of 64 tokens x 64 experts, a wave 32 x 32 of them.
 // Lanes that load MFMA fragments straight from rows touch 16 rows with 16
 // bytes each, four times the requests of whole lines, which is what bound such
 // a kernel (66 us at T 4096, E 256, H 4096); so 128 h of the 128 rows go
@@ -750,16 +751,24 @@ void choose(const GateArgs &a, int parts, double gamma, hipStream_t s) {
     else choose_score<FAST, T, W, MOE_SCORE_SQRT_SOFTPLUS>(a, parts, gamma, s);
 }
 
+// Which kernel, by the products T * E * H. Logits and choice together, H 4096,
+// 16 x 16 / 64 x 64 tiles, in us: bf16, E 256, T 32 11 / 20, T 256 20.5 / 22.7,
+// T 300 24.1 / 23.5, T 512 29.9 / 26.5; E 128, T 509 19.8 / 21.6; E 64, T 1024
+// 21.1 / 18.9. fp64 MFMA: E 256, T 128 15 / 29, T 512 36 / 32; T 509, E 72, H
+// 2501 17.3 / 22.9. Rows under a chunk per wave leave waves idle: T 1024, E
+// 1024, H 256 35 / 32.
+constexpr int64_t kFewUpTo = int64_t(1) << 28;
+
 // Parts of H: two workgroups per CU where that takes no more than kMaxSplit
 // parts (T 4096: 31 us, one workgroup per CU 38 us), of at least two chunks per
-// wave (few tokens) or workgroup.
+// wave (small products) or workgroup.
 struct Plan {
     bool few;
     int t_tiles, e_tiles, parts, chunks_per_part;
 };
 Plan plan_of(int T, int E, int H) {
     Plan p;
-    p.few = T <= 16;
+    p.few = T <= 16 || (H >= kSlices * kChunk && static_cast<int64_t>(T) * E * H <= kFewUpTo);
     const int rows = p.few ? 16 : kTileRows, chunks = (H + kChunk - 1) / kChunk;
     p.t_tiles = (T + rows - 1) / rows;
     p.e_tiles = (E + rows - 1) / rows;
@@ -781,7 +790,7 @@ hipError_t launch(const GateArgs &a, hipStream_t s) {
     const bool fast = p.few || kPlanes<T, W> == 1 ? kFast<T, W>
                                                   : kPlanes<T, W> > 1 && static_cast<int64_t>(a.T) * a.E * a.H > kPlanesFrom;
     if (p.few) {
-        hipLaunchKernelGGL((logits_few_kernel<T, W>), dim3(p.e_tiles, p.parts), dim3(kBlock), 0, s, g,
+        hipLaunchKernelGGL((logits_few_kernel<T, W>), dim3(p.e_tiles, p.parts, p.t_tiles), dim3(kBlock), 0, s, g,
                            p.chunks_per_part);
     } else {
         const int units = p.t_tiles * p.parts;

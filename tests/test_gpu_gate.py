@@ -71,7 +71,8 @@ def check(got, want, x, w):
 
 SIZES = [(1, 1, 1, 1), (1, 4096, 256, 8), (8, 4096, 256, 8), (3, 7, 5, 5), (2, 8, 64, 16), (5, 130, 65, 6), (16, 1000, 128, 4),
          (17, 2501, 72, 6), (33, 512, 256, 8), (64, 7168, 384, 8), (100, 640, 1024, 16), (129, 1024, 257, 9),
-         (300, 2048, 160, 6), (509, 2501, 72, 6), (1000, 333, 30, 3), (1, 16384, 1024, 16), (2, 16383, 511, 2), (700, 4096, 256, 8)]
+         (300, 2048, 160, 6), (509, 2501, 72, 6), (1000, 333, 30, 3), (1, 16384, 1024, 16), (2, 16383, 511, 2), (700, 4096, 256, 8),
+         (250, 4095, 255, 8), (1100, 2501, 130, 6), (40, 511, 70, 4)]
 
 
 @pytest.mark.parametrize("T,H,E,K", SIZES)
@@ -84,13 +85,14 @@ def test_sizes(T, H, E, K, score):
 
 
 @pytest.mark.parametrize("dt,wdt", [(BF, F32), (FP, FP), (FP, BF), (FP, F32), (F32, BF), (F32, F32)], ids=str)
-@pytest.mark.parametrize("T,H,E,K", [(1, 4096, 256, 8), (7, 1001, 40, 4), (64, 2048, 256, 8), (200, 515, 130, 8), (600, 1024, 64, 6)])
+@pytest.mark.parametrize("T,H,E,K", [(1, 4096, 256, 8), (7, 1001, 40, 4), (64, 2048, 256, 8), (200, 515, 130, 8), (600, 1024, 64, 6),
+                                     (1100, 2501, 130, 6)])
 def test_types(T, H, E, K, dt, wdt):
     x, w, b = make(T, H, E, dt, wdt, bias=True)
     check(run(x, w, b, K, SIGMOID), formula(x, w, b, K, SIGMOID, True, 1.0), x, w)
 
 
-@pytest.mark.parametrize("T", [3, 40, 600])
+@pytest.mark.parametrize("T", [3, 40, 600, 1400])
 def test_ties_go_to_the_lowest_id(T):
     x, w, _ = make(T, 1024, 200)
     w[60:120] = w[0:60]     # every expert of 60..119 ties with one of 0..59
@@ -106,7 +108,7 @@ def test_ties_go_to_the_lowest_id(T):
     assert ids.tolist() == [list(range(8))] * T and bool((sc == 0.125).all())
 
 
-@pytest.mark.parametrize("T", [5, 200])
+@pytest.mark.parametrize("T", [5, 200, 1500])
 @pytest.mark.parametrize("keep", [None, 0, 3, 7], ids=lambda k: "all" if k is None else f"element{k}")
 @pytest.mark.parametrize("bias", [False, True], ids=["logit", "bias"])
 @pytest.mark.parametrize("dt", [BF, FP], ids=["bf16", "fp16"])
@@ -173,7 +175,7 @@ def test_subnormal_and_tiny_inputs(T):
     check(run((x.float() * 2.0 ** -50).to(BF), w, None, 6), formula((x.float() * 2.0 ** -50).to(BF), w, None, 6, SOFTMAX, True, 1.0), x, w)
 
 
-@pytest.mark.parametrize("T", [7, 150])
+@pytest.mark.parametrize("T", [7, 150, 1500])
 @pytest.mark.parametrize("dt,wdt,xs,ws", [(BF, BF, -82, 60), (BF, BF, 56, -76), (FP, FP, -20, 4), (BF, F32, -82, 60)],
                          ids=["bf16-x", "bf16-w", "fp16", "fp32-w"])
 def test_close_logits_of_inputs_whose_squares_vanish(T, dt, wdt, xs, ws):

@@ -129,10 +129,11 @@ def test_gate_workspace_for_the_largest_batch_serves_all(lib, H, E):
     for T in [*range(0, 5000), *range(5000, 65537, 53), 65536]:
         n = moe.moe_w8a8_gate_workspace_size(moe.make_gate_dims(T, H, E, 1))
         assert n >= last
-        rows, chunks = 16 if T <= 16 else 64, -(-H // 128)
+        few = T <= 16 or (H >= 512 and T * E * H <= 2 ** 28)
+        rows, chunks = 16 if few else 64, -(-H // 128)
         tiles = -(-T // rows) * -(-E // rows)
         if T:
-            parts = max(1, min(8, -(-512 // tiles), chunks // (8 if T <= 16 else 2)))
+            parts = max(1, min(8, -(-512 // tiles), chunks // (8 if few else 2)))
             parts = -(-chunks // -(-chunks // parts))
             assert n >= parts * (8 * T * E + 4 * (T + E))
         last = n
