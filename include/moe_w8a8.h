@@ -500,9 +500,9 @@ typedef struct {
  *   `normalize`, times route_scale; rounded once, to fp32
  *
  * The choice is that of 64-bit sums, whatever the types, so that it does not
- * depend on the order of a sum. The weights come from 64-bit logits too, or,
- * where x and weight are both BF16 or both FP16 (or x BF16 and weight FP32 in
- * large products), from logits whose sums of up to 64 products are in fp32.
+ * depend on the order of a sum. The weights come from 64-bit logits too, or, in
+ * large products of x and weight both BF16, both FP16, or x BF16 and weight
+ * FP32, from logits whose sums of 64 products are in fp32.
  *
  *  x              [T, H]
  *  weight         [E, H]

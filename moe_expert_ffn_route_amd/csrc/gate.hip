@@ -8,13 +8,14 @@
 // depend on its order would make them depend on the tiling, the batch size
 // and the split of H. They are therefore those of 64-bit logits, in one of
 // two ways:
-//   - x and W both bf16, or both fp16, or bf16 x and fp32 W (large products;
-//     W is split into three bf16 parts, which hold its 24 bits): MFMA with
-//     fp32 sums over 32 or 64 h, which are added up in fp64. |x| |w| (2-norms),
+//   - large products of x and W both bf16, or both fp16, or bf16 x and fp32 W
+//     (W is split into three bf16 parts, which hold its 24 bits): MFMA with
+//     fp32 sums over 64 h, which are added up in fp64. |x| |w| (2-norms),
 //     which is no less than the sum of |x * w|, bounds how far such a logit is
 //     off. Where the bound leaves open which of two experts comes first, the
 //     choice kernel computes the logits of those experts again, in fp64.
-//   - other types: fp64 MFMA throughout (their products are exact in it).
+//   - small products and other types: fp64 MFMA throughout (products are exact
+//     in it).
 //
 // Two launches: the logits, in up to kMaxSplit parts of H, into the
 // workspace; and one wave per token, which adds the parts in order, for
@@ -222,9 +223,10 @@ struct Tiles {
 // Small products: workgroup (16 experts, part, 16 tokens), its four waves take
 // every fourth chunk of the part. Lane l loads row l % 16, eight h from 8 * (l
 // / 16) of each step, straight from memory: there is too little of it for LDS
-// to pay, and 16 x 16 tiles are enough workgroups. Every step is folded: that
-// keeps the bound, and with it the share of logits that are computed again,
-// small.
+// to pay, and 16 x 16 tiles are enough workgroups. fp64 MFMA, also for bf16 and
+// fp16: at these sizes its time is less than that of computing the one doubtful
+// choice again that a batch of fp32 sums has as a rule (T 64, E 256, H 4096:
+// 11 us against 15).
 constexpr int kSlices = 4;
 template <typename T, typename W>
 __global__ __launch_bounds__(kBlock) void logits_few_kernel(GateArgs a, int chunks_per_part) {
@@ -235,9 +237,8 @@ __global__ __launch_bounds__(kBlock) void logits_few_kernel(GateArgs a, int chun
     // rows past the end read the last one; their results are not stored
     const T *x = static_cast<const T *>(a.x) + static_cast<size_t>(min(t0 + r, a.T - 1)) * a.H;
     const W *w = static_cast<const W *>(a.weight) + static_cast<size_t>(min(e0 + r, a.E - 1)) * a.H;
-    Tiles<T, W, kFast<T, W>, 1, 1> tile;
+    Tiles<T, W, false, 1, 1> tile;
     tile.clear();
-    float xn = 0.0f, wn = 0.0f;  // squares of the lane's elements
     const int c_end = min((part + 1) * chunks_per_part, (a.H + kChunk - 1) / kChunk);
     auto chunk = [&](auto whole, int c) {
         T xv[kChunk / kStep][1][kVec];
@@ -249,47 +250,19 @@ __global__ __launch_bounds__(kBlock) void logits_few_kernel(GateArgs a, int chun
             load8<decltype(whole)::value>(w, k, a.H, wv[s][0]);
         }
 #pragma unroll
-        for (int s = 0; s < kChunk / kStep; ++s) {
-            if constexpr (kFast<T, W>) {
-                v4i xf[1][1], wf[1][1][1];
-                __builtin_memcpy(&xf[0][0], xv[s][0], 16);
-                __builtin_memcpy(&wf[0][0][0], wv[s][0], 16);
-                add_squares<T>(xf[0][0], xn);
-                add_squares<T>(wf[0][0][0], wn);
-                tile.template fast<1, 1>(xf, wf);
-            } else {
-                tile.full(xv[s], wv[s]);
-            }
-        }
+        for (int s = 0; s < kChunk / kStep; ++s) tile.full(xv[s], wv[s]);
     };
     for (int c = part * chunks_per_part + wave; c < c_end; c += kSlices) {
         if ((c + 1) * kChunk <= a.H) chunk(std::true_type{}, c);
         else chunk(std::false_type{}, c);
     }
     __shared__ v4d s_sum[kSlices - 1][kWave];
-    __shared__ float s_xn[kSlices][kWave], s_wn[kSlices][kWave];
     if (wave > 0) s_sum[wave - 1][lane] = tile.sum[0][0];
-    s_xn[wave][lane] = xn;
-    s_wn[wave][lane] = wn;
     __syncthreads();
     if (wave > 0) return;
 #pragma unroll
     for (int i = 0; i < kSlices - 1; ++i) tile.sum[0][0] += s_sum[i][lane];
     tile.store(a, part, t0, e0, lane);
-    if constexpr (kFast<T, W>) {
-        if (lane < 16) {  // row `lane` lies in lanes lane + 16 q of every wave
-            xn = wn = 0.0f;
-#pragma unroll
-            for (int i = 0; i < kSlices; ++i)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    xn += s_xn[i][lane + 16 * q];
-                    wn += s_wn[i][lane + 16 * q];
-                }
-            if (e0 == 0 && t0 + lane < a.T) a.x_norms[part * a.T + t0 + lane] = xn;
-            if (t0 == 0 && e0 + lane < a.E) a.w_norms[part * a.E + e0 + lane] = wn;
-        }
-    }
 }
 
 // Large products: workgroups of 64 tokens x 64 experts, a wave 32 x 32 of them.
@@ -752,16 +725,15 @@ void choose(const GateArgs &a, int parts, double gamma, hipStream_t s) {
 }
 
 // Which kernel, by the products T * E * H. Logits and choice together, H 4096,
-// 16 x 16 / 64 x 64 tiles, in us: bf16, E 256, T 32 11 / 20, T 256 20.5 / 22.7,
-// T 300 24.1 / 23.5, T 512 29.9 / 26.5; E 128, T 509 19.8 / 21.6; E 64, T 1024
-// 21.1 / 18.9. fp64 MFMA: E 256, T 128 15 / 29, T 512 36 / 32; T 509, E 72, H
-// 2501 17.3 / 22.9. Rows under a chunk per wave leave waves idle: T 1024, E
-// 1024, H 256 35 / 32.
+// 16 x 16 / 64 x 64 tiles, in us: bf16, E 256, T 32 10 / 20, T 256 19 / 23, T
+// 300 23.7 / 23.2, T 512 31 / 26; E 128, T 509 19 / 21.5. fp64 MFMA in both: E
+// 256, T 128 15 / 29, T 512 36 / 32; T 509, E 72, H 2501 15 / 23. Rows under a
+// chunk per wave leave waves idle: T 1024, E 1024, H 256 35 / 32.
 constexpr int64_t kFewUpTo = int64_t(1) << 28;
 
 // Parts of H: two workgroups per CU where that takes no more than kMaxSplit
-// parts (T 4096: 31 us, one workgroup per CU 38 us), of at least two chunks per
-// wave (small products) or workgroup.
+// parts (T 4096: 31 us, one workgroup per CU 38 us), of at least one chunk per
+// wave (small products; two: T 8 10.1 us instead of 9.2) or two per workgroup.
 struct Plan {
     bool few;
     int t_tiles, e_tiles, parts, chunks_per_part;
@@ -773,7 +745,7 @@ Plan plan_of(int T, int E, int H) {
     p.t_tiles = (T + rows - 1) / rows;
     p.e_tiles = (E + rows - 1) / rows;
     int parts = (512 + p.t_tiles * p.e_tiles - 1) / (p.t_tiles * p.e_tiles);
-    parts = min(min(parts, kMaxSplit), chunks / (p.few ? 2 * kSlices : 2));
+    parts = min(min(parts, kMaxSplit), chunks / (p.few ? kSlices : 2));
     parts = max(parts, 1);
     p.chunks_per_part = (chunks + parts - 1) / parts;
     p.parts = (chunks + p.chunks_per_part - 1) / p.chunks_per_part;
@@ -787,8 +759,8 @@ hipError_t launch(const GateArgs &a, hipStream_t s) {
     g.x_norms = reinterpret_cast<float *>(a.logits + static_cast<size_t>(p.parts) * a.T * a.E);
     g.w_norms = g.x_norms + static_cast<size_t>(p.parts) * a.T;
     // whether the logits are bounded fp32 sums
-    const bool fast = p.few || kPlanes<T, W> == 1 ? kFast<T, W>
-                                                  : kPlanes<T, W> > 1 && static_cast<int64_t>(a.T) * a.E * a.H > kPlanesFrom;
+    const bool fast = !p.few && (kPlanes<T, W> == 1 ||
+                                 (kPlanes<T, W> > 1 && static_cast<int64_t>(a.T) * a.E * a.H > kPlanesFrom));
     if (p.few) {
         hipLaunchKernelGGL((logits_few_kernel<T, W>), dim3(p.e_tiles, p.parts, p.t_tiles), dim3(kBlock), 0, s, g,
                            p.chunks_per_part);
@@ -804,7 +776,7 @@ hipError_t launch(const GateArgs &a, hipStream_t s) {
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const double gamma = kStep * (p.few ? 1 : kFold) * kUnit;
+    const double gamma = kStep * kFold * kUnit;
     if constexpr (kPlanes<T, W> > 0) {
         if (fast) choose<true, T, W>(g, p.parts, gamma, s);
     }

@@ -282,7 +282,7 @@ def test_batch_does_not_change_a_token():
     for n in (1, 9, 40, 200):
         i2, s2 = run(x[:n], w, b, 8, SQRTSP)
         assert torch.equal(i2, ids[:n])
-        # fp32 sums of 32 products or of 64, which is the whole difference
+        # 64-bit sums, or fp32 sums of 64 products joined in 64 bits
         assert bool(((s2 - sc[:n]).abs() <= 2.0 ** -23 * sc[:n]).all())
 
 
