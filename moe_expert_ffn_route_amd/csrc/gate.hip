@@ -279,13 +279,12 @@ struct Stage {  // kTileRows rows of kChunk elements
     static constexpr int kPer = kTileRows * kSlots / kBlock;         // per thread
     static constexpr int kBytes = kTileRows * kSlots * 16;
     static constexpr int kElems = 16 / sizeof(T);
-    v4i v[kPer];
-    const T *p[kPer];  // where the thread's slots of the next chunk lie
+    const T *p[kPer];  // where the thread's slots of the first chunk lie
     int k;             // and their element (the same for all of them)
     static_assert(kBlock % kSlots == 0, "a thread's slots are one column");
     // rows past the end read the last one
-    __device__ __forceinline__ void start(const T *base, int row0, int rows, int H, int c) {
-        k = c * kChunk + static_cast<int>(threadIdx.x) % kSlots * kElems;
+    __device__ __forceinline__ void start(const T *base, int row0, int rows, int H) {
+        k = static_cast<int>(threadIdx.x) % kSlots * kElems;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int row = min(row0 + static_cast<int>(threadIdx.x + i * kBlock) / kSlots, rows - 1);
@@ -293,25 +292,23 @@ struct Stage {  // kTileRows rows of kChunk elements
         }
     }
     template <bool WHOLE>
-    __device__ __forceinline__ void fetch(int H) {
+    __device__ __forceinline__ void fetch(int c, int H, v4i (&v)[kPer]) const {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            if (WHOLE || k + kElems <= H) {
-                __builtin_memcpy(&v[i], p[i], 16);
+            if (WHOLE || c * kChunk + k + kElems <= H) {
+                __builtin_memcpy(&v[i], p[i] + c * kChunk, 16);
             } else {
                 T raw[kElems];
 #pragma unroll
                 for (int e = 0; e < kElems; ++e) {
                     raw[e] = T{};
-                    if (k + e < H) raw[e] = p[i][e];
+                    if (c * kChunk + k + e < H) raw[e] = p[i][c * kChunk + e];
                 }
                 __builtin_memcpy(&v[i], raw, 16);
             }
-            p[i] += kChunk;
         }
-        k += kChunk;
     }
-    __device__ __forceinline__ void put(char *lds) const {
+    static __device__ __forceinline__ void put(char *lds, const v4i (&v)[kPer]) {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int slot = threadIdx.x + i * kBlock, row = slot / kSlots, c = slot % kSlots;
@@ -321,7 +318,7 @@ struct Stage {  // kTileRows rows of kChunk elements
     // fp32 slots as three planes of bf16: the upper 8 of the 24 bits, the next
     // and the last (a truncation and an exact difference each)
     static constexpr int kPlaneBytes = kTileRows * kChunk * 2;
-    __device__ __forceinline__ void put_planes(char *lds) const {
+    static __device__ __forceinline__ void put_planes(char *lds, const v4i (&v)[kPer]) {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int slot = threadIdx.x + i * kBlock, row = slot / kSlots, c = slot % kSlots;
@@ -376,33 +373,30 @@ __global__ __launch_bounds__(kBlock) void logits_many_kernel(GateArgs a, int chu
     tile.clear();
     Stage<T> sx;
     Stage<W> sw;
-    auto fetch = [&](int c) {
-        if ((c + 1) * kChunk <= a.H) {
-            sx.template fetch<true>(a.H);
-            sw.template fetch<true>(a.H);
-        } else {
-            sx.template fetch<false>(a.H);
-            sw.template fetch<false>(a.H);
-        }
-    };
+    sx.start(static_cast<const T *>(a.x), t0, a.T, a.H);
+    sw.start(static_cast<const W *>(a.weight), e0, a.E, a.H);
     float xn[Stage<T>::kPer] = {}, wn[Stage<W>::kPer] = {};  // squares of the thread's slots
-    const int c0 = part * chunks_per_part, c_end = min(c0 + chunks_per_part, (a.H + kChunk - 1) / kChunk);
-    sx.start(static_cast<const T *>(a.x), t0, a.T, a.H, c0);
-    sw.start(static_cast<const W *>(a.weight), e0, a.E, a.H, c0);
-    fetch(c0);  // a part has at least one chunk
-    for (int c = c0; c < c_end; ++c) {
+    struct Chunk {
+        v4i x[Stage<T>::kPer], w[Stage<W>::kPer];
+    };
+    auto fetch = [&](auto whole, int c, Chunk &f) {
+        sx.template fetch<decltype(whole)::value>(c, a.H, f.x);
+        sw.template fetch<decltype(whole)::value>(c, a.H, f.w);
+    };
+    auto put = [&](const Chunk &f) {
         __syncthreads();
-        sx.put(s_x);
-        if constexpr (PLANES > 1) sw.put_planes(s_w);
-        else sw.put(s_w);
+        Stage<T>::put(s_x, f.x);
+        if constexpr (PLANES > 1) Stage<W>::put_planes(s_w, f.w);
+        else Stage<W>::put(s_w, f.w);
         if constexpr (FAST) {
 #pragma unroll
-            for (int i = 0; i < Stage<T>::kPer; ++i) add_squares<T>(sx.v[i], xn[i]);
+            for (int i = 0; i < Stage<T>::kPer; ++i) add_squares<T>(f.x[i], xn[i]);
 #pragma unroll
-            for (int i = 0; i < Stage<W>::kPer; ++i) add_squares<W>(sw.v[i], wn[i]);
+            for (int i = 0; i < Stage<W>::kPer; ++i) add_squares<W>(f.w[i], wn[i]);
         }
         __syncthreads();
-        if (c + 1 < c_end) fetch(c + 1);
+    };
+    auto multiply = [&] {
         if constexpr (FAST) {
 #pragma unroll
             for (int s = 0; s < kChunk / kStep; s += kFold) {
@@ -437,6 +431,23 @@ __global__ __launch_bounds__(kBlock) void logits_many_kernel(GateArgs a, int chu
                 tile.full(xv, wv);
             }
         }
+    };
+    // The next whole chunk is loaded meanwhile, and past the last one that one
+    // again: no load is conditional, so the compiler's wait counts are exact
+    // (T 8192, H 7168, with the choice 117 -> 100 us; two ahead 106).
+    const int c0 = part * chunks_per_part, c_end = min(c0 + chunks_per_part, (a.H + kChunk - 1) / kChunk);
+    const int whole_end = min(c_end, a.H / kChunk);
+    Chunk chunk;
+    if (c0 < whole_end) fetch(std::true_type{}, c0, chunk);
+    for (int c = c0; c < whole_end; ++c) {
+        put(chunk);
+        fetch(std::true_type{}, min(c + 1, whole_end - 1), chunk);
+        multiply();
+    }
+    if (whole_end < c_end) {
+        fetch(std::false_type{}, whole_end, chunk);
+        put(chunk);
+        multiply();
     }
     tile.store(a, part, t0 + tm, e0 + en, lane);
     if constexpr (FAST) {  // a row's slots lie in neighbouring lanes, 16 of them or 32
