@@ -353,10 +353,12 @@ struct Stage {  // kTileRows rows of kChunk elements
 // 21.6, four 28.8 + 24.5 (a wider bound leaves more tokens open).
 constexpr int kFold = 2;
 
-// Registers for three workgroups per CU: T 8192, H 7168, with the choice 95 us
-// instead of 100.
+// Registers for three workgroups per CU where their LDS fits: T 8192, H 7168,
+// with the choice 95 us instead of 100.
 template <typename T, typename W, int PLANES>
-__global__ __launch_bounds__(kBlock, 3) void logits_many_kernel(GateArgs a, int chunks_per_part, int e_tiles, int units) {
+constexpr int kPerCu = sizeof(T) + (PLANES > 1 ? 2 * PLANES : sizeof(W)) > 6 ? 2 : 3;
+template <typename T, typename W, int PLANES>
+__global__ __launch_bounds__(kBlock, (kPerCu<T, W, PLANES>)) void logits_many_kernel(GateArgs a, int chunks_per_part, int e_tiles, int units) {
     constexpr bool FAST = PLANES > 0;
     __shared__ __attribute__((aligned(16))) char s_x[Stage<T>::kBytes];
     __shared__ __attribute__((aligned(16))) char s_w[PLANES > 1 ? PLANES * Stage<T>::kBytes : Stage<W>::kBytes];
@@ -722,12 +724,15 @@ __global__ __launch_bounds__(kBlock) void choose_kernel(GateArgs a, int parts, d
     }
 }
 
+// Experts per lane: the fewest that hold E (E 384, H 7168, logits and choice, 8
+// / 16 per lane: T 8 14.2 / 18.4 us, T 2048 61 / 70).
 template <bool FAST, typename T, typename W, int SCORE>
 void choose_score(const GateArgs &a, int parts, double gamma, hipStream_t s) {
     const dim3 grid((a.T + kBlock / kWave - 1) / (kBlock / kWave)), blk(kBlock);
     if (a.E <= kWave) hipLaunchKernelGGL((choose_kernel<FAST, T, W, SCORE, 1>), grid, blk, 0, s, a, parts, gamma);
     else if (a.E <= 2 * kWave) hipLaunchKernelGGL((choose_kernel<FAST, T, W, SCORE, 2>), grid, blk, 0, s, a, parts, gamma);
     else if (a.E <= 4 * kWave) hipLaunchKernelGGL((choose_kernel<FAST, T, W, SCORE, 4>), grid, blk, 0, s, a, parts, gamma);
+    else if (a.E <= 8 * kWave) hipLaunchKernelGGL((choose_kernel<FAST, T, W, SCORE, 8>), grid, blk, 0, s, a, parts, gamma);
     else hipLaunchKernelGGL((choose_kernel<FAST, T, W, SCORE, 16>), grid, blk, 0, s, a, parts, gamma);
 }
 template <bool FAST, typename T, typename W>

@@ -72,7 +72,7 @@ def check(got, want, x, w):
 SIZES = [(1, 1, 1, 1), (1, 4096, 256, 8), (8, 4096, 256, 8), (3, 7, 5, 5), (2, 8, 64, 16), (5, 130, 65, 6), (16, 1000, 128, 4),
          (17, 2501, 72, 6), (33, 512, 256, 8), (64, 7168, 384, 8), (100, 640, 1024, 16), (129, 1024, 257, 9),
          (300, 2048, 160, 6), (509, 2501, 72, 6), (1000, 333, 30, 3), (1, 16384, 1024, 16), (2, 16383, 511, 2), (700, 4096, 256, 8),
-         (250, 4095, 255, 8), (1100, 2501, 130, 6), (40, 511, 70, 4)]
+         (250, 4095, 255, 8), (1100, 2501, 130, 6), (40, 511, 70, 4), (7, 600, 512, 16), (900, 2048, 500, 8)]
 
 
 @pytest.mark.parametrize("T,H,E,K", SIZES)
