@@ -348,9 +348,10 @@ struct Stage {  // kTileRows rows of kChunk elements
     }
 };
 
-// Steps that are summed in fp32 before the fp64 sum: 64 products. At T 4096,
-// E 256, H 4096 (logits, then choice): one step 37.5 + 19.0 us, two 31.2 +
-// 21.6, four 28.8 + 24.5 (a wider bound leaves more tokens open).
+// Steps that are summed in fp32 before the fp64 sum: 64 products. Logits and
+// choice at E 256, two / four steps: T 4096, H 4096 48 / 50 us, T 8192, H 7168
+// 100 / 104 (a wider bound leaves more tokens open); one step: fewer open
+// tokens, but 3 us more in all.
 constexpr int kFold = 2;
 
 // Registers for three workgroups per CU where their LDS fits: T 8192, H 7168,
@@ -750,8 +751,9 @@ void choose(const GateArgs &a, int parts, double gamma, hipStream_t s) {
 constexpr int64_t kFewUpTo = int64_t(1) << 28;
 
 // Parts of H: two workgroups per CU where that takes no more than kMaxSplit
-// parts (T 4096: 31 us, one workgroup per CU 38 us), of at least one chunk per
-// wave (small products; two: T 8 10.1 us instead of 9.2) or two per workgroup.
+// parts (T 4096, E 256, with the choice: 48 us, three 49, four 51), of at least
+// one chunk per wave (small products; two: T 8 10.1 us instead of 9.2) or two
+// per workgroup.
 struct Plan {
     bool few;
     int t_tiles, e_tiles, parts, chunks_per_part;
