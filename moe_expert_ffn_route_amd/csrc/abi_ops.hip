@@ -4,7 +4,7 @@
 #include <math.h>
 
 #include "../../include/moe_w8a8.h"
-#include "internal.h"
+#include "ops.h"
 
 using namespace moe;
 

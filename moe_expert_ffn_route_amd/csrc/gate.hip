@@ -20,7 +20,7 @@
 // Two launches: the logits, in up to kMaxSplit parts of H, into the
 // workspace; and one wave per token, which adds the parts in order, for
 // scores and choice.
-#include "internal.h"
+#include "ops.h"
 
 #include <type_traits>
 

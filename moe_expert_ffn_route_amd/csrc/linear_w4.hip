@@ -23,7 +23,7 @@
 // time is the matrix products (below). Sums over K are split over waves and
 // joined in LDS in a fixed order: no workspace, no atomics, and results do not
 // depend on timing.
-#include "internal.h"
+#include "ops.h"
 
 #include <type_traits>
 

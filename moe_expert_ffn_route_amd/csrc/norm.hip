@@ -20,7 +20,7 @@
 // branch. Lanes past the row's end read its last chunk again and count nothing.
 // A row whose length is no multiple of kVec ends in up to seven elements more,
 // one per thread.
-#include "internal.h"
+#include "ops.h"
 #include "rowquant.h"
 
 #include "../../include/moe_w8a8.h"
