@@ -529,9 +529,10 @@ __device__ __forceinline__ double score_of(double l, double m) {
 // and T and W do not matter.
 //
 // K choices in order. FAST, an expert that lies closer than `off` below a
-// choice is marked, and so is that choice; the marked ones' logits are then
-// computed in fp64 and the choice is made again. An unmarked expert is further
-// than `off` from all that it was compared with, so its place stands.
+// choice is marked, and so is that choice, and so is every expert whose fp32
+// sum is not finite; the marked ones' logits are then computed in fp64 and the
+// choice is made again. An unmarked expert is further than `off` from all that
+// it was compared with, so its place stands.
 //
 // A token is a chain of reductions, and few tokens are a single wave's
 // latency, most of it instruction fetches of a kernel that runs once: scores
@@ -587,10 +588,11 @@ __global__ __launch_bounds__(kBlock) void choose_kernel(GateArgs a, int parts, d
     // sqrt(softplus) under 1/3; a softmax share moves by at most twice its
     // logits' error.
     double off = 0.0;
+    uint32_t overflowed = 0;  // bit j: expert j * 64 + lane
     if constexpr (FAST) {
-        float wn = 0.0f;  // squares order like their bits; a NaN is the largest, and marks all
+        float wn = 0.0f;  // squares order like their bits; rows with a NaN have no logit to be told from others
 #pragma unroll
-        for (int j = 0; j < NPL; ++j) wn = n[j] <= wn ? wn : n[j];
+        for (int j = 0; j < NPL; ++j) wn = n[j] > wn ? n[j] : wn;
         wn = __uint_as_float(wave_max_int<uint32_t>(__float_as_uint(wn), 0u));
         off = 2.0 * (gamma * 1.05 * sqrt((xn + kTinySquares) * (wn + kTinySquares)) + kTiny);
         if (a.bias) off *= SCORE == MOE_SCORE_SOFTMAX ? 2.5 : SCORE == MOE_SCORE_SIGMOID ? 0.25 : 0.34;
@@ -602,8 +604,21 @@ __global__ __launch_bounds__(kBlock) void choose_kernel(GateArgs a, int parts, d
         off += 0x1p-50 * static_cast<double>(bm);
         // A row of zeros (a padded batch): its logits are 0, all of them equal
         // and right. Without this 243 us instead of 10 for two such rows of 8.
-        if (xn == 0.0f && row_is_zero(a, static_cast<const T *>(a.x) + static_cast<size_t>(t) * a.H, lane))
+        if (xn == 0.0f && row_is_zero(a, static_cast<const T *>(a.x) + static_cast<size_t>(t) * a.H, lane)) {
             off = -__builtin_inf();
+        } else {
+            // An fp32 sum that is infinite or NaN says nothing, it may have
+            // overflowed, and key_of would leave its expert out: then every
+            // logit is computed again. (Not where x or the expert's row hold a
+            // NaN, which their squares show: that logit is NaN. Nor where the
+            // bias leaves the expert out.)
+#pragma unroll
+            for (int j = 0; j < NPL; ++j)
+                if (j * kWave + lane < a.E && !(fabs(l[j]) < __builtin_inf()) && xn == xn && n[j] == n[j] &&
+                    (!a.bias || bias[j] > -__builtin_inff()))
+                    overflowed |= 1u << j;
+            if (__ballot(overflowed != 0)) off = __builtin_inf();
+        }
     }
     double s[NPL], total;  // scores (softmax: undivided, `total` their sum)
     int id_mine;           // lane k keeps the k-th choice
@@ -664,19 +679,21 @@ __global__ __launch_bounds__(kBlock) void choose_kernel(GateArgs a, int parts, d
             const double mine = value_of(c_mine);
             const bool chosen = id_mine >= 0;
             const int count = __popcll(__ballot(chosen));
-            if (count == 0) break;
             const double next = value_of(__shfl_down(c_mine, 1, kWave));
-            const double last = value_of(__shfl(c_mine, count - 1, kWave));
+            const double last = value_of(__shfl(c_mine, max(count - 1, 0), kWave));
             uint32_t marked = 0;  // bit j: expert j * 64 + lane
 #pragma unroll
             for (int j = 0; j < NPL; ++j)
                 if (c[j] != kNone && !(last - value_of(c[j]) > off)) marked |= 1u << j;
             const unsigned long long left = __ballot(marked != 0);
-            const unsigned long long near =
-                __ballot(chosen && lane + 1 < count && !(mine - next > off)) | (left ? 1ull << (count - 1) : 0);
-            if (!near) break;
+            const unsigned long long near = __ballot(chosen && lane + 1 < count && !(mine - next > off)) |
+                                            (left && count > 0 ? 1ull << (count - 1) : 0);
+#pragma unroll
+            for (int j = 0; j < NPL; ++j)
+                if (overflowed >> j & 1) marked |= 1u << j;
+            if (!__ballot(marked != 0) && !near) break;
             unsigned long long todo = near | near << 1;  // both of a pair
-            if (count < kWave) todo &= (1ull << count) - 1;
+            todo &= (1ull << count) - 1;                 // count <= kMaxTopK
             while (todo) {
                 const int id = __builtin_amdgcn_readlane(id_mine, __builtin_ctzll(todo));
                 todo &= todo - 1;

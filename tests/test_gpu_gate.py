@@ -311,3 +311,24 @@ def test_largest_batch():
     rows = torch.arange(0, T, 1021)
     want = formula(x[rows], w, None, 2, SOFTMAX, True, 1.0)
     check((ids[rows], sc[rows]), want, x[rows], w)
+
+
+@pytest.mark.parametrize("T,dt,wdt", [(9, BF, BF), (300, BF, BF), (9, BF, F32), (600, BF, F32)], ids=str)
+@pytest.mark.parametrize("sign", [-1, 0, 1], ids=["all-negative", "mixed", "all-positive"])
+def test_finite_inputs_whose_fp32_sums_overflow(T, dt, wdt, sign):
+    """Products of 2^130: the 64-bit logits are finite, sums in fp32 would be infinite or NaN. All logits of one sign,
+    and rows whose terms cancel."""
+    x, w, _ = make(T, 4096, 256, dt, wdt, seed=41)
+    if sign:
+        x, w = x.abs(), sign * w.abs()
+    x, w = (x.float() * 2.0 ** 100).to(dt), (w.float() * 2.0 ** 36).to(wdt)
+    want = formula(x, w, None, 8, SOFTMAX, True, 1.0)
+    assert bool(torch.isfinite(want[1]).all())
+    ids, sc = run(x, w, None, 8, SOFTMAX)
+    assert torch.equal(ids.long(), want[0])
+    assert bool(((sc.double() - want[1]).abs() <= 2.0 ** -24 * want[1]).all())  # logits lie far apart: shares are 1 and 0
+    b = torch.zeros(256)
+    b[want[0][:, 0].unique()] = -float("inf")  # an expert that the bias takes out stays out
+    ids, _ = run(x, w, b, 8, SIGMOID)
+    want = formula(x, w, b, 8, SIGMOID, False, 1.0)
+    assert torch.equal(ids.long(), want[0])
