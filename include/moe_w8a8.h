@@ -502,7 +502,8 @@ typedef struct {
  * The choice is that of 64-bit sums, whatever the types, so that it does not
  * depend on the order of a sum. The weights come from 64-bit logits too, or, in
  * large products of x and weight both BF16, both FP16, or x BF16 and weight
- * FP32, from logits whose sums of 64 products are in fp32.
+ * FP32 (softmax with a bias apart), from logits whose sums of 64 products are
+ * in fp32.
  *
  *  x              [T, H]
  *  weight         [E, H]

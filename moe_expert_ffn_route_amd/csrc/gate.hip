@@ -14,8 +14,8 @@
 //     which is no less than the sum of |x * w|, bounds how far such a logit is
 //     off. Where the bound leaves open which of two experts comes first, the
 //     choice kernel computes the logits of those experts again, in fp64.
-//   - small products and other types: fp64 MFMA throughout (products are exact
-//     in it).
+//   - small products, other types, and softmax with a bias: fp64 MFMA
+//     throughout (products are exact in it).
 //
 // Two launches: the logits, in up to kMaxSplit parts of H, into the
 // workspace; and one wave per token, which adds the parts in order, for
@@ -585,8 +585,8 @@ __global__ __launch_bounds__(kBlock) void choose_kernel(GateArgs a, int parts, d
         }
     }
     // How far two choice values may be off together. Slopes: sigmoid 1/4,
-    // sqrt(softplus) under 1/3; a softmax share moves by at most twice its
-    // logits' error.
+    // sqrt(softplus) under 1/3. (Softmax goes by the logit: with a bias its
+    // logits are in 64 bits.)
     double off = 0.0;
     uint32_t overflowed = 0;  // bit j: expert j * 64 + lane
     if constexpr (FAST) {
@@ -595,7 +595,7 @@ __global__ __launch_bounds__(kBlock) void choose_kernel(GateArgs a, int parts, d
         for (int j = 0; j < NPL; ++j) wn = n[j] > wn ? n[j] : wn;
         wn = __uint_as_float(wave_max_int<uint32_t>(__float_as_uint(wn), 0u));
         off = 2.0 * (gamma * 1.05 * sqrt((xn + kTinySquares) * (wn + kTinySquares)) + kTiny);
-        if (a.bias) off *= SCORE == MOE_SCORE_SOFTMAX ? 2.5 : SCORE == MOE_SCORE_SIGMOID ? 0.25 : 0.34;
+        if (a.bias) off *= SCORE == MOE_SCORE_SIGMOID ? 0.25 : 0.34;
         // and the 64-bit roundings of score + bias
         float bm = 1.0f;
 #pragma unroll
@@ -795,9 +795,14 @@ hipError_t launch(const GateArgs &a, hipStream_t s) {
     GateArgs g = a;
     g.x_norms = reinterpret_cast<float *>(a.logits + static_cast<size_t>(p.parts) * a.T * a.E);
     g.w_norms = g.x_norms + static_cast<size_t>(p.parts) * a.T;
-    // whether the logits are bounded fp32 sums
-    const bool fast = !p.few && (kPlanes<T, W> == 1 ||
-                                 (kPlanes<T, W> > 1 && static_cast<int64_t>(a.T) * a.E * a.H > kPlanesFrom));
+    // Whether the logits are bounded fp32 sums. Not for softmax with a bias:
+    // what is ordered there, share + bias, holds the sum over all experts, so
+    // that exact logits of the doubtful ones alone would not decide (a bias can
+    // cancel the difference of two shares to any number of bits). T 4096, E
+    // 256, H 4096 takes 157 us so (72 without certainty), T 512 31 (39).
+    const bool fast = !p.few && !(a.score == MOE_SCORE_SOFTMAX && a.bias) &&
+                      (kPlanes<T, W> == 1 ||
+                       (kPlanes<T, W> > 1 && static_cast<int64_t>(a.T) * a.E * a.H > kPlanesFrom));
     if (p.few) {
         hipLaunchKernelGGL((logits_few_kernel<T, W>), dim3(p.e_tiles, p.parts, p.t_tiles), dim3(kBlock), 0, s, g,
                            p.chunks_per_part);
@@ -807,7 +812,7 @@ hipError_t launch(const GateArgs &a, hipStream_t s) {
         if (fast)
             hipLaunchKernelGGL((logits_many_kernel<T, W, kPlanes<T, W>>), grid, dim3(kBlock), 0, s, g,
                                p.chunks_per_part, p.e_tiles, units);
-        else if constexpr (!kFast<T, W>)
+        else
             hipLaunchKernelGGL((logits_many_kernel<T, W, 0>), grid, dim3(kBlock), 0, s, g, p.chunks_per_part,
                                p.e_tiles, units);
     }

@@ -332,3 +332,26 @@ def test_finite_inputs_whose_fp32_sums_overflow(T, dt, wdt, sign):
     ids, _ = run(x, w, b, 8, SIGMOID)
     want = formula(x, w, b, 8, SIGMOID, False, 1.0)
     assert torch.equal(ids.long(), want[0])
+
+
+@pytest.mark.parametrize("T,dt,wdt", [(5, BF, BF), (300, BF, BF), (300, FP, FP), (600, BF, F32)], ids=str)
+def test_softmax_shares_whose_difference_the_bias_all_but_cancels(T, dt, wdt):
+    """Two experts of unlike shares p0 > p1 and biases that differ by p0 - p1, but for 2e-11 either way: every other
+    expert's logit counts, through the softmax's sum, in which comes first. 64-bit values are 1e-15 apart at most."""
+    x, w, _ = make(T, 4096, 256, dt, wdt, seed=43)
+    x[:] = x[0].clone()
+    n = float((x[0].double() ** 2).sum())
+    w[3], w[200] = (x[0].float() * (8.0 / n)).to(wdt), (x[0].float() * (7.4 / n)).to(wdt)
+    p = torch.softmax(torch.mv(w.double(), x[0].double()), 0)
+    d = float(p[3] - p[200])
+    assert d > 0.1
+    for side in (-1, 1):
+        b = torch.zeros(256)
+        b[200] = d + 2e-5
+        b[3] = float(b[200].double()) - d + side * 2e-11
+        gap = float(p[3] + b[3].double() - p[200] - b[200].double())
+        assert 1e-11 < side * gap < 4e-11
+        ids, sc = run(x, w, b, 2)
+        assert torch.equal(ids, torch.tensor([[3, 200] if side > 0 else [200, 3]], dtype=torch.int32).expand(T, 2))
+        check((ids, sc), formula(x, w, b, 2, SOFTMAX, True, 1.0), x, w)
+        assert bool((run(x, w, b, 1)[0] == (3 if side > 0 else 200)).all())
