@@ -512,8 +512,10 @@ typedef struct {
  *  expert_scales  fp32 [T, K]
  *  workspace      >= moe_w8a8_gate_workspace_size() bytes, 256-byte aligned
  *
- * Where fewer than K experts are left (by the bias, or because a logit is
- * NaN), the places that remain get id -1, which the block drops, and weight 0.
+ * An expert whose logit is NaN is taken as not there, by the softmax too, and
+ * so is one whose logit is -infinity where bias is NULL. Where fewer than K
+ * experts are left, by the bias or so, the places that remain get id -1, which
+ * the block drops, and weight 0.
  * x and weight are 16-byte aligned, the others 4. The outputs overlap nothing.
  * The workspace's size does not fall as T or E grows: one that is made for the
  * largest batch serves every smaller one.

@@ -516,7 +516,7 @@ __device__ __forceinline__ bool row_is_zero(const GateArgs &a, const T *x, int l
 }
 
 // Score of a logit (softmax: before the division by the sum; m = the largest
-// logit).
+// logit, finite). NaN of NaN.
 template <int SCORE>
 __device__ __forceinline__ double score_of(double l, double m) {
     if constexpr (SCORE == MOE_SCORE_SOFTMAX) return exp(l - m);
@@ -634,12 +634,17 @@ __global__ __launch_bounds__(kBlock) void choose_kernel(GateArgs a, int parts, d
             }
             top = value_of(wave_max(k));
             total = 0.0;
+            if (top > __DBL_MAX__) {  // the infinite ones share alike, the others have nothing
+#pragma unroll
+                for (int j = 0; j < NPL; ++j) l[j] = l[j] > __DBL_MAX__ ? __DBL_MAX__ : l[j];
+                top = __DBL_MAX__;
+            }
         }
         int64_t c[NPL];  // what the choice goes by
 #pragma unroll
         for (int j = 0; j < NPL; ++j) {
             s[j] = score_of<SCORE>(l[j], top);
-            if (SCORE == MOE_SCORE_SOFTMAX) total += s[j];
+            if (SCORE == MOE_SCORE_SOFTMAX && s[j] == s[j]) total += s[j];  // an expert with a NaN logit is not there
         }
         if (SCORE == MOE_SCORE_SOFTMAX) total = wave_sum(total);
 #pragma unroll

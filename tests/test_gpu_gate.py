@@ -355,3 +355,42 @@ def test_softmax_shares_whose_difference_the_bias_all_but_cancels(T, dt, wdt):
         assert torch.equal(ids, torch.tensor([[3, 200] if side > 0 else [200, 3]], dtype=torch.int32).expand(T, 2))
         check((ids, sc), formula(x, w, b, 2, SOFTMAX, True, 1.0), x, w)
         assert bool((run(x, w, b, 1)[0] == (3 if side > 0 else 200)).all())
+
+
+@pytest.mark.parametrize("T", [9, 300])
+@pytest.mark.parametrize("bias", [False, True], ids=["logit", "bias"])
+@pytest.mark.parametrize("normalize", [False, True], ids=["plain", "normalized"])
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID, SQRTSP], ids=["softmax", "sigmoid", "sqrtsoftplus"])
+def test_nan_logit_takes_its_own_expert_out(score, normalize, bias, T):
+    """As a row of weights that was never filled gives: the other experts are chosen and weighted as if it were not there."""
+    x, w, b = make(T, 4096, 256, bias=bias, seed=47)
+    rest = [e for e in range(256) if e not in (17, 130)]
+    w[17], w[130, 40] = float("nan"), float("nan")
+    ids, sc = run(x, w, b, 6, score, normalize)
+    want, v = formula(x, w[rest], None if b is None else b[rest], 6, score, normalize, 1.0)
+    check((ids, sc), (torch.tensor(rest)[want], v), x, w[rest])
+    w3 = w.clone()
+    w3[:] = float("nan")
+    w3[:3] = w[:3]
+    ids, sc = run(x, w3, b, 6, score, normalize)
+    assert bool((ids[:, 3:] == -1).all()) and bool((sc[:, 3:] == 0).all())
+    want, v = formula(x, w[:3], None if b is None else b[:3], 3, score, normalize, 1.0)
+    check((ids[:, :3], sc[:, :3]), (want, v), x, w[:3])
+
+
+@pytest.mark.parametrize("T", [9, 300])
+@pytest.mark.parametrize("dt,wdt", [(BF, BF), (BF, F32)], ids=["bf16", "fp32-w"])
+def test_infinite_logit_comes_first(T, dt, wdt):
+    x, w, b = make(T, 4096, 256, dt, wdt, bias=True, seed=53)
+    x[:, 5] = x[:, 5].abs() + 1
+    w[9, 5] = float("inf")
+    w[77, 5] = -float("inf")
+    l = torch.nan_to_num(x.double() @ w.double().t(), posinf=1e300, neginf=-1e300)
+    for bias, score in ((None, SOFTMAX), (b, SOFTMAX), (None, SIGMOID)):
+        ids, sc = run(x, w, bias, 4, score)
+        s = torch.softmax(l, 1) if score == SOFTMAX else torch.sigmoid(l)
+        want = torch.sort(l if bias is None else s + bias.double(), dim=1, descending=True, stable=True)[1][:, :4]
+        v = s.gather(1, want)
+        assert torch.equal(ids.long(), want) and bool((want[:, 0] == 9).all())
+        v = v / v.sum(1, keepdim=True)
+        assert bool(((sc.double() - v).abs() <= 2.0 ** -20 * v + 1e-45).all())
