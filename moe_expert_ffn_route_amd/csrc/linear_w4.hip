@@ -6,12 +6,16 @@
 // D covers 16 output rows and 16 tokens, lane l holding rows 4 * (l / 16) ..+3
 // of token l % 16. The 4-bit codes go to the matrix operand in few operations
 // per eight of them:
-//   fp16:  0x6400 | c is 1024 + c; minus (1024 + z), exact
-//   bf16:  0x4300 | c is 128 + c, exact; the group's sum then carries
-//          (128 + z) * sum(x), which is subtracted with the sum of x that one
+//   fp16:  0x5800 | c << 3 is 128 + c; minus (128 + z), exact
+//   bf16:  0x4180 | c << 3 is 16 + c, exact; the group's sum then carries
+//          (16 + z) * sum(x), which is subtracted with the sum of x that one
 //          more MFMA with a matrix of ones makes (per token tile, shared by
-//          the weight tiles). bf16 has no packed subtraction here. The fp32
-//          cancellation costs at most a factor of about 2^5 of fp32 rounding.
+//          the weight tiles). bf16 has no packed subtraction here. 16 is the
+//          smallest base with all codes in one binade: products of up to 31 x
+//          stand for up to 15 x, one bit of fp32. (128 + c, three more: T 512,
+//          N 8192, K 4096, outputs that are not the rounded 64-bit value:
+//          0.12 %, with 16 + c 0.016 %, an fp32 product of whole rows 0.072 %.)
+//   For both, codes are packed rotated by 3, so that c << 3 costs no shift.
 //   int8:  codes are packed as the nibble of c - 8; kept in a byte's high half
 //          it is 16 * (c - 8) as int8. Zero points other than 8 are subtracted
 //          with the int32 sum of x, as for bf16; the 16 divides out at the end,
@@ -75,7 +79,7 @@ __global__ __launch_bounds__(256) void pack_codes_kernel(const uint8_t *__restri
         const int nib = i8 ? (j & 3) * 2 + (j >> 2) : (j >> 1) + 4 * (j & 1);
         w |= (i8 ? c ^ 8u : c) << (4 * nib);
     }
-    dst[o] = w;
+    dst[o] = i8 ? w : w << 3 | w >> 29;
 }
 
 // One thread per (tile, group, row).
@@ -154,12 +158,12 @@ struct GroupScale {
         if (Z) z = X == 1 ? zero[o + r] : *reinterpret_cast<const uint32_t *>(zero + o + kq * 4);
     }
     __device__ __forceinline__ v2h half_zero() const {
-        const _Float16 h = static_cast<_Float16>(Z ? 1024.0f + static_cast<float>(z) : 1032.0f);
+        const _Float16 h = static_cast<_Float16>(Z ? 128.0f + static_cast<float>(z) : 136.0f);
         return v2h{h, h};
     }
     // what one unit of the sum of x takes off the group's product of row i
     __device__ __forceinline__ float offset(int i) const {
-        return Z ? 128.0f + static_cast<float>((z >> (8 * i)) & 255u) : 136.0f;
+        return Z ? 16.0f + static_cast<float>((z >> (8 * i)) & 255u) : 24.0f;
     }
     __device__ __forceinline__ int offset8(int i) const {
         return Z ? static_cast<int>((z >> (8 * i)) & 255u) * 16 - 128 : 0;
@@ -172,9 +176,9 @@ template <int X>
 struct ExpandConst {
     uint32_t mask, base;
     __device__ __forceinline__ ExpandConst() {
-        asm("s_mov_b32 %0, 0x000F000F" : "=s"(mask));
-        if (X == 1) asm("v_mov_b32 %0, 0x64006400" : "=v"(base));
-        else asm("v_mov_b32 %0, 0x43004300" : "=v"(base));
+        asm("s_mov_b32 %0, 0x00780078" : "=s"(mask));
+        if (X == 1) asm("v_mov_b32 %0, 0x58005800" : "=v"(base));
+        else asm("v_mov_b32 %0, 0x41804180" : "=v"(base));
     }
 };
 
@@ -184,7 +188,8 @@ __device__ __forceinline__ v4i expand16(const ExpandConst<X> &c, uint32_t w, v2h
     v4i a;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        uint32_t u = ((w >> (4 * e)) & c.mask) | c.base;
+        // the last pair's upper code reaches around the word's end
+        uint32_t u = ((e < 3 ? w >> (4 * e) : __builtin_rotateright32(w, 12)) & c.mask) | c.base;
         if (X == 1) u = __builtin_bit_cast(uint32_t, __builtin_bit_cast(v2h, u) - zh);
         a[e] = static_cast<int>(u);
     }

@@ -217,3 +217,35 @@ def test_weights_past_32_bits():
         c = dict(code=torch.stack((b & 15, b >> 4), -1).view(64, K), scale=scale[rows].cpu(), zero=None, x=x, xs=None,
                  bias=None)
         check(c, G, False, out[:, rows].cpu().contiguous())
+
+
+@pytest.mark.parametrize("T,N,K,G", [(1, 48, 1024, 128), (7, 4100, 512, 128), (20, 260, 320, 64), (50, 130, 416, 32),
+                                     (130, 8300, 512, 128), (600, 2000, 320, 64), (515, 2320, 160, 32)])
+@pytest.mark.parametrize("zeros", [False, True], ids=["sym", "zeros"])
+@pytest.mark.parametrize("act", [BF, FP], ids=["bf16", "fp16"])
+def test_whole_numbers_come_out_exactly(T, N, K, G, zeros, act):
+    """Whole x up to 2^24 / (32 G), positive as activations may be, and small whole outputs: every partial sum of
+    (16 + code) * x and of 31 * x is a whole number under 2^24, so fp32 holds all of them and nothing may be lost."""
+    g = torch.Generator().manual_seed(3 * T + N + K + G)
+    top = 2 ** 24 // (32 * G)
+    x = torch.randint(top // 2, top, (T, K // 2), generator=g).float()
+    mant = {BF: 2.0 ** 8, FP: 2.0 ** 11}[act]
+    step = torch.exp2(torch.floor(torch.log2(x)) + 1) / mant  # whole, or x is exact already
+    x = torch.where(step > 1, torch.floor(x / step) * step, x)
+    x = torch.stack((x, x), -1).view(T, K)  # equal neighbours: opposite codes cancel
+    x[:, 0::G] = torch.randint(1, 4, (T, K // G), generator=g).float()
+    x[:, 1::G] = 1.0
+    zero = torch.randint(5, 12, (N, K // G), generator=g, dtype=torch.uint8) if zeros else None
+    z = zero.repeat_interleave(G, 1) if zeros else torch.full((N, K), 8, dtype=torch.uint8)
+    d = torch.randint(0, 5, (N, K // 2), generator=g).to(torch.int16)
+    code = z.to(torch.int16) + torch.stack((d, -d), -1).view(N, K)
+    few = torch.zeros(K, dtype=torch.bool)
+    few[0::G], few[1::G] = True, True
+    live = (torch.arange(K // G) == K // G - 1).repeat_interleave(G)  # one group whose pair does not cancel
+    code[:, few & live] = (z.to(torch.int16) + torch.randint(0, 3, (N, K), generator=g, dtype=torch.int16))[:, few & live]
+    code[:, few & ~live] = z.to(torch.int16)[:, few & ~live]
+    c = dict(code=code.to(torch.uint8), scale=torch.ones(N, K // G), zero=zero, x=x.to(act), xs=None, bias=None)
+    assert torch.equal(c["x"].float(), x) and bool((code >= 0).all()) and bool((code <= 15).all())
+    want = torch.mm(x.double(), (code.double() - z.double()).t().contiguous())
+    assert float(want.abs().max()) <= 8 and float((x.view(T, K // G, G).sum(-1)).max()) * 31 < 2 ** 24
+    assert torch.equal(run(c, G).double(), want)
