@@ -45,11 +45,14 @@ constexpr int kMaxSplit = 8;
 // truncates): n * 2^-23 of the sum of magnitudes, which Cauchy's inequality
 // bounds by the norms.
 constexpr double kUnit = 0x1p-23;
-// Numbers under the smallest normal fp32 may be dropped. Products: at most
-// 16384 of them. Squares: the norms' (8192 sums of two at a time) may lack as
-// much, which also covers inputs that are dropped: 2^-126 of each is under
-// kUnit * 2^-56.
-constexpr double kTiny = 0x1p-112, kTinySquares = 0x1p-112;
+// Numbers under the smallest normal fp32 may be dropped. Products, and sums of
+// them: at most 16384 of each for every plane of W. Squares: the norms' (at
+// most 16384 of them) may lack their share of it, which also covers inputs
+// that are dropped: 2^-126 of each is under kUnit * 2^-56.
+constexpr int kMaxPlanes = 3, kMaxTerms = 16384;
+constexpr double kTiny = 0x1p-109, kTinySquares = 0x1p-112;
+static_assert(kTiny >= 2.0 * kMaxPlanes * kMaxTerms * 0x1p-126 && kTinySquares >= kMaxTerms * 0x1p-126,
+              "what is dropped is inside the bound");
 
 // Eight elements from h = k of a row of H. WHOLE: they are known to be there
 // (no branch, so that loads can be issued in a row).
@@ -78,7 +81,7 @@ constexpr bool kFast<Fp16, Fp16> = true;
 template <typename T, typename W>
 constexpr int kPlanes = kFast<T, W> ? 1 : 0;
 template <>
-constexpr int kPlanes<Bf16, float> = 3;
+constexpr int kPlanes<Bf16, float> = kMaxPlanes;
 // Three planes pay where the fp64 MFMA is the time: bf16 x, fp32 W, E 256, H
 // 4096, logits and choice together, planes / fp64: T 4096 92 / 177 us, T 512
 // 30 / 28 (the doubtful choices cost 6 us).
@@ -325,7 +328,7 @@ struct Stage {  // kTileRows rows of kChunk elements
             float f[4];
             __builtin_memcpy(f, &v[i], 16);
 #pragma unroll
-            for (int p = 0; p < 3; ++p) {
+            for (int p = 0; p < kMaxPlanes; ++p) {
                 uint32_t b[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
