@@ -346,12 +346,16 @@ def _native():
     return _pycall
 
 
+def _tensor(t, name: str) -> None:
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: expected a tensor, got {type(t).__name__}")
+
+
 def _call(where: str, fn, first, stream, *args) -> None:
     """fn(*args, stream handle) with the device of tensor `first` current; the
     stream defaults to that device's current one (its handle: the stream
     object costs a microsecond)."""
-    if not isinstance(first, torch.Tensor):
-        raise ValueError(f"{where}: expected a tensor, got {type(first).__name__}")
+    _tensor(first, where)
     device = first.get_device()
     if device < 0:  # refused by fn
         handle = 0
@@ -369,6 +373,7 @@ def _arg(t, name: str, dtype, numel: int, device: int) -> Optional[int]:
     """The device pointer of an argument of `numel` elements (None: NULL)."""
     if t is None:
         return None
+    _tensor(t, name)
     if t.dtype is not dtype or t.numel() != numel:
         raise ValueError(f"{name}: expected {numel} elements of {dtype}, got {tuple(t.shape)} of {t.dtype}")
     if t.get_device() != device or device < 0:
@@ -430,12 +435,16 @@ def moe_w8a8_gate(dims: GateDims, x, weight, bias=None, expert_ids=None, expert_
     """Router: top-k experts of x [T, H] and their weights. Returns
     (expert_ids int32 [T, K], expert_scales fp32 [T, K]), allocated if None,
     as is the workspace."""
-    if expert_ids is None:
-        expert_ids = _empty((dims.num_tokens, dims.topk), torch.int32, x.device, stream)
-    if expert_scales is None:
-        expert_scales = _empty((dims.num_tokens, dims.topk), torch.float32, x.device, stream)
-    if workspace is None:
-        workspace = _empty(max(256, moe_w8a8_gate_workspace_size(dims)), torch.uint8, x.device, stream)
+    if expert_ids is None or expert_scales is None or workspace is None:
+        _tensor(x, "x")
+        n = moe_w8a8_gate_workspace_size(dims)  # dims that no buffer can have raise here
+        if expert_ids is None:
+            expert_ids = _empty((dims.num_tokens, dims.topk), torch.int32, x.device, stream)
+        if expert_scales is None:
+            expert_scales = _empty((dims.num_tokens, dims.topk), torch.float32, x.device, stream)
+        if workspace is None:
+            workspace = _empty(max(256, n), torch.uint8, x.device, stream)
+    _tensor(workspace, "workspace")
     _call("moe_w8a8_gate", _native().gate, x, stream, dims, x, weight, bias, expert_ids, expert_scales, workspace,
           workspace.numel())
     return expert_ids, expert_scales
@@ -458,6 +467,7 @@ def moe_w8a8_pack_weights_w4(dims: LinearW4Dims, codes, scale, zero=None, dst=No
     """Pack 4-bit weights (codes uint8 [N, K/2], scale fp32 [N, K/group], zero
     uint8 [N, K/group] if has_zeros) for moe_w8a8_linear_w4 with these dims
     (num_tokens aside). Returns dst (uint8, allocated if None)."""
+    _tensor(codes, "codes")
     nbytes, dev = moe_w8a8_packed_w4_bytes(dims), codes.get_device()
     if dst is None:
         dst = _empty(nbytes, torch.uint8, codes.device, stream)
@@ -474,6 +484,8 @@ def moe_w8a8_linear_w4(dims: LinearW4Dims, x, weight, x_scale=None, bias=None, o
     with packed 4-bit weights. Returns out (bf16, fp16 for fp16 x; [T, N], or
     [T, N/2] when gated), allocated if None."""
     if out is None:
+        _tensor(x, "x")
+        moe_w8a8_packed_w4_bytes(dims)  # dims that no buffer can have raise here
         width = dims.out_features // 2 if dims.gated else dims.out_features
         out = _empty((dims.num_tokens, width), torch.float16 if dims.act_dtype == MOE_DTYPE_FP16 else torch.bfloat16,
                      x.device, stream)

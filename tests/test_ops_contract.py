@@ -235,3 +235,27 @@ def test_binding_refuses_host_tensors_and_misfits(lib):
         moe.moe_w8a8_norm_quant(d, x.data_ptr(), y=x)
     with pytest.raises(ValueError, match="dims"):
         moe.moe_w8a8_norm_quant(moe.make_gate_dims(2, 64, 4, 2), x, y=x)
+
+
+def test_binding_refuses_what_is_no_tensor_where_outputs_are_allocated(lib):
+    g, ld = moe.make_gate_dims(2, 64, 4, 2), moe.make_linear_w4_dims(2, 16, 64, group=64)
+    for x in (None, 4096, [1.0]):
+        with pytest.raises(ValueError, match="expected a tensor"):
+            moe.moe_w8a8_gate(g, x, x)
+        with pytest.raises(ValueError, match="expected a tensor"):
+            moe.moe_w8a8_linear_w4(ld, x, x)
+        with pytest.raises(ValueError, match="expected a tensor"):
+            moe.moe_w8a8_pack_weights_w4(ld, x, x)
+    x = torch.zeros(2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="expected a tensor"):
+        moe.moe_w8a8_gate(g, x, x, workspace=4096)
+    with pytest.raises(ValueError, match="expected a tensor"):
+        moe.moe_w8a8_pack_weights_w4(ld, torch.zeros(16, 32, dtype=torch.uint8), 4096)
+
+
+def test_binding_reports_bad_dims_where_outputs_are_allocated(lib):
+    x = torch.zeros(2, 64, dtype=torch.bfloat16)
+    with pytest.raises(moe.MoeError):
+        moe.moe_w8a8_gate(moe.make_gate_dims(-1, 64, 4, 2), x, x)
+    with pytest.raises(moe.MoeError):
+        moe.moe_w8a8_linear_w4(moe.make_linear_w4_dims(-1, 16, 64, group=64), x, x)
