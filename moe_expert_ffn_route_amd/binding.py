@@ -341,7 +341,10 @@ def _native():
     global _pycall
     if _pycall is None:
         library()
-        from . import _pycall as module
+        try:
+            from . import _pycall as module
+        except ImportError as e:
+            raise ImportError(f"_pycall.so ({e}): build it with `python -m moe_expert_ffn_route_amd.build`") from e
         _pycall = module
     return _pycall
 

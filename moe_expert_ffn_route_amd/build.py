@@ -3,6 +3,9 @@ in parallel, then a link), and _pycall.so, the Python entry of the operators
 around the block (host code, against the installed torch).
 
     python -m moe_expert_ffn_route_amd.build
+    python moe_expert_ffn_route_amd/build.py --library
+
+The second makes the C library alone and needs hipcc, but neither g++ nor torch.
 
 Flags: -O3; -ffp-contract=off so every fp32 multiply and add of the epilogues
 is a separately rounded IEEE operation (no FMA contraction); packed-fp32
@@ -55,8 +58,9 @@ def _run(cmd, verbose):
         print(errs, file=sys.stderr)
 
 
-def build(verbose: bool = False, jobs: int = 0) -> str:
-    """Compile every HIP source into the shared library (always rebuilds):
+def build(verbose: bool = False, jobs: int = 0, python: bool = True) -> str:
+    """Compile every HIP source into the shared library (always rebuilds) and,
+    if `python`, the Python entry against it:
     one hipcc per source, in parallel, then one link. Every kernel is launched
     from the source that defines it, so no relocatable device code is needed."""
     import shutil
@@ -74,13 +78,14 @@ def build(verbose: bool = False, jobs: int = 0) -> str:
         tmp = LIB + f".tmp{os.getpid()}"
         _run([HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", *objs, "-o", tmp], verbose)
         os.replace(tmp, LIB)
-        tmp = PYCALL + f".tmp{os.getpid()}"
-        _run(_pycall_cmd(tmp), verbose)
-        os.replace(tmp, PYCALL)
+        if python:
+            tmp = PYCALL + f".tmp{os.getpid()}"
+            _run(_pycall_cmd(tmp), verbose)
+            os.replace(tmp, PYCALL)
     finally:
         shutil.rmtree(obj_dir, ignore_errors=True)
     return LIB
 
 
 if __name__ == "__main__":
-    print(build(verbose=True))
+    print(build(verbose=True, python="--library" not in sys.argv[1:]))

@@ -259,3 +259,12 @@ def test_binding_reports_bad_dims_where_outputs_are_allocated(lib):
         moe.moe_w8a8_gate(moe.make_gate_dims(-1, 64, 4, 2), x, x)
     with pytest.raises(moe.MoeError):
         moe.moe_w8a8_linear_w4(moe.make_linear_w4_dims(-1, 16, 64, group=64), x, x)
+
+
+def test_missing_python_entry_says_how_to_build_it(lib, monkeypatch):
+    import sys
+    monkeypatch.setattr(binding, "_pycall", None)
+    monkeypatch.setitem(sys.modules, "moe_expert_ffn_route_amd._pycall", None)
+    monkeypatch.delattr(moe, "_pycall", raising=False)
+    with pytest.raises(ImportError, match="python -m moe_expert_ffn_route_amd.build"):
+        moe.moe_w8a8_norm_quant(moe.make_norm_dims(2, 64), torch.zeros(2, 64, dtype=torch.bfloat16))
