@@ -394,3 +394,15 @@ def test_infinite_logit_comes_first(T, dt, wdt):
         assert torch.equal(ids.long(), want) and bool((want[:, 0] == 9).all())
         v = v / v.sum(1, keepdim=True)
         assert bool(((sc.double() - v).abs() <= 2.0 ** -20 * v + 1e-45).all())
+
+
+@pytest.mark.parametrize("T,H,E,K", [(1, 4096, 256, 8), (16, 1000, 128, 4), (64, 4096, 256, 8), (200, 2048, 500, 8)])
+@pytest.mark.parametrize("dt,wdt", [(BF, BF), (FP, FP), (BF, F32)], ids=str)
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID, SQRTSP], ids=["softmax", "sigmoid", "sqrtsoftplus"])
+def test_weights_of_small_products_are_rounded_once(T, H, E, K, dt, wdt, score):
+    """Up to 2^28 products T * E * H the logits are in 64 bits whatever the types: 2^-24 relative, and 1e-10."""
+    x, w, b = make(T, H, E, dt, wdt, bias=True, seed=59)
+    want, v = formula(x, w, b, K, score, True, 2.5)
+    ids, sc = run(x, w, b, K, score, route_scale=2.5)
+    assert torch.equal(ids.long(), want)
+    assert bool(((sc.double() - v).abs() <= (2.0 ** -24 + 1e-10) * v).all())

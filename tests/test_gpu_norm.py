@@ -216,3 +216,24 @@ def test_offsets_past_32_bits():
     moe.moe_w8a8_norm_quant(moe.make_norm_dims(T, H, dtype=F32), x, q=q, q_scale=s)
     ref = run(x[-1:].cpu(), None, None, Q8, 0)
     assert torch.equal(q[-1:].cpu(), ref["q"]) and bool((q[:-1:997] == 127).all())
+
+
+@pytest.mark.parametrize("group", [0, 128])
+@pytest.mark.parametrize("T,H", [(4, 1024), (600, 5120)])
+def test_e4m3_codes_against_64_bits(T, H, group):
+    """Rows over the amax floor and under it. The value that is rounded is off by at most 60 u, so its code lies between
+    the codes of the 64-bit value moved by 64 u (one more rounding, to fp32) either way."""
+    x, res, w = make(T, H, BF, BF, True, seed=61)
+    eps = 100.0 if group else 1e4  # amax of groups on both sides of 1, of rows under it
+    for amax_eps in (1e-6, 1.0):
+        out = run(x, res, w, E4, group, eps=eps, amax_eps=amax_eps)
+        r = x.double() + res.double()
+        y = r * w.double() / torch.sqrt((r * r).mean(1, keepdim=True) + eps)
+        n = group or H
+        a = y.view(T, H // n, n).abs().amax(-1, keepdim=True)
+        assert bool((a < amax_eps).any()) == (amax_eps == 1.0) and (amax_eps < 1 or group == 0 or bool((a > 1).any()))
+        v = y.view(T, H // n, n) / (torch.clamp(a, min=amax_eps) / 448)
+        code = lambda f: (v * (1 + f * v.sign() * 64 * U)).float().to(torch.float8_e4m3fn).float()  # noqa: E731
+        got = out["q"].float().view(T, H // n, n)
+        assert float(got.abs().max()) > 8
+        assert bool(((got >= code(-1)) & (got <= code(1))).all())
