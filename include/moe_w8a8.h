@@ -386,7 +386,9 @@ MOE_W8A8_API moe_status_t moe_w8a8_read_write_probe(const void *src, size_t src_
  * skips its own quantisation of x. Results are bit for bit those of
  * moe_w8a8_forward on any x whose codes and scales these are.
  *
- *  q_x      [T, H] codes: int8 (MOE_WEIGHT_INT8) or FP8 E4M3 (MOE_WEIGHT_MXFP4)
+ *  q_x      [T, H] codes: int8 (MOE_WEIGHT_INT8) or FP8 E4M3 (MOE_WEIGHT_MXFP4;
+ *           moe_w8a8_norm_quant makes them with MOE_QUANT_E4M3). Bytes do not
+ *           tell which they are: that is not checked
  *  x_scale  fp32 [T] (quant_mode 1) or [T, H / quant_group] (quant_mode 2);
  *           element i of token t stands for q_x[t][i] * its scale
  *
@@ -463,7 +465,8 @@ typedef struct {
  *  q, q_scale    [T, H] bytes, and fp32 [T] or [T, H / quant_group]; both NULL
  *                iff quant == MOE_QUANT_NONE
  *
- * Every pointer is 16-byte aligned (q_scale: 4). residual_out and y may be x
+ * Every pointer is 16-byte aligned (q_scale: 4, but 16 where
+ * moe_w8a8_forward_quantized is to take it). residual_out and y may be x
  * or residual themselves (not both the same one); any other overlap of an
  * output with anything is refused. At least one of y and q is given. A row
  * whose values are not finite, or whose squares' sum or r * weight * 448 leaves
@@ -499,8 +502,9 @@ typedef struct {
  *   weight of a chosen expert: s (without bias), over the chosen ones' sum if
  *   `normalize`, times route_scale; rounded once, to fp32
  *
- * The choice is that of 64-bit sums, whatever the types, so that it does not
- * depend on the order of a sum. The weights come from 64-bit logits too, or, in
+ * The choice is that of 64-bit sums, whatever the types: it changes with the
+ * order of a sum (with the batch, that is) only where two values are within
+ * the last bits of such sums. The weights come from 64-bit logits too, or, in
  * large products of x and weight both BF16, both FP16, or x BF16 and weight
  * FP32 (softmax with a bias apart), from logits whose sums of 64 products are
  * in fp32.

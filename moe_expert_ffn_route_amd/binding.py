@@ -296,13 +296,15 @@ def moe_w8a8_forward_quantized(dims: Dims, q_x, x_scale, expert_ids, expert_scal
                                check: bool = True) -> int:
     """moe_w8a8_forward on codes and scales that moe_w8a8_norm_quant (or the
     caller) made of x: q_x [T, H] int8 (float8_e4m3fn for FP4 weights), x_scale
-    fp32 [T] or [T, H / quant_group]. Runs on q_x's device. Returns the status
-    code; raises MoeError on failure when check=True."""
+    fp32 [T] or [T, H / quant_group]. int8 and uint8 tensors are also taken as
+    the raw bytes of E4M3 codes, so norm codes for FP4 weights have to be made
+    with MOE_QUANT_E4M3 (the default is int8). Runs on q_x's device. Returns
+    the status code; raises MoeError on failure when check=True."""
     T, H = dims.num_tokens, dims.hidden
     if isinstance(q_x, torch.Tensor):
         want = torch.float8_e4m3fn if dims.weight_format == MOE_WEIGHT_MXFP4 else torch.int8
         if q_x.numel() != T * H or q_x.dtype not in (want, torch.uint8, torch.int8):
-            raise ValueError(f"q_x: expected {T * H} codes of {want}, got {tuple(q_x.shape)} of {q_x.dtype}")
+            raise ValueError(f"q_x: expected {T * H} codes of {want} (or their bytes), got {tuple(q_x.shape)} of {q_x.dtype}")
         if q_x.is_cuda and q_x.get_device() != torch.cuda.current_device():
             with torch.cuda.device(q_x.get_device()):
                 return moe_w8a8_forward_quantized(

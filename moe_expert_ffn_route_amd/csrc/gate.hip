@@ -83,8 +83,9 @@ constexpr int kPlanes = kFast<T, W> ? 1 : 0;
 template <>
 constexpr int kPlanes<Bf16, float> = kMaxPlanes;
 // Three planes pay where the fp64 MFMA is the time: bf16 x, fp32 W, E 256, H
-// 4096, logits and choice together, planes / fp64: T 4096 92 / 177 us, T 512
-// 30 / 28 (the doubtful choices cost 6 us).
+// 4096, logits and choice together, planes / fp64: T 4096 64 / 153 us, T 1024
+// 34 / 48, T 520 31 / 47; under the border they gain 10 % (T 512 30 / 33, T 400
+// 29 / 32).
 constexpr int64_t kPlanesFrom = int64_t(1) << 29;  // products
 
 template <typename T>

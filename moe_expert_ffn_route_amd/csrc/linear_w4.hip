@@ -652,17 +652,18 @@ hipError_t launch_few(const LinearW4Args &a, hipStream_t s) {
     return hipGetLastError();
 }
 // Which kernel: linear_w4_many_kernel needs workgroups to fill the chip, the
-// other re-reads x for every 16 rows. In microseconds, few / many, bf16, groups
-// of 128, K 4096:
-//   T 32, N 28672: 33 / 34      T 40, N 28672: 44 / 35    T 40, N 14336: 26 / 33
-//   T 64, N 4096: 12 / 32       T 64, N 14336: 34.5 / 33  T 128, N 4096: 19 / 33
-//   T 256, N 4096: 34 / 34      T 300, N 4096: 40 / 34    T 512, N 8192: 129 / 53
-// so it goes by 16-row tiles x 64-token tiles. (int8 x: 26 / 41 at T 256, 23 /
-// 24 at T 300; groups of 32: 52 / 43 at T 300.)
+// other re-reads x for every 16 rows. In microseconds (in a captured graph),
+// few / many, bf16, groups of 128, K 4096:
+//   T 32, N 28672: 32 / 34      T 40, N 28672: 46 / 33    T 40, N 14336: 27 / 33
+//   T 64, N 4096: 12 / 33       T 64, N 14336: 33 / 33    T 128, N 4096: 18 / 33
+//   T 256, N 4096: 32 / 33      T 300, N 4096: 39 / 33    T 512, N 8192: 121 / 49
+// so it goes by 16-row tiles x 64-token tiles. (int8 x: 22 / 24 at T 256, 24 /
+// 24 at T 300; groups of 32: 52 / 42 at T 300.)
 // Two row tiles per workgroup halve what x costs, and four halve it again,
 // where there are enough of them and registers hold their scales: T 16, N
-// 28672, K 8192, one / two / four 46 / 39 / 33 us; T 64, N 8192, K 4096, int8
-// x, one / two 12 / 9.5 (bf16 19 / 25). N 4096 would fill half the chip.
+// 28672, K 8192, one / two / four 43 / 37 / 33 us; T 8, N 8192, K 4096, one /
+// two 6.7 / 5.9; T 64, N 8192, K 4096, int8 x, one / two 12.4 / 9.2 (bf16 19.6
+// / 20.5). N 4096 would fill half the chip.
 template <int X, int G, bool Z>
 hipError_t launch_tokens(const LinearW4Args &a, hipStream_t s) {
     const bool wide = G != 32 && a.n_tiles >= 512;
