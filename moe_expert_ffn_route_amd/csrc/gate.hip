@@ -533,10 +533,10 @@ __device__ __forceinline__ double score_of(double l, double m) {
 // and T and W do not matter.
 //
 // K choices in order. FAST, an expert that lies closer than `off` below a
-// choice is marked, and so is that choice, and so is every expert whose fp32
-// sum is not finite; the marked ones' logits are then computed in fp64 and the
-// choice is made again. An unmarked expert is further than `off` from all that
-// it was compared with, so its place stands.
+// choice is marked, and so is that choice (all experts, where an fp32 sum is
+// not finite); the marked ones' logits are then computed in fp64 and the choice
+// is made again. An unmarked expert is further than `off` from all that it was
+// compared with, so its place stands.
 //
 // A token is a chain of reductions, and few tokens are a single wave's
 // latency, most of it instruction fetches of a kernel that runs once: scores

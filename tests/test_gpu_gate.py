@@ -406,3 +406,14 @@ def test_weights_of_small_products_are_rounded_once(T, H, E, K, dt, wdt, score):
     ids, sc = run(x, w, b, K, score, route_scale=2.5)
     assert torch.equal(ids.long(), want)
     assert bool(((sc.double() - v).abs() <= (2.0 ** -24 + 1e-10) * v).all())
+
+
+@pytest.mark.parametrize("dt,wdt", [(BF, BF), (FP, FP), (BF, F32)], ids=str)
+@pytest.mark.parametrize("bias", [False, True], ids=["logit", "bias"])
+@pytest.mark.parametrize("score", [SOFTMAX, SIGMOID, SQRTSP], ids=["softmax", "sigmoid", "sqrtsoftplus"])
+def test_batch_does_not_change_the_experts(score, bias, dt, wdt):
+    """Every kernel that a batch size leads to, among them the split of fp32 weights (from 513 tokens on)."""
+    x, w, b = make(700, 4096, 256, dt, wdt, bias=bias, seed=67)
+    ids = run(x, w, b, 8, score)[0]
+    for n in (1, 17, 64, 257, 520):
+        assert torch.equal(run(x[:n], w, b, 8, score)[0], ids[:n])
