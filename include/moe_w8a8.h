@@ -580,6 +580,249 @@ MOE_W8A8_API moe_status_t moe_w8a8_linear_w4(const moe_w8a8_linear_w4_dims_t *di
                                              const float *x_scale, const void *weight, const float *bias, void *out,
                                              void *stream);
 
+/* ------------------------------------------------------------------------
+ * Between the block and the rest of a W8A8 program: dense products of the
+ * same model in 8-bit integers, the quantiser of an activation that comes
+ * from no norm, the norm that joins the block's outputs to the residual
+ * stream, and tokens sorted by expert (for other ranks' experts, or for a
+ * program's own) and back. The conventions at the top of this file hold; with
+ * num_tokens == 0 a call does nothing, whatever its pointers, but that
+ * moe_w8a8_dispatch writes its counts and offsets.
+ * ------------------------------------------------------------------------ */
+
+typedef struct {
+    int32_t num_tokens;   /* T in [0, 65536]                                          */
+    int32_t out_features; /* N in [1, 2^20]; even when gated                          */
+    int32_t in_features;  /* K in [1, 65536], any size; N * K <= about 2^34           */
+    int32_t out_dtype;    /* of out: BF16, FP16 or FP32                               */
+    int32_t gated;        /* 0: out [T, N]; 1: rows [0, N/2) are the gate, [N/2, N)   */
+                          /*   the up projection, out [T, N/2] = silu(gate) * up      */
+} moe_w8a8_linear_w8_dims_t;
+
+/*
+ * Dense product in 8-bit integers, the block's GEMM rule for one weight:
+ *
+ *   acc[t,n] = sum_k x[t,k] * codes[n,k]          (exact, int32)
+ *   o[t,n]   = (float(acc) * scale[n]) * x_scale[t] + bias[n]   (fp32)
+ *
+ * and out = o, or SwiGLU of its halves (gated), rounded once. x and x_scale
+ * are what moe_w8a8_norm_quant, moe_w8a8_join_norm and moe_w8a8_quant write
+ * with one scale per row. A token's outputs are the same bits in every batch.
+ *
+ * The weights are re-laid once, at load time, for one (N, K, gated);
+ * num_tokens and out_dtype may differ from call to call.
+ *
+ *  codes    int8 [N, K]
+ *  scale    fp32 [N]
+ *  dst      moe_w8a8_packed_w8_bytes() bytes, 16-byte aligned: for each 16
+ *           rows and 64 k (rows padded to a multiple of 16, k to one of 128,
+ *           with zeros) 1024 bytes, byte 16*l + b (l in [0,64), b in [0,16))
+ *           holding row l % 16, k 16*(l/16) + b; then the rows' scales in the
+ *           same order. Gated: a tile holds 8 gate rows and their 8 up rows
+ *           in turn
+ */
+MOE_W8A8_API moe_status_t moe_w8a8_packed_w8_bytes(const moe_w8a8_linear_w8_dims_t *dims, size_t *bytes);
+MOE_W8A8_API moe_status_t moe_w8a8_pack_weights_w8(const moe_w8a8_linear_w8_dims_t *dims, const int8_t *codes,
+                                                   const float *scale, void *dst, void *stream);
+/*
+ *  x        int8 [T, K], 16-byte aligned
+ *  x_scale  fp32 [T]
+ *  weight   from moe_w8a8_pack_weights_w8 with the same dims
+ *  bias     fp32 [N] or NULL
+ *  out      [T, N] or [T, N/2], 16-byte aligned, overlapping nothing
+ */
+MOE_W8A8_API moe_status_t moe_w8a8_linear_w8(const moe_w8a8_linear_w8_dims_t *dims, const int8_t *x,
+                                             const float *x_scale, const void *weight, const float *bias, void *out,
+                                             void *stream);
+
+typedef struct {
+    int32_t num_tokens;   /* T in [0, 65536]                                          */
+    int32_t hidden;       /* H in [1, 16384], any size                                */
+    int32_t dtype;        /* of x: BF16, FP16 or FP32                                 */
+    int32_t quant;        /* MOE_QUANT_INT8 or MOE_QUANT_E4M3                         */
+    int32_t quant_group;  /* 0: one scale per row; 64, 128 or 256 (dividing H): one   */
+                          /*   per row and group of that many consecutive elements    */
+    float amax_eps;       /* >= 1e-20: floor of an amax, as in moe_w8a8_dims_t        */
+} moe_w8a8_quant_dims_t;
+
+/*
+ * The block's quantiser for any activation: v = x * smooth (fp32), a' =
+ * max(max|v|, amax_eps) over the row or group, scale = a' / 127 (int8) or
+ * a' / 448 (E4M3), q = v / scale rounded to nearest even.
+ *
+ *  x        [T, H]
+ *  smooth   fp32 [H] or NULL (all ones)
+ *  q        [T, H] bytes
+ *  q_scale  fp32 [T] or [T, H / quant_group]
+ *
+ * x, smooth and q are 16-byte aligned, q_scale 4; the outputs overlap nothing.
+ * A row whose values are not finite, or leave fp32 when multiplied by 448, is
+ * unspecified; the other rows are not affected by it.
+ */
+MOE_W8A8_API moe_status_t moe_w8a8_quant(const moe_w8a8_quant_dims_t *dims, const void *x, const float *smooth, void *q,
+                                         float *q_scale, void *stream);
+
+typedef struct {
+    int32_t num_tokens;   /* T in [0, 65536]                                          */
+    int32_t hidden;       /* H in [1, 16384], any size                                */
+    int32_t dtype;        /* of block, share, residual, residual_out and y: BF16,     */
+                          /*   FP16 or FP32                                           */
+    int32_t weight_dtype; /* of post_weight, gate and weight: the same as dtype, or   */
+                          /*   FP32                                                   */
+    int32_t post_norm;    /* 1: the block's output is normed before it is added       */
+    int32_t gate_rows;    /* rows of gate: 0 (none), 1, or T                          */
+    int32_t quant;        /* MOE_QUANT_*: what q holds                                */
+    int32_t quant_group;  /* as in moe_w8a8_norm_dims_t                               */
+    float residual_scale; /* finite                                                   */
+    float branch_scale;   /* finite                                                   */
+    float post_eps;       /* >= 1e-30: added to the block's mean square               */
+    float rms_eps;        /* >= 1e-30: added to the stream's mean square              */
+    float amax_eps;       /* >= 1e-20                                                 */
+} moe_w8a8_join_norm_dims_t;
+
+/*
+ * What stands between the block's outputs and the next layer, in one pass:
+ *
+ *   b = block + share * share_scale[t]
+ *   n = (b * post_weight) / sqrt(mean(b^2) + post_eps)     (post_norm; else b)
+ *   r = residual * residual_scale + n * (gate * branch_scale)
+ *   residual_out = r rounded
+ *   y and the codes: those of moe_w8a8_norm_quant's norm of r (before its
+ *   rounding) by weight
+ *
+ * fp32 operations in this order, each rounded by itself; mean(b^2) is summed
+ * in fp64 and 1 / sqrt(...) rounded once. So r, and the codes as in
+ * moe_w8a8_norm_quant, do not depend on the order of a sum.
+ *
+ *  block         [T, H]
+ *  share         [T, H] or NULL; share_scale fp32 [T] or NULL (all ones; NULL
+ *                without share)
+ *  residual      [T, H] or NULL (zeros)
+ *  post_weight   [H] or NULL (all ones; NULL without post_norm)
+ *  gate          [H] or [T, H] as gate_rows says; NULL iff gate_rows == 0 (ones)
+ *  weight        [H] or NULL (all ones)
+ *  residual_out  [T, H] or NULL
+ *  y             [T, H] or NULL
+ *  q, q_scale    as in moe_w8a8_norm_quant
+ *
+ * Every pointer is 16-byte aligned (share_scale 4; q_scale 4, but 16 where
+ * moe_w8a8_forward_quantized is to take it). residual_out and y may be block,
+ * share or residual themselves (not both the same one); any other overlap of
+ * an output with anything is refused. At least one of residual_out, y and q is
+ * given. A row whose values are not finite, or leave fp32 in their squares'
+ * sum or multiplied by 448, is unspecified; the other rows are not affected.
+ */
+MOE_W8A8_API moe_status_t moe_w8a8_join_norm(const moe_w8a8_join_norm_dims_t *dims, const void *block,
+                                             const void *share, const float *share_scale, const void *residual,
+                                             const void *post_weight, const void *gate, const void *weight,
+                                             void *residual_out, void *y, void *q, float *q_scale, void *stream);
+
+typedef struct {
+    int32_t num_tokens;     /* T in [0, 65536]                                        */
+    int32_t topk;           /* K in [1, 16]                                           */
+    int32_t moe_expert_num; /* E in [1, 1024]                                         */
+    int32_t hidden;         /* H in [1, 16384], any size                              */
+    int32_t dtype;          /* of x and rows: BF16, FP16, FP32, or INT8 (any 8-bit    */
+                            /*   codes: bytes are moved)                              */
+    int32_t scale_groups;   /* fp32 scales of a row of x, in [0, 256]                 */
+    int32_t row_align;      /* 1, 2, 4, ... 256: an expert's rows begin at a multiple */
+} moe_w8a8_dispatch_dims_t;
+
+/*
+ * Tokens sorted by expert. Pair (t, k) is kept where expert_ids[t,k] lies in
+ * [0, E) and token t is active; an expert's pairs get consecutive rows in the
+ * order of (t, k), beginning at the next multiple of row_align:
+ *
+ *   expert_token_nums[e] = kept pairs of expert e
+ *   expert_offset[e] = its first row; expert_offset[E]: behind the last one,
+ *                rounded up to row_align too
+ *   row_of_pair[t,k] = the pair's row, -1 if it is dropped
+ *   pair_of_row[r] = the row's pair t*K + k, -1 where a row has none
+ *   rows[r] = x[t], row_scale[r] = x_scale[t]: zeros in the rows that fill an
+ *                expert's last row_align, left as they were behind
+ *                expert_offset[E]
+ *
+ * Ids follow moe_w8a8_gate (-1: none). Rows of one expert can be sent to its
+ * rank as they are, and a rank's rows run through moe_w8a8_forward_quantized
+ * with topk 1.
+ *
+ *  expert_ids         int32 [T, K]
+ *  x, rows            [T, H] and [R, H] with R from moe_w8a8_dispatch_rows (the
+ *                     most that T*K pairs can need); both NULL: maps only
+ *  x_scale, row_scale fp32 [T, scale_groups], [R, scale_groups]; NULL iff
+ *                     scale_groups == 0 or rows is NULL
+ *  x_active_mask      uint8 [T] (0 / non-0) or NULL = every token active
+ *  expert_token_nums  int32 [E];  expert_offset  int32 [E + 1]
+ *  row_of_pair        int32 [T, K];  pair_of_row  int32 [R]
+ *  workspace          >= moe_w8a8_dispatch_workspace_size() bytes (0 for small
+ *                     batches: then NULL will do), 256-byte aligned. The size
+ *                     does not fall as T or E grows
+ *
+ * x and rows are 16-byte aligned, the others 4. The outputs overlap nothing.
+ */
+MOE_W8A8_API moe_status_t moe_w8a8_dispatch_rows(const moe_w8a8_dispatch_dims_t *dims, int64_t *rows);
+MOE_W8A8_API moe_status_t moe_w8a8_dispatch_workspace_size(const moe_w8a8_dispatch_dims_t *dims, size_t *bytes);
+MOE_W8A8_API moe_status_t moe_w8a8_dispatch(const moe_w8a8_dispatch_dims_t *dims, const int32_t *expert_ids,
+                                            const void *x, const float *x_scale, const uint8_t *x_active_mask,
+                                            void *rows, float *row_scale, int32_t *expert_token_nums,
+                                            int32_t *expert_offset, int32_t *row_of_pair, int32_t *pair_of_row,
+                                            void *workspace, size_t workspace_bytes, void *stream);
+
+typedef struct {
+    int32_t num_tokens;   /* T in [0, 65536]                                          */
+    int32_t topk;         /* K in [1, 16]                                             */
+    int32_t hidden;       /* H in [1, 16384], any size                                */
+    int32_t num_rows;     /* R in [0, 2^22] rows                                      */
+    int32_t dtype;        /* of rows and drows: BF16, FP16 or FP32                    */
+    int32_t out_dtype;    /* of out, addend and dout: the same as dtype, or FP32      */
+} moe_w8a8_combine_dims_t;
+
+/*
+ * Sorted rows back to their tokens:
+ *
+ *   out[t] = sum over k (ascending, fp32, from +0) of rows[row_of_pair[t,k]] *
+ *            expert_scales[t,k], + addend[t]; rounded once
+ *
+ * Pairs whose row lies outside [0, R) add nothing. With bf16 rows this is the
+ * block's own combine, bit for bit. Without expert_scales it is the gradient
+ * of moe_w8a8_dispatch: rows = the gradient of its rows, out = that of x.
+ *
+ *  rows           [R, H]
+ *  row_of_pair    int32 [T, K]
+ *  expert_scales  fp32 [T, K] or NULL (all ones: no product is formed)
+ *  addend         [T, H] or NULL; may be out itself
+ *  out            [T, H], overlapping nothing else
+ *
+ * rows, addend and out are 16-byte aligned, the others 4.
+ */
+MOE_W8A8_API moe_status_t moe_w8a8_combine(const moe_w8a8_combine_dims_t *dims, const void *rows,
+                                           const int32_t *row_of_pair, const float *expert_scales, const void *addend,
+                                           void *out, void *stream);
+/*
+ * Its gradient, given that of out (which is that of addend, too):
+ *
+ *   drows[r] = dout[t] * expert_scales[t,k] (fp32, then rounded to dtype) for
+ *              the pair (t, k) of row r; zeros in rows without one
+ *   dscales[t,k] = sum over h (fp32) of rows[row_of_pair[t,k]][h] * dout[t][h],
+ *              0 for a dropped pair
+ *
+ * The two maps are those that moe_w8a8_dispatch wrote, each the other's
+ * inverse; a pair whose row is not the pair's by pair_of_row is taken as
+ * dropped, so that no row is written twice.
+ *
+ *  dout           [T, H]
+ *  row_of_pair    int32 [T, K];  pair_of_row  int32 [R]
+ *  rows           [R, H]; NULL iff dscales is
+ *  expert_scales  fp32 [T, K] or NULL (all ones)
+ *  drows          [R, H] or NULL, overlapping nothing
+ *  dscales        fp32 [T, K] or NULL, overlapping nothing; one of the two is
+ *                 given
+ */
+MOE_W8A8_API moe_status_t moe_w8a8_combine_grad(const moe_w8a8_combine_dims_t *dims, const void *dout,
+                                                const int32_t *row_of_pair, const int32_t *pair_of_row,
+                                                const void *rows, const float *expert_scales, void *drows,
+                                                float *dscales, void *stream);
+
 /* Static description of a status code. Never NULL. */
 MOE_W8A8_API const char *moe_w8a8_status_string(moe_status_t status);
 

@@ -16,3 +16,8 @@ from .binding import (GateDims, LinearW4Dims, NormDims, make_gate_dims, make_lin
                       moe_w8a8_norm_quant, moe_w8a8_pack_weights_w4, moe_w8a8_packed_w4_bytes,
                       MOE_DTYPE_BF16, MOE_DTYPE_FP16, MOE_DTYPE_FP32, MOE_DTYPE_INT8, MOE_QUANT_E4M3,
                       MOE_QUANT_INT8, MOE_QUANT_NONE, MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX, MOE_SCORE_SQRT_SOFTPLUS)
+from .binding import (CombineDims, DispatchDims, JoinNormDims, LinearW8Dims, QuantDims, make_combine_dims,  # noqa: F401
+                      make_dispatch_dims, make_join_norm_dims, make_linear_w8_dims, make_quant_dims, moe_w8a8_combine,
+                      moe_w8a8_combine_grad, moe_w8a8_dispatch, moe_w8a8_dispatch_rows,
+                      moe_w8a8_dispatch_workspace_size, moe_w8a8_join_norm, moe_w8a8_linear_w8,
+                      moe_w8a8_pack_weights_w8, moe_w8a8_packed_w8_bytes, moe_w8a8_quant)

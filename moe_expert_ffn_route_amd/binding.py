@@ -25,7 +25,9 @@ EXPORTS = ("moe_w8a8_workspace_size", "moe_w8a8_forward", "moe_w8a8_forward_noal
            "moe_w8a8_packed_mx_bytes", "moe_w8a8_pack_weights_mx", "moe_w8a8_warm", "moe_w8a8_read_probe",
            "moe_w8a8_read_write_probe", "moe_w8a8_status_string", "moe_w8a8_forward_quantized", "moe_w8a8_norm_quant",
            "moe_w8a8_gate_workspace_size", "moe_w8a8_gate", "moe_w8a8_packed_w4_bytes", "moe_w8a8_pack_weights_w4",
-           "moe_w8a8_linear_w4")
+           "moe_w8a8_linear_w4", "moe_w8a8_packed_w8_bytes", "moe_w8a8_pack_weights_w8", "moe_w8a8_linear_w8",
+           "moe_w8a8_quant", "moe_w8a8_join_norm", "moe_w8a8_dispatch_rows", "moe_w8a8_dispatch_workspace_size",
+           "moe_w8a8_dispatch", "moe_w8a8_combine", "moe_w8a8_combine_grad")
 MOE_WEIGHT_ROW_MAJOR, MOE_WEIGHT_PACKED = 0, 1
 MOE_WEIGHT_INT8, MOE_WEIGHT_MXFP4 = 0, 1
 MOE_PACK_GMM1, MOE_PACK_GMM2 = 1, 2
@@ -75,6 +77,40 @@ class LinearW4Dims(ctypes.Structure):
     _fields_ = [("num_tokens", ctypes.c_int32), ("out_features", ctypes.c_int32), ("in_features", ctypes.c_int32),
                 ("group", ctypes.c_int32), ("act_dtype", ctypes.c_int32), ("gated", ctypes.c_int32),
                 ("has_zeros", ctypes.c_int32)]
+
+
+class LinearW8Dims(ctypes.Structure):
+    """moe_w8a8_linear_w8_dims_t"""
+    _fields_ = [("num_tokens", ctypes.c_int32), ("out_features", ctypes.c_int32), ("in_features", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("gated", ctypes.c_int32)]
+
+
+class QuantDims(ctypes.Structure):
+    """moe_w8a8_quant_dims_t"""
+    _fields_ = [("num_tokens", ctypes.c_int32), ("hidden", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("quant", ctypes.c_int32), ("quant_group", ctypes.c_int32), ("amax_eps", ctypes.c_float)]
+
+
+class JoinNormDims(ctypes.Structure):
+    """moe_w8a8_join_norm_dims_t"""
+    _fields_ = [("num_tokens", ctypes.c_int32), ("hidden", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("weight_dtype", ctypes.c_int32), ("post_norm", ctypes.c_int32), ("gate_rows", ctypes.c_int32),
+                ("quant", ctypes.c_int32), ("quant_group", ctypes.c_int32), ("residual_scale", ctypes.c_float),
+                ("branch_scale", ctypes.c_float), ("post_eps", ctypes.c_float), ("rms_eps", ctypes.c_float),
+                ("amax_eps", ctypes.c_float)]
+
+
+class DispatchDims(ctypes.Structure):
+    """moe_w8a8_dispatch_dims_t"""
+    _fields_ = [("num_tokens", ctypes.c_int32), ("topk", ctypes.c_int32), ("moe_expert_num", ctypes.c_int32),
+                ("hidden", ctypes.c_int32), ("dtype", ctypes.c_int32), ("scale_groups", ctypes.c_int32),
+                ("row_align", ctypes.c_int32)]
+
+
+class CombineDims(ctypes.Structure):
+    """moe_w8a8_combine_dims_t"""
+    _fields_ = [("num_tokens", ctypes.c_int32), ("topk", ctypes.c_int32), ("hidden", ctypes.c_int32),
+                ("num_rows", ctypes.c_int32), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
 
 
 DEBUG_FIELDS = ("sorted_pair", "row_of_pair", "group_offset", "shared_token", "num_rows", "q_x", "xs", "acc1",
@@ -133,6 +169,26 @@ def library() -> ctypes.CDLL:
         L.moe_w8a8_pack_weights_w4.argtypes = [ctypes.POINTER(LinearW4Dims)] + [P] * 5
         L.moe_w8a8_linear_w4.restype = ctypes.c_int
         L.moe_w8a8_linear_w4.argtypes = [ctypes.POINTER(LinearW4Dims)] + [P] * 6
+        L.moe_w8a8_packed_w8_bytes.restype = ctypes.c_int
+        L.moe_w8a8_packed_w8_bytes.argtypes = [ctypes.POINTER(LinearW8Dims), ctypes.POINTER(ctypes.c_size_t)]
+        L.moe_w8a8_pack_weights_w8.restype = ctypes.c_int
+        L.moe_w8a8_pack_weights_w8.argtypes = [ctypes.POINTER(LinearW8Dims)] + [P] * 4
+        L.moe_w8a8_linear_w8.restype = ctypes.c_int
+        L.moe_w8a8_linear_w8.argtypes = [ctypes.POINTER(LinearW8Dims)] + [P] * 6
+        L.moe_w8a8_quant.restype = ctypes.c_int
+        L.moe_w8a8_quant.argtypes = [ctypes.POINTER(QuantDims)] + [P] * 5
+        L.moe_w8a8_join_norm.restype = ctypes.c_int
+        L.moe_w8a8_join_norm.argtypes = [ctypes.POINTER(JoinNormDims)] + [P] * 12
+        L.moe_w8a8_dispatch_rows.restype = ctypes.c_int
+        L.moe_w8a8_dispatch_rows.argtypes = [ctypes.POINTER(DispatchDims), ctypes.POINTER(ctypes.c_int64)]
+        L.moe_w8a8_dispatch_workspace_size.restype = ctypes.c_int
+        L.moe_w8a8_dispatch_workspace_size.argtypes = [ctypes.POINTER(DispatchDims), ctypes.POINTER(ctypes.c_size_t)]
+        L.moe_w8a8_dispatch.restype = ctypes.c_int
+        L.moe_w8a8_dispatch.argtypes = [ctypes.POINTER(DispatchDims)] + [P] * 11 + [ctypes.c_size_t, P]
+        L.moe_w8a8_combine.restype = ctypes.c_int
+        L.moe_w8a8_combine.argtypes = [ctypes.POINTER(CombineDims)] + [P] * 6
+        L.moe_w8a8_combine_grad.restype = ctypes.c_int
+        L.moe_w8a8_combine_grad.argtypes = [ctypes.POINTER(CombineDims)] + [P] * 8
         L.moe_w8a8_status_string.restype = ctypes.c_char_p
         L.moe_w8a8_status_string.argtypes = [ctypes.c_int]
         _lib = L
@@ -406,6 +462,13 @@ def _code(dt) -> int:
     return _DTYPE_CODE[dt]
 
 
+def _torch_type(code: int):
+    for dt, c in _DTYPE_CODE.items():
+        if c == code:
+            return dt
+    raise ValueError(f"unsupported element type code {code}")
+
+
 def make_norm_dims(num_tokens, hidden, dtype=torch.bfloat16, weight_dtype=None, quant=MOE_QUANT_INT8, quant_group=0,
                    rms_eps=1e-6, amax_eps=1e-6) -> NormDims:
     return NormDims(num_tokens, hidden, _code(dtype), _code(dtype if weight_dtype is None else weight_dtype), quant,
@@ -496,6 +559,171 @@ def moe_w8a8_linear_w4(dims: LinearW4Dims, x, weight, x_scale=None, bias=None, o
                      x.device, stream)
     _call("moe_w8a8_linear_w4", _native().linear_w4, x, stream, dims, x, x_scale, weight, bias, out)
     return out
+
+
+# ------------------------- operators between the block and the rest of a program
+
+def make_linear_w8_dims(num_tokens, out_features, in_features, out_dtype=torch.bfloat16, gated=False) -> LinearW8Dims:
+    return LinearW8Dims(num_tokens, out_features, in_features, _code(out_dtype), int(gated))
+
+
+def moe_w8a8_packed_w8_bytes(dims: LinearW8Dims) -> int:
+    b = ctypes.c_size_t(0)
+    rc = library().moe_w8a8_packed_w8_bytes(ctypes.byref(dims), ctypes.byref(b))
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_w8a8_packed_w8_bytes")
+    return int(b.value)
+
+
+def moe_w8a8_pack_weights_w8(dims: LinearW8Dims, codes, scale, dst=None, stream=None):
+    """Pack int8 weights (codes int8 [N, K], scale fp32 [N]) for
+    moe_w8a8_linear_w8 with these dims (num_tokens and out_dtype aside).
+    Returns dst (uint8, allocated if None)."""
+    _tensor(codes, "codes")
+    nbytes, dev = moe_w8a8_packed_w8_bytes(dims), codes.get_device()
+    if dst is None:
+        dst = _empty(nbytes, torch.uint8, codes.device, stream)
+    N = dims.out_features
+    _call("moe_w8a8_pack_weights_w8", library().moe_w8a8_pack_weights_w8, codes, stream, ctypes.byref(dims),
+          _arg(codes, "codes", torch.int8, N * dims.in_features, dev), _arg(scale, "scale", torch.float32, N, dev),
+          _arg(dst, "dst", torch.uint8, nbytes, dev))
+    return dst
+
+
+def moe_w8a8_linear_w8(dims: LinearW8Dims, x, x_scale, weight, bias=None, out=None, stream=None):
+    """Dense product of int8 codes x [T, K] with scales x_scale fp32 [T] by
+    packed int8 weights. Returns out (dims.out_dtype; [T, N], or [T, N/2] when
+    gated), allocated if None."""
+    if out is None:
+        _tensor(x, "x")
+        moe_w8a8_packed_w8_bytes(dims)  # dims that no buffer can have raise here
+        width = dims.out_features // 2 if dims.gated else dims.out_features
+        out = _empty((dims.num_tokens, width), _torch_type(dims.out_dtype), x.device, stream)
+    _call("moe_w8a8_linear_w8", _native().linear_w8, x, stream, dims, x, x_scale, weight, bias, out)
+    return out
+
+
+def make_quant_dims(num_tokens, hidden, dtype=torch.bfloat16, quant=MOE_QUANT_INT8, quant_group=0,
+                    amax_eps=1e-6) -> QuantDims:
+    return QuantDims(num_tokens, hidden, _code(dtype), quant, quant_group, amax_eps)
+
+
+def moe_w8a8_quant(dims: QuantDims, x, smooth=None, q=None, q_scale=None, stream=None):
+    """Codes and scales of x [T, H], times smooth fp32 [H] if given. Returns
+    (q int8 or float8_e4m3fn [T, H], q_scale fp32 [T] or [T, H / quant_group]),
+    allocated if None."""
+    if q is None or q_scale is None:
+        _tensor(x, "x")
+        T, H, g = dims.num_tokens, dims.hidden, dims.quant_group
+        if T < 0 or H <= 0 or g < 0 or (g and H % g):  # dims that no buffer can have
+            raise MoeError(MOE_ERR_INVALID_ARG, "moe_w8a8_quant")
+        if q is None:
+            q = _empty((T, H), torch.float8_e4m3fn if dims.quant == MOE_QUANT_E4M3 else torch.int8, x.device, stream)
+        if q_scale is None:
+            q_scale = _empty((T, H // g) if g else (T,), torch.float32, x.device, stream)
+    _call("moe_w8a8_quant", _native().quant, x, stream, dims, x, smooth, q, q_scale)
+    return q, q_scale
+
+
+def make_join_norm_dims(num_tokens, hidden, dtype=torch.bfloat16, weight_dtype=None, post_norm=False, gate_rows=0,
+                        quant=MOE_QUANT_INT8, quant_group=0, residual_scale=1.0, branch_scale=1.0, post_eps=1e-6,
+                        rms_eps=1e-6, amax_eps=1e-6) -> JoinNormDims:
+    return JoinNormDims(num_tokens, hidden, _code(dtype), _code(dtype if weight_dtype is None else weight_dtype),
+                        int(post_norm), gate_rows, quant, quant_group, residual_scale, branch_scale, post_eps, rms_eps,
+                        amax_eps)
+
+
+def moe_w8a8_join_norm(dims: JoinNormDims, block, residual=None, share=None, share_scale=None, post_weight=None,
+                       gate=None, weight=None, residual_out=None, y=None, q=None, q_scale=None, stream=None) -> None:
+    """The block's outputs (share times share_scale fp32 [T]), normed if
+    dims.post_norm, gated and scaled, onto the residual stream, and the next
+    norm with its codes; writes those of residual_out, y, q and q_scale that
+    are given (see the header). residual_out and y may be block, share or
+    residual themselves."""
+    _call("moe_w8a8_join_norm", _native().join_norm, block, stream, dims, block, share, share_scale, residual,
+          post_weight, gate, weight, residual_out, y, q, q_scale)
+
+
+def make_dispatch_dims(num_tokens, hidden, moe_expert_num, topk, dtype=torch.bfloat16, scale_groups=0,
+                       row_align=1) -> DispatchDims:
+    """dtype of x and its rows; torch.int8 stands for any 8-bit codes."""
+    return DispatchDims(num_tokens, topk, moe_expert_num, hidden, _code(dtype), scale_groups, row_align)
+
+
+def moe_w8a8_dispatch_rows(dims: DispatchDims) -> int:
+    n = ctypes.c_int64(0)
+    rc = library().moe_w8a8_dispatch_rows(ctypes.byref(dims), ctypes.byref(n))
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_w8a8_dispatch_rows")
+    return int(n.value)
+
+
+def moe_w8a8_dispatch_workspace_size(dims: DispatchDims) -> int:
+    n = ctypes.c_size_t(0)
+    rc = library().moe_w8a8_dispatch_workspace_size(ctypes.byref(dims), ctypes.byref(n))
+    if rc != MOE_OK:
+        raise MoeError(rc, "moe_w8a8_dispatch_workspace_size")
+    return int(n.value)
+
+
+def moe_w8a8_dispatch(dims: DispatchDims, expert_ids, x=None, x_scale=None, x_active_mask=None, rows=None,
+                      row_scale=None, expert_token_nums=None, expert_offset=None, row_of_pair=None, pair_of_row=None,
+                      workspace=None, stream=None) -> dict:
+    """Sort the pairs of expert_ids int32 [T, K] by expert, and with them the
+    rows of x [T, H] and its scales x_scale fp32 [T, scale_groups]. Returns a
+    dict of rows, row_scale, expert_token_nums, expert_offset, row_of_pair and
+    pair_of_row (see the header), allocated if None, as is the workspace.
+    Without x the maps are made alone (rows and row_scale None)."""
+    if (expert_token_nums is None or expert_offset is None or row_of_pair is None or pair_of_row is None
+            or workspace is None or x is not None and (rows is None or row_scale is None and dims.scale_groups)):
+        _tensor(expert_ids, "expert_ids")
+        R, need = moe_w8a8_dispatch_rows(dims), moe_w8a8_dispatch_workspace_size(dims)  # impossible dims raise here
+
+        def new(t, shape, dtype):
+            return _empty(shape, dtype, expert_ids.device, stream) if t is None else t
+        i32 = torch.int32
+        expert_token_nums = new(expert_token_nums, (dims.moe_expert_num,), i32)
+        expert_offset = new(expert_offset, (dims.moe_expert_num + 1,), i32)
+        row_of_pair = new(row_of_pair, (dims.num_tokens, dims.topk), i32)
+        pair_of_row = new(pair_of_row, (R,), i32)
+        workspace = new(workspace, (max(256, need),), torch.uint8)
+        if x is not None:
+            _tensor(x, "x")
+            rows = new(rows, (R, dims.hidden), x.dtype)
+            if dims.scale_groups:
+                row_scale = new(row_scale, (R, dims.scale_groups), torch.float32)
+    _tensor(workspace, "workspace")
+    _call("moe_w8a8_dispatch", _native().dispatch, expert_ids, stream, dims, expert_ids, x, x_scale, x_active_mask, rows,
+          row_scale, expert_token_nums, expert_offset, row_of_pair, pair_of_row, workspace, workspace.numel())
+    return dict(rows=rows, row_scale=row_scale, expert_token_nums=expert_token_nums, expert_offset=expert_offset,
+                row_of_pair=row_of_pair, pair_of_row=pair_of_row)
+
+
+def make_combine_dims(num_tokens, hidden, topk, num_rows, dtype=torch.bfloat16, out_dtype=None) -> CombineDims:
+    return CombineDims(num_tokens, topk, hidden, num_rows, _code(dtype), _code(dtype if out_dtype is None else out_dtype))
+
+
+def moe_w8a8_combine(dims: CombineDims, rows, row_of_pair, expert_scales=None, addend=None, out=None, stream=None):
+    """Sorted rows [R, H] back to their tokens, weighted by expert_scales fp32
+    [T, K] if given, plus addend [T, H] if given (may be out). Returns out
+    [T, H] (dims.out_dtype), allocated if None. Without expert_scales it is
+    the gradient of moe_w8a8_dispatch."""
+    if out is None:
+        _tensor(rows, "rows")
+        if dims.num_tokens < 0 or dims.hidden <= 0:  # dims that no buffer can have
+            raise MoeError(MOE_ERR_INVALID_ARG, "moe_w8a8_combine")
+        out = _empty((dims.num_tokens, dims.hidden), _torch_type(dims.out_dtype), rows.device, stream)
+    _call("moe_w8a8_combine", _native().combine, rows, stream, dims, rows, row_of_pair, expert_scales, addend, out)
+    return out
+
+
+def moe_w8a8_combine_grad(dims: CombineDims, dout, row_of_pair, pair_of_row, rows=None, expert_scales=None, drows=None,
+                          dscales=None, stream=None) -> None:
+    """The gradient of moe_w8a8_combine: writes those of drows [R, H] (of its
+    rows) and dscales fp32 [T, K] (of expert_scales; needs rows) that are
+    given. The maps are those of moe_w8a8_dispatch."""
+    _call("moe_w8a8_combine_grad", _native().combine_grad, dout, stream, dims, dout, row_of_pair, pair_of_row, rows,
+          expert_scales, drows, dscales)
 
 
 # ---------------------------------------------------------------- helpers

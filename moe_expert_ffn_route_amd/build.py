@@ -22,7 +22,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmoe_w8a8.so")
 SOURCES = ["abi.hip", "route.hip", "quant.hip", "gemm.hip", "gemm_wide.hip", "gemm_tall.hip", "gemm_mx.hip", "combine.hip",
-           "pack.hip", "warm.hip", "abi_ops.hip", "norm.hip", "gate.hip", "linear_w4.hip"]
+           "pack.hip", "warm.hip", "abi_ops.hip", "norm.hip", "gate.hip", "linear_w4.hip", "abi_join.hip", "join.hip",
+           "linear_w8.hip", "dispatch.hip"]
 PYCALL = os.path.join(PKG, "_pycall.so")
 ARCH = os.environ.get("MOE_OFFLOAD_ARCH", "gfx950")
 

@@ -3,35 +3,15 @@
 // Nothing here allocates or synchronises.
 #include <math.h>
 
-#include "../../include/moe_w8a8.h"
-#include "ops.h"
+#include "abi_check.h"
 
 using namespace moe;
 
 namespace {
 
-constexpr int kMaxHidden = 16384;
-constexpr int kMaxExperts = 1024;
 constexpr int kMaxOut = 1 << 20;
 constexpr int kMaxIn = 1 << 17;
 constexpr int64_t kMaxW4Tiles = 1 << 23;  // 16 x 128 weights each: 17 G weights, and a packing grid under 2^31 threads
-
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-struct Range {
-    const void *p;
-    size_t bytes;
-};
-bool overlap(const Range &a, const Range &b) {
-    if (!a.p || !b.p || !a.bytes || !b.bytes) return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-    return a0 < b0 + b.bytes && b0 < a0 + a.bytes;
-}
-
-size_t dtype_bytes(int dt) { return dt == MOE_DTYPE_FP32 ? 4 : dt == MOE_DTYPE_INT8 ? 1 : 2; }
-bool is_float_dtype(int dt) { return dt == MOE_DTYPE_BF16 || dt == MOE_DTYPE_FP16 || dt == MOE_DTYPE_FP32; }
-
-moe_status_t of_launch(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
 moe_status_t check_norm(const moe_w8a8_norm_dims_t *d) {
     if (!d) return MOE_ERR_INVALID_ARG;

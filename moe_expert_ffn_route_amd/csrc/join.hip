@@ -1,0 +1,294 @@
+// Two operators on rows: the quantiser of an activation, and the norm that
+// joins a block's outputs to the residual stream.
+//
+// Codes follow the block's rule (rowquant.h). As in norm.hip, those of y = p *
+// rstd come from p and max|p| alone, so that rstd enters only the scales (and
+// the codes of rows under the amax floor). The branch's own norm does enter p;
+// its mean square is summed in fp64 and 1 / sqrt rounded once to fp32, so that
+// the codes are the same whatever the order of that sum (it decides only sums
+// within 2^-50 or so of a rounding border of 1 / sqrt).
+//
+// A row of up to 16384 elements stays in the registers of one workgroup
+// between the one read of its inputs and the writes: what bounds both
+// operators is memory.
+#include "rowwise.h"
+
+#include "../../include/moe_w8a8.h"
+
+namespace moe {
+namespace {
+
+__device__ __forceinline__ float lane63(float v) {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), kWave - 1));
+}
+__device__ __forceinline__ double wave_sum(double v) {  // in every lane
+#pragma unroll
+    for (int d = kWave / 2; d > 0; d >>= 1) v += __shfl_xor(v, d, kWave);
+    return v;
+}
+
+// TPR threads per row, CH chunks of kVec elements per thread: H <= TPR * CH *
+// kVec. A workgroup is one row, or four rows of one wave each. TAIL: H is no
+// multiple of kVec. Loads stand behind no branch: lanes past the row's end
+// read its last chunk again and count nothing.
+template <typename T, int TPR, int CH, bool TAIL>
+__global__ __launch_bounds__(TPR *kRows<TPR>) void quant_kernel(QuantArgs a) {
+    constexpr int kWaves = TPR / kWave;
+    const int tr = threadIdx.x % TPR, row = blockIdx.x * kRows<TPR> + threadIdx.x / TPR;
+    if (kRows<TPR> > 1 && row >= a.T) return;  // whole waves, and such a row has no barrier
+    const size_t base = static_cast<size_t>(row) * a.H;
+    const T *x = static_cast<const T *>(a.x) + base;
+    const int chunks = a.H / kVec, rest = a.H % kVec;
+    const bool tail = TAIL && tr < rest;
+    const int it = TAIL ? chunks * kVec + min(tr, rest - 1) : 0;
+    auto at = [&](int j) { return min(tr + j * TPR, chunks - 1) * kVec; };
+    float p[CH][kVec] = {}, pt = 0.0f;
+    if (!TAIL || chunks > 0) {
+        float g[CH][kVec];
+#pragma unroll
+        for (int j = 0; j < CH; ++j) load8(x + at(j), p[j]);
+        if (a.smooth) {
+#pragma unroll
+            for (int j = 0; j < CH; ++j) load8(a.smooth + at(j), g[j]);
+#pragma unroll
+            for (int j = 0; j < CH; ++j)
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) p[j][e] = p[j][e] * g[j][e];
+        }
+    }
+    if (TAIL) {
+        pt = to_f32(x[it]);
+        if (a.smooth) pt = pt * a.smooth[it];
+        if (!tail) pt = 0.0f;
+    }
+    float mx = fabsf(pt);
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+        const bool in = tr + j * TPR < chunks;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+            if (!in) p[j][e] = 0.0f;
+            mx = fmaxf(mx, fabsf(p[j][e]));
+        }
+    }
+    if (!a.group) {
+        mx = last_lane_max(mx);
+        __shared__ float s_max[kWaves];
+        if constexpr (kWaves == 1) mx = lane63(mx);
+        else mx = join_waves<kWaves>(mx, s_max, tr, [](float u, float v) { return fmaxf(u, v); });
+    }
+    write_codes<TPR, CH, TAIL>(p, pt, mx, 1.0f, a.amax_eps, a.quant == MOE_QUANT_E4M3, a.group, a.H, tr, tail, it,
+                               static_cast<uint8_t *>(a.q) + base,
+                               a.q_scale + static_cast<size_t>(row) * (a.group ? a.H / a.group : 1));
+}
+
+template <typename T, typename W, int TPR, int CH, bool TAIL>
+__global__ __launch_bounds__(TPR *kRows<TPR>) void join_norm_kernel(JoinNormArgs a) {
+    constexpr int kWaves = TPR / kWave;
+    __shared__ double s_sq[kWaves];
+    __shared__ float s_sum[kWaves], s_max[kWaves];
+    const int tr = threadIdx.x % TPR, row = blockIdx.x * kRows<TPR> + threadIdx.x / TPR;
+    if (kRows<TPR> > 1 && row >= a.T) return;  // whole waves, and such a row has no barrier
+    const size_t base = static_cast<size_t>(row) * a.H;
+    const T *block = static_cast<const T *>(a.block) + base, *share = static_cast<const T *>(a.share) + base;
+    const T *res = static_cast<const T *>(a.residual) + base;
+    const W *pw = static_cast<const W *>(a.post_weight), *w = static_cast<const W *>(a.weight);
+    const W *gate = static_cast<const W *>(a.gate) + row * a.gate_stride;
+    const int chunks = a.H / kVec, rest = a.H % kVec;
+    const bool tail = TAIL && tr < rest, whole = !TAIL || chunks > 0;
+    const int it = TAIL ? chunks * kVec + min(tr, rest - 1) : 0;
+    auto at = [&](int j) { return min(tr + j * TPR, chunks - 1) * kVec; };
+
+    // b, and what will be needed later on its way
+    float p[CH][kVec] = {}, r[CH][kVec] = {}, pt = 0.0f, rt = 0.0f;
+    const float ss = a.share_scale ? a.share_scale[row] : 1.0f;
+    if (whole) {
+#pragma unroll
+        for (int j = 0; j < CH; ++j) load8(block + at(j), p[j]);
+        if (a.share) {
+            float v[CH][kVec];
+#pragma unroll
+            for (int j = 0; j < CH; ++j) load8(share + at(j), v[j]);
+            if (a.residual) {
+#pragma unroll
+                for (int j = 0; j < CH; ++j) load8(res + at(j), r[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < CH; ++j)
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) p[j][e] = p[j][e] + v[j][e] * ss;
+        } else if (a.residual) {
+#pragma unroll
+            for (int j = 0; j < CH; ++j) load8(res + at(j), r[j]);
+        }
+    }
+    if (TAIL) {
+        pt = to_f32(block[it]);
+        if (a.share) pt = pt + to_f32(share[it]) * ss;
+        if (a.residual) rt = to_f32(res[it]);
+    }
+    if (a.post_norm) {
+        double sq = tail ? static_cast<double>(pt) * pt : 0.0;
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            const bool in = tr + j * TPR < chunks;
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) {
+                const double v = in ? p[j][e] : 0.0f;
+                sq = __builtin_fma(v, v, sq);
+            }
+        }
+        sq = wave_sum(sq);
+        if constexpr (kWaves > 1) sq = join_waves<kWaves>(sq, s_sq, tr, [](double u, double v) { return u + v; });
+        const float rstd = static_cast<float>(1.0 / sqrt(sq / a.H + static_cast<double>(a.post_eps)));
+        if (pw && whole) {
+            float v[CH][kVec];
+#pragma unroll
+            for (int j = 0; j < CH; ++j) load8(pw + at(j), v[j]);
+#pragma unroll
+            for (int j = 0; j < CH; ++j)
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) p[j][e] = p[j][e] * v[j][e];
+        }
+        if (TAIL && pw) pt = pt * to_f32(pw[it]);
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) p[j][e] = p[j][e] * rstd;
+        pt = pt * rstd;
+    }
+    // r = residual * residual_scale + n * (gate * branch_scale), in p
+    if (a.gate && whole) {
+        float v[CH][kVec];
+#pragma unroll
+        for (int j = 0; j < CH; ++j) load8(gate + at(j), v[j]);
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) p[j][e] = p[j][e] * (v[j][e] * a.branch_scale);
+    } else {
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) p[j][e] = p[j][e] * a.branch_scale;
+    }
+    if (TAIL) pt = pt * (a.gate ? to_f32(gate[it]) * a.branch_scale : a.branch_scale);
+    if (a.residual) {
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) p[j][e] = r[j][e] * a.residual_scale + p[j][e];
+        pt = rt * a.residual_scale + pt;
+    }
+    if (a.residual_out) {  // its row has been read by the threads that write it
+        T *out = static_cast<T *>(a.residual_out) + base;
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+            if (tr + j * TPR < chunks) store8(out + at(j), p[j]);
+        if (tail) from_f32(pt, out[it]);
+    }
+    if (!a.y && !a.q) return;  // uniform
+    if (w && whole) {
+#pragma unroll
+        for (int j = 0; j < CH; ++j) load8(w + at(j), r[j]);
+    }
+    float sum = 0.0f, mx = 0.0f;
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+        const bool in = tr + j * TPR < chunks;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+            if (!in) p[j][e] = 0.0f;
+            sum += p[j][e] * p[j][e];
+            if (in && w) p[j][e] = p[j][e] * r[j][e];
+            mx = fmaxf(mx, fabsf(p[j][e]));
+        }
+    }
+    if (TAIL) {
+        if (!tail) pt = 0.0f;
+        sum += pt * pt;
+        if (tail && w) pt = pt * to_f32(w[it]);
+        mx = fmaxf(mx, fabsf(pt));
+    }
+    sum = last_lane_sum(sum);
+    mx = last_lane_max(mx);
+    if constexpr (kWaves == 1) {
+        sum = lane63(sum);
+        mx = lane63(mx);
+    } else {
+        if ((tr & (kWave - 1)) == kWave - 1) s_max[tr / kWave] = mx;
+        sum = join_waves<kWaves>(sum, s_sum, tr, [](float u, float v) { return u + v; });
+        mx = s_max[0];
+#pragma unroll
+        for (int i = 1; i < kWaves; ++i) mx = fmaxf(mx, s_max[i]);
+    }
+    const float rstd = 1.0f / sqrtf(sum / static_cast<float>(a.H) + a.rms_eps);
+    if (a.y) {
+        T *y = static_cast<T *>(a.y) + base;
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            if (tr + j * TPR >= chunks) break;
+            float v[kVec];
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) v[e] = p[j][e] * rstd;
+            store8(y + at(j), v);
+        }
+        if (tail) from_f32(pt * rstd, y[it]);
+    }
+    if (!a.q) return;
+    write_codes<TPR, CH, TAIL>(p, pt, mx, rstd, a.amax_eps, a.quant == MOE_QUANT_E4M3, a.group, a.H, tr, tail, it,
+                               static_cast<uint8_t *>(a.q) + base,
+                               a.q_scale + static_cast<size_t>(row) * (a.group ? a.H / a.group : 1));
+}
+
+template <typename T, int TPR, int CH>
+hipError_t quant_rows(const QuantArgs &a, hipStream_t s) {
+    const dim3 grid((a.T + kRows<TPR> - 1) / kRows<TPR>), blk(TPR * kRows<TPR>);
+    if (a.H % kVec) hipLaunchKernelGGL((quant_kernel<T, TPR, CH, true>), grid, blk, 0, s, a);
+    else hipLaunchKernelGGL((quant_kernel<T, TPR, CH, false>), grid, blk, 0, s, a);
+    return hipGetLastError();
+}
+template <typename T>
+hipError_t quant_of(const QuantArgs &a, hipStream_t s) {
+    if (a.H <= 64 * kVec) return quant_rows<T, 64, 1>(a, s);
+    if (a.H <= 256 * kVec) return quant_rows<T, 256, 1>(a, s);
+    if (a.H <= 512 * kVec) return quant_rows<T, 256, 2>(a, s);
+    if (a.T < 512) return a.H <= 1024 * kVec ? quant_rows<T, 1024, 1>(a, s) : quant_rows<T, 1024, 2>(a, s);
+    return a.H <= 1024 * kVec ? quant_rows<T, 256, 4>(a, s) : quant_rows<T, 256, 8>(a, s);
+}
+
+template <typename T, typename W, int TPR, int CH>
+hipError_t join_rows(const JoinNormArgs &a, hipStream_t s) {
+    const dim3 grid((a.T + kRows<TPR> - 1) / kRows<TPR>), blk(TPR * kRows<TPR>);
+    if (a.H % kVec) hipLaunchKernelGGL((join_norm_kernel<T, W, TPR, CH, true>), grid, blk, 0, s, a);
+    else hipLaunchKernelGGL((join_norm_kernel<T, W, TPR, CH, false>), grid, blk, 0, s, a);
+    return hipGetLastError();
+}
+template <typename T, typename W>
+hipError_t join_of(const JoinNormArgs &a, hipStream_t s) {
+    if (a.H <= 64 * kVec) return join_rows<T, W, 64, 1>(a, s);
+    if (a.H <= 256 * kVec) return join_rows<T, W, 256, 1>(a, s);
+    if (a.H <= 512 * kVec) return join_rows<T, W, 256, 2>(a, s);
+    if (a.T < 512) return a.H <= 1024 * kVec ? join_rows<T, W, 1024, 1>(a, s) : join_rows<T, W, 1024, 2>(a, s);
+    return a.H <= 1024 * kVec ? join_rows<T, W, 256, 4>(a, s) : join_rows<T, W, 256, 8>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_quant(const QuantArgs &a, hipStream_t s) {
+    switch (a.dtype) {
+        case MOE_DTYPE_BF16: return quant_of<Bf16>(a, s);
+        case MOE_DTYPE_FP16: return quant_of<Fp16>(a, s);
+        default: return quant_of<float>(a, s);
+    }
+}
+
+hipError_t launch_join_norm(const JoinNormArgs &a, hipStream_t s) {
+    switch (a.dtype) {
+        case MOE_DTYPE_BF16: return a.weight_dtype == MOE_DTYPE_FP32 ? join_of<Bf16, float>(a, s) : join_of<Bf16, Bf16>(a, s);
+        case MOE_DTYPE_FP16: return a.weight_dtype == MOE_DTYPE_FP32 ? join_of<Fp16, float>(a, s) : join_of<Fp16, Fp16>(a, s);
+        default: return join_of<float, float>(a, s);
+    }
+}
+
+}  // namespace moe

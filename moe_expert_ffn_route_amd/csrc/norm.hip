@@ -21,64 +21,16 @@
 // branch. Lanes past the row's end read its last chunk again and count nothing.
 // A row whose length is no multiple of kVec ends in up to seven elements more,
 // one per thread.
-#include "ops.h"
-#include "rowquant.h"
+#include "rowwise.h"
 
 #include "../../include/moe_w8a8.h"
 
 namespace moe {
 namespace {
 
-constexpr int kVec = 8;  // elements per thread and chunk
-
-// kVec consecutive elements; rows of odd length start at any element, so
-// nothing is assumed about the address but the element's own alignment (the
-// hardware takes such 16-byte accesses).
-template <typename T>
-__device__ __forceinline__ void load8(const T *p, float (&v)[kVec]) {
-    T raw[kVec];
-    __builtin_memcpy(raw, p, sizeof raw);
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) v[e] = to_f32(raw[e]);
-}
-template <typename T>
-__device__ __forceinline__ void store8(T *p, const float (&v)[kVec]) {
-    T raw[kVec];
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) from_f32(v[e], raw[e]);
-    __builtin_memcpy(p, raw, sizeof raw);
-}
-// Sum and maximum over the wave: DPP shifts within rows of 16 lanes, then the
-// row ends to the following rows; lane 63 holds the result.
-template <int CTRL>
-__device__ __forceinline__ float dpp_or(float v, float absent) {
-    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(absent), __float_as_int(v), CTRL, 0xF, 0xF, false));
-}
-__device__ __forceinline__ float last_lane_sum(float v) {
-    v += dpp_or<0x111>(v, 0.0f);
-    v += dpp_or<0x112>(v, 0.0f);
-    v += dpp_or<0x114>(v, 0.0f);
-    v += dpp_or<0x118>(v, 0.0f);
-    // lanes 15, 31, 47, 63 hold their rows' sums; rows 1 and 3, then 2 and 3, take what is before them
-    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x142, 0xA, 0xF, false));
-    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x143, 0xC, 0xF, false));
-    return v;
-}
-__device__ __forceinline__ float last_lane_max(float v) {  // of magnitudes
-    v = fmaxf(v, dpp_or<0x111>(v, 0.0f));
-    v = fmaxf(v, dpp_or<0x112>(v, 0.0f));
-    v = fmaxf(v, dpp_or<0x114>(v, 0.0f));
-    v = fmaxf(v, dpp_or<0x118>(v, 0.0f));
-    v = fmaxf(v, dpp_or<0x142>(v, 0.0f));
-    v = fmaxf(v, dpp_or<0x143>(v, 0.0f));
-    return v;
-}
-
 // TPR threads per row, CH chunks of kVec elements per thread: H <= TPR * CH *
 // kVec. A workgroup is one row, or four rows of one wave each. TAIL: H is no
 // multiple of kVec.
-template <int TPR>
-constexpr int kRows = TPR == kWave ? 4 : 1;
 template <typename T, typename W, int TPR, int CH, bool TAIL>
 __global__ __launch_bounds__(TPR *kRows<TPR>) void norm_kernel(NormArgs a) {
     constexpr int kWaves = TPR / kWave;
@@ -175,50 +127,9 @@ __global__ __launch_bounds__(TPR *kRows<TPR>) void norm_kernel(NormArgs a) {
         if (tail) from_f32(pt * rstd, y[it]);
     }
     if (!a.q) return;
-    const bool fp8 = a.quant == MOE_QUANT_E4M3;
-    const float top_inv = fp8 ? 1.0f / kQMax<true> : 1.0f / kQMax<false>;
-    uint8_t *q = static_cast<uint8_t *>(a.q) + base;
-    float *scale = a.q_scale + static_cast<size_t>(row) * (a.group ? a.H / a.group : 1);
-    auto inv_of = [&](float pm, float am) {
-        return am >= a.amax_eps ? 1.0f / pm : rstd * (1.0f / a.amax_eps);
-    };
-    auto quant8 = [&](const float (&v)[kVec], float inv) -> uint64_t {
-        uint32_t lo, hi;
-        if (fp8) {
-            lo = quant4<true>(v[0], v[1], v[2], v[3], inv);
-            hi = quant4<true>(v[4], v[5], v[6], v[7], inv);
-        } else {
-            lo = quant4<false>(v[0], v[1], v[2], v[3], inv);
-            hi = quant4<false>(v[4], v[5], v[6], v[7], inv);
-        }
-        return lo | (static_cast<uint64_t>(hi) << 32);
-    };
-    if (a.group) {  // a group is gl neighbouring lanes' chunks; groups divide H, so there is no tail
-        const int gl = a.group / kVec;
-#pragma unroll
-        for (int j = 0; j < CH; ++j) {
-            if (j * TPR >= chunks) break;  // uniform
-            float pm = 0.0f;
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) pm = fmaxf(pm, fabsf(p[j][e]));
-            for (int d = gl / 2; d > 0; d >>= 1) pm = fmaxf(pm, __shfl_xor(pm, d, kWave));
-            if (tr + j * TPR >= chunks) continue;
-            const float am = pm * rstd;
-            const uint64_t code = quant8(p[j], inv_of(pm, am));
-            __builtin_memcpy(q + at(j), &code, sizeof code);
-            if ((tr & (gl - 1)) == 0) scale[at(j) / a.group] = fmaxf(am, a.amax_eps) * top_inv;
-        }
-        return;
-    }
-    const float am = mx * rstd, inv = inv_of(mx, am);
-#pragma unroll
-    for (int j = 0; j < CH; ++j) {
-        if (tr + j * TPR >= chunks) break;
-        const uint64_t code = quant8(p[j], inv);
-        __builtin_memcpy(q + at(j), &code, sizeof code);
-    }
-    if (tail) q[it] = static_cast<uint8_t>(fp8 ? quant4<true>(pt, 0.0f, 0.0f, 0.0f, inv) : quant4<false>(pt, 0.0f, 0.0f, 0.0f, inv));
-    if (tr == 0) *scale = fmaxf(am, a.amax_eps) * top_inv;
+    write_codes<TPR, CH, TAIL>(p, pt, mx, rstd, a.amax_eps, a.quant == MOE_QUANT_E4M3, a.group, a.H, tr, tail, it,
+                               static_cast<uint8_t *>(a.q) + base,
+                               a.q_scale + static_cast<size_t>(row) * (a.group ? a.H / a.group : 1));
 }
 
 template <typename T, typename W, int TPR, int CH>

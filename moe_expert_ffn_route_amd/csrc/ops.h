@@ -36,12 +36,69 @@ struct LinearW4Args {
     int T, N, K, group, act, gated;
     int n_tiles, k_tiles;    // 16 rows, 128 k
 };
+struct LinearW8Args {
+    const int8_t *x;
+    const float *x_scale;
+    const int8_t *codes;     // packed weight: codes, then scales
+    const float *scale;
+    const float *bias;
+    void *out;
+    int T, N, K, out_dtype, gated;
+    int n_tiles, k_tiles;    // 16 rows, 128 k
+};
+struct QuantArgs {
+    const void *x;
+    const float *smooth;
+    void *q;
+    float *q_scale;
+    int T, H, dtype, quant;
+    int group;  // elements per scale, 0 = one per row
+    float amax_eps;
+};
+struct JoinNormArgs {
+    const void *block, *share, *residual, *post_weight, *gate, *weight;
+    const float *share_scale;
+    void *residual_out, *y, *q;
+    float *q_scale;
+    int T, H, dtype, weight_dtype, quant, group, post_norm;
+    size_t gate_stride;  // elements between the tokens' rows of gate
+    float residual_scale, branch_scale, post_eps, rms_eps, amax_eps;
+};
+struct DispatchArgs {
+    const int32_t *ids;
+    const void *x;
+    const float *x_scale;
+    const uint8_t *mask;
+    void *rows;
+    float *row_scale;
+    int32_t *counts, *offset, *row_of_pair, *pair_of_row;
+    int32_t *workspace;
+    int T, K, E, H, elem, groups, align;  // elem: bytes of an element
+    int64_t R;                            // rows of `rows` and pair_of_row
+};
+struct RowsArgs {  // sorted rows back to tokens, and the gradient
+    const void *rows, *addend, *dout;
+    const int32_t *row_of_pair, *pair_of_row;
+    const float *scales;
+    void *out, *drows;
+    float *dscales;
+    int T, K, H, R, dtype, out_dtype;
+};
 hipError_t launch_norm_quant(const NormArgs &a, hipStream_t s);
 size_t gate_workspace(int T, int E, int H);
 hipError_t launch_gate(const GateArgs &a, hipStream_t s);
 hipError_t launch_pack_w4(const uint8_t *codes, const float *scale, const uint8_t *zero, uint8_t *dst_codes,
                           float *dst_scale, uint8_t *dst_zero, const LinearW4Args &a, hipStream_t s);
 hipError_t launch_linear_w4(const LinearW4Args &a, hipStream_t s);
+hipError_t launch_pack_w8(const int8_t *codes, const float *scale, int8_t *dst_codes, float *dst_scale,
+                          const LinearW8Args &a, hipStream_t s);
+hipError_t launch_linear_w8(const LinearW8Args &a, hipStream_t s);
+hipError_t launch_quant(const QuantArgs &a, hipStream_t s);
+hipError_t launch_join_norm(const JoinNormArgs &a, hipStream_t s);
+size_t dispatch_workspace(int T, int K, int E);
+hipError_t launch_dispatch(const DispatchArgs &a, hipStream_t s);
+hipError_t launch_combine_rows(const RowsArgs &a, hipStream_t s);
+hipError_t launch_combine_grad(const RowsArgs &a, hipStream_t s);
 
 // One element of a MOE_DTYPE_* array to fp32, and back with one rounding to
 // nearest even (fp16 overflow to infinity).
