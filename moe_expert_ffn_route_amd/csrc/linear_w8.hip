@@ -12,8 +12,6 @@
 // behind a row's end (the next row's codes) meets zeros.
 #include "ops.h"
 
-#include <type_traits>
-
 #include "../../include/moe_w8a8.h"
 
 namespace moe {
@@ -69,34 +67,37 @@ __device__ __forceinline__ v4i load16(const int8_t *p) {
     __builtin_memcpy(&v, p, 16);
     return v;
 }
+__device__ __forceinline__ v4i shift_down(v4i v, int bytes) {
+    uint64_t q[2];
+    __builtin_memcpy(q, &v, 16);
+    const unsigned __int128 w = ((static_cast<unsigned __int128>(q[1]) << 64) | q[0]) >> (min(bytes, 15) * 8);
+    q[0] = static_cast<uint64_t>(w);
+    q[1] = static_cast<uint64_t>(w >> 64);
+    __builtin_memcpy(&v, q, 16);
+    return v;
+}
 // Rows whose length is no multiple of 16 begin anywhere, and the last 16 bytes
 // of the last ones may end behind x. The load is moved back to x's last 16
-// bytes then, and its bytes back to their places where they are used.
-struct OddX {
-    int64_t total;  // T * K
-    __device__ __forceinline__ int64_t from(int64_t off) const {
-        const int64_t last = total - 16;
-        return off < last ? off : last < 0 ? 0 : last;
+// bytes then, and its bytes back to their places where they are used: only
+// the last tile of k needs that. Offsets are from token t0's row.
+struct RowEnd {
+    int last;   // of the offsets with 16 bytes of x behind them (may be negative)
+    int bytes;  // of x, where they are fewer than 16
+    __device__ __forceinline__ RowEnd(const LinearW8Args &a, int t0) {
+        const int64_t behind = static_cast<int64_t>(a.T - t0) * a.K - 16, all = static_cast<int64_t>(a.T) * a.K;
+        last = static_cast<int>(behind < 0x7FFFFFFF ? behind : 0x7FFFFFFF);
+        bytes = all < 16 ? static_cast<int>(all) : 0;
     }
-    __device__ __forceinline__ v4i load(const int8_t *x, int64_t off) const {
-        if (total >= 16) return load16(x + from(off));
+    __device__ __forceinline__ v4i load(const int8_t *x, int off) const {
+        if (bytes == 0) return load16(x + min(off, last));
         int8_t b[16] = {};
-        for (int i = 0; i < static_cast<int>(total); ++i) b[i] = x[i];
+        for (int i = 0; i < bytes; ++i) b[i] = x[i];  // then t0 is 0
         v4i v;
         __builtin_memcpy(&v, b, 16);
         return v;
     }
-    __device__ __forceinline__ v4i place(v4i v, int64_t off) const {
-        const int64_t by = off - from(off);  // 0 but behind the end
-        if (by == 0) return v;
-        uint64_t q[2];
-        __builtin_memcpy(q, &v, 16);
-        const int s = static_cast<int>(by < 15 ? by : 15) * 8;
-        const unsigned __int128 w = ((static_cast<unsigned __int128>(q[1]) << 64) | q[0]) >> s;
-        q[0] = static_cast<uint64_t>(w);
-        q[1] = static_cast<uint64_t>(w >> 64);
-        __builtin_memcpy(&v, q, 16);
-        return v;
+    __device__ __forceinline__ v4i place(v4i v, int off) const {
+        return shift_down(v, max(off - (bytes == 0 ? last : 0), 0));
     }
 };
 
@@ -133,63 +134,85 @@ __device__ __forceinline__ void finish(const LinearW8Args &a, int nt, int kq, in
     }
 }
 
-// Few tokens: a workgroup takes 16 weight rows, its WAVES waves every WAVES-th
-// tile of 128 k, loaded DEPTH tiles ahead; the waves' sums meet in LDS.
+// Few tokens: a workgroup takes R tiles of 16 weight rows and ROWS tokens, its
+// WAVES waves every WAVES-th tile of 128 k, loaded DEPTH tiles ahead; the waves'
+// sums meet in LDS.
 //
 // Whole rows of x are loaded and turned to operands in LDS, in a place of the
 // wave's own. Nothing is masked: tokens past the end read the last token's x
 // (columns that are not stored), k past the end meets zero weights.
-template <int ROWS, bool ODD>
-__global__ __launch_bounds__(8 * kWave) void linear_w8_few_kernel(LinearW8Args a) {
+template <int ROWS, int R, bool ODD>
+__global__ __launch_bounds__(8 * kWave) void linear_w8_few_kernel(LinearW8Args a, int token_blocks) {
     constexpr int WAVES = 8, DEPTH = 2;
     constexpr int MT = (ROWS + 15) / 16;
-    constexpr int kL = (ROWS + 7) / 8;  // loads of x per tile: 8 rows each
-    constexpr int kStage = WAVES * MT * 2048, kRed = WAVES * MT * kWave * 16;
+    constexpr int kL = (ROWS + 7) / 8;               // loads of x per tile: 8 rows each
+    constexpr int kPer = kL > 1 ? 2 : 1;             // of them per token tile
+    constexpr int kBufs = MT > 1 ? 2 : 1;            // token tiles in a wave's place
+    constexpr int kSums = R * MT, kJoin = kSums < WAVES ? kSums : WAVES;  // tiles of sums, and those joined at once
+    constexpr int kStage = WAVES * kBufs * 2048, kRed = WAVES * kJoin * kWave * 16;
     __shared__ __attribute__((aligned(16))) char lds[kStage > kRed ? kStage : kRed];
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int r = lane & 15, kq = lane >> 4;
-    const int nt = blockIdx.x, t0 = blockIdx.y * ROWS;
-    char *place = lds + wave * MT * 2048;
-    const OddX odd{static_cast<int64_t>(a.T) * a.K};
+    // Workgroups b, b + 8, ... run on one XCD: each gets consecutive pairs of a
+    // row block and a token block, token blocks first, so that the weights of a
+    // row block come from one XCD's L2.
+    const int row_blocks = (a.n_tiles + R - 1) / R, share = gridDim.x >> 3;
+    const int pair = static_cast<int>(blockIdx.x & 7) * share + static_cast<int>(blockIdx.x >> 3);
+    if (pair >= row_blocks * token_blocks) return;
+    const int nt0 = pair / token_blocks * R, t0 = pair % token_blocks * ROWS;
+    char *place = lds + wave * kBufs * 2048;
+    const int8_t *x = a.x + static_cast<size_t>(t0) * a.K;
+    const RowEnd end(a, t0);
     const int count = (a.k_tiles - wave + WAVES - 1) / WAVES;  // the wave's tiles; <= 0: none
     struct Tile {
-        v4i codes[2];
+        v4i codes[R][2];
         v4i x[kL];
     };
-    auto offset = [&](int i, int j) -> int64_t {  // of the lane's j-th load of its i-th tile
-        const int kt = wave + min(i, count - 1) * WAVES;
-        const int t = min(t0 + j * 8 + lane / 8, a.T - 1);
-        int k = kt * kTileK + lane % 8 * 16;
-        k = ODD ? min(k, a.K - 1) : min(k, a.K - 16);
-        return static_cast<int64_t>(t) * a.K + k;
-    };
+    int row_off[kL];  // at most 64 rows of 2^16 bytes
+#pragma unroll
+    for (int j = 0; j < kL; ++j) row_off[j] = min(j * 8 + lane / 8, a.T - 1 - t0) * a.K;
+    auto tile_of = [&](int i) { return wave + min(i, count - 1) * WAVES; };  // past the end: the last one again
+    auto offset = [&](int kt, int j) { return row_off[j] + min(kt * kTileK + lane % 8 * 16, ODD ? a.K - 1 : a.K - 16); };
     auto fetch = [&](int i, Tile &f) {
-        const int kt = wave + min(i, count - 1) * WAVES;
-        const int8_t *w = a.codes + (static_cast<size_t>(nt) * a.k_tiles + kt) * kTileBytes + lane * 16;
+        const int kt = tile_of(i);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) f.codes[h] = load16(w + h * 1024);
+        for (int j = 0; j < R; ++j) {  // rows past the end: the last tile, not stored
+            const int8_t *w = a.codes + (static_cast<size_t>(min(nt0 + j, a.n_tiles - 1)) * a.k_tiles + kt) * kTileBytes + lane * 16;
 #pragma unroll
-        for (int j = 0; j < kL; ++j) f.x[j] = ODD ? odd.load(a.x, offset(i, j)) : load16(a.x + offset(i, j));
-    };
-    v4i acc[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) acc[m] = v4i{0, 0, 0, 0};
-    typedef __attribute__((address_space(3))) volatile v4i own_lds;  // one wave's own: in order without a barrier
-    auto multiply = [&](int i, const Tile &f) {
-#pragma unroll
-        for (int j = 0; j < kL; ++j) {
-            const int row = j * 8 + lane / 8;
-            *(own_lds *)(place + row / 16 * 2048 + x_at(row % 16, lane % 8)) = ODD ? odd.place(f.x[j], offset(i, j)) : f.x[j];
+            for (int h = 0; h < 2; ++h) f.codes[j][h] = load16(w + h * 1024);
         }
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int j = 0; j < kL; ++j) f.x[j] = ODD ? end.load(x, offset(kt, j)) : load16(x + offset(kt, j));
+    };
+    v4i acc[R][MT];
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[j][m] = v4i{0, 0, 0, 0};
+    typedef __attribute__((address_space(3))) volatile v4i own_lds;  // one wave's own: in order without a barrier
+    auto multiply = [&](int i, Tile &f) {
+        if (ODD && tile_of(i) == a.k_tiles - 1) {  // the only tile that reaches behind x
+#pragma unroll
+            for (int j = 0; j < kL; ++j) f.x[j] = end.place(f.x[j], offset(tile_of(i), j));
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            char *buf = place + m % kBufs * 2048;
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) *(own_lds *)(buf + x_at(j * 8 + lane / 8, lane % 8)) = f.x[m * kPer + j];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const v4i xf = *(own_lds *)(place + m * 2048 + x_at(r, h * 4 + kq));
-                acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.codes[h], xf, acc[m], 0, 0, 0);
+                const v4i xf = *(own_lds *)(buf + x_at(r, h * 4 + kq));
+#pragma unroll
+                for (int j = 0; j < R; ++j)
+                    acc[j][m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.codes[j][h], xf, acc[j][m], 0, 0, 0);
             }
+        }
     };
+    // Loads complete in the order of their issue, and the compiler counts them
+    // exactly only where none is conditional: the loop refills all DEPTH tiles,
+    // and the last round, which refills none, stands behind it.
     if (count > 0) {
         Tile ring[DEPTH];
 #pragma unroll
@@ -206,24 +229,307 @@ __global__ __launch_bounds__(8 * kWave) void linear_w8_few_kernel(LinearW8Args a
         for (int d = 0; d < DEPTH; ++d)
             if (i + d < count) multiply(i + d, ring[d]);
     }
-    v4i(*red)[MT][kWave] = reinterpret_cast<v4i(*)[MT][kWave]>(lds);
-    __syncthreads();  // the places are read until here
+    v4i(*red)[kJoin][kWave] = reinterpret_cast<v4i(*)[kJoin][kWave]>(lds);
 #pragma unroll
-    for (int m = 0; m < MT; ++m) red[wave][m][lane] = acc[m];
-    __syncthreads();
-    if (wave >= MT) return;
-    v4i sum = red[0][wave][lane];
+    for (int p = 0; p < kSums; p += kJoin) {
+        __syncthreads();  // the places, or the sums before, are read until here
 #pragma unroll
-    for (int w = 1; w < WAVES; ++w) sum += red[w][wave][lane];
-    const int t = t0 + wave * 16 + r;
-    if (t < a.T) finish(a, nt, kq, t, sum);
+        for (int i = 0; i < kJoin; ++i) red[wave][i][lane] = acc[(p + i) / MT][(p + i) % MT];
+        __syncthreads();
+        if (wave >= kJoin) continue;
+        v4i sum = red[0][wave][lane];
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) sum += red[w][wave][lane];
+        const int nt = nt0 + (p + wave) / MT, t = t0 + (p + wave) % MT * 16 + r;
+        if (nt < a.n_tiles && t < a.T && (ROWS >= 16 || r < ROWS)) finish(a, nt, kq, t, sum);
+    }
 }
 
-template <int ROWS>
+// Many tokens: the matrix rate is what counts. A workgroup takes 16 MT tokens
+// and 64 NW weight rows, NW tiles of 16 for each of its four waves. Only x goes
+// through LDS, where all waves read it, one tile of 128 k (a stage) at a time;
+// weights come packed in operand order and go from memory to the wave's
+// registers, a stage ahead. Per stage a wave reads 2 MT KB of LDS for 2 MT NW
+// products of 16 cycles: four waves take 64 MT of their 32 MT NW cycles at 128
+// bytes a cycle, half of the time with NW = 4. (With both operands in LDS and
+// 64 x 64 sums per wave, reading LDS would take all of it.)
+//
+// x lies in four buffers, stage s in buffer s % 4, copied straight to LDS two
+// stages ahead (into a buffer whose operands every wave has multiplied by the
+// last barrier, not only asked for), eight rows of 128 bytes an instruction: a lane fetches the
+// 16-byte chunk that belongs at its place (x_at). Rows of ODD length are not
+// aligned for such copies: they go through registers, a stage ahead.
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(1))) void glb_void;
+constexpr int kManyWaves = 4;
+
+// The sums of a wave, NW row tiles from nt0 by MT token tiles from t0, to out
+// in elements of E bytes. Lanes hold up to four neighbouring outputs of a token
+// each; through LDS of the wave's own (its lanes' accesses in order, for the
+// compiler too) they become 16 bytes of a row that neighbouring lanes continue.
+template <int NW>
+constexpr int kPlaceBytes = 16 * (NW * 16 * 4 + 16);
+template <int MT, int NW, int E, bool GATED>
+__device__ __forceinline__ void write_sums(const LinearW8Args &a, const v4i (&acc)[NW][MT], int nt0, int t0, int lane,
+                                           char *place) {
+    typedef int v2i __attribute__((ext_vector_type(2)));
+    constexpr int kUnits = NW * (GATED ? 8 : 16), kRow = kUnits * E + 16;  // outputs of a token, and their bytes in LDS
+    constexpr int kPer = 16 / E, kLanes = kUnits / kPer, kTokens = kWave / kLanes;
+    const int r = lane & 15, kq = lane >> 4;
+    const int units = GATED ? a.N / 2 : a.N, n0 = nt0 * (GATED ? 8 : 16);
+    const bool fp16 = a.out_dtype == MOE_DTYPE_FP16;
+    float ws[NW][4], bias[NW][4] = {};
+#pragma unroll
+    for (int j = 0; j < NW; ++j) {
+        const int nt = min(nt0 + j, a.n_tiles - 1);
+        __builtin_memcpy(ws[j], a.scale + nt * 16 + kq * 4, 16);
+        if (a.bias) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int n = GATED ? nt * 8 + kq * 2 + i / 2 : nt * 16 + kq * 4 + i;
+                bias[j][i] = a.bias[min(n, units - 1) + (GATED && (i & 1) ? units : 0)];
+            }
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        const float xs = a.x_scale[min(t0 + m * 16 + r, a.T - 1)];
+#pragma unroll
+        for (int j = 0; j < NW; ++j) {
+            float o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                o[i] = dequant(acc[j][m][i], ws[j][i], xs);
+                if (a.bias) o[i] += bias[j][i];
+            }
+            char *at = place + r * kRow;
+            if constexpr (GATED) {
+                const float u = swiglu_y(o[0], o[1]), v = swiglu_y(o[2], o[3]);
+                if constexpr (E == 4) {
+                    *(__attribute__((address_space(3))) volatile v2i *)(at + j * 32 + kq * 8) =
+                        v2i{__float_as_int(u), __float_as_int(v)};
+                } else {
+                    *(__attribute__((address_space(3))) volatile int *)(at + j * 16 + kq * 4) =
+                        bits16(u, fp16) | static_cast<int>(bits16(v, fp16)) << 16;
+                }
+            } else if constexpr (E == 4) {
+                *(__attribute__((address_space(3))) volatile v4i *)(at + j * 64 + kq * 16) =
+                    v4i{__float_as_int(o[0]), __float_as_int(o[1]), __float_as_int(o[2]), __float_as_int(o[3])};
+            } else {
+                *(__attribute__((address_space(3))) volatile v2i *)(at + j * 32 + kq * 8) =
+                    v2i{bits16(o[0], fp16) | static_cast<int>(bits16(o[1], fp16)) << 16,
+                        bits16(o[2], fp16) | static_cast<int>(bits16(o[3], fp16)) << 16};
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < (16 + kTokens - 1) / kTokens; ++i) {
+            const int row = i * kTokens + lane / kLanes, n = lane % kLanes * kPer, t = t0 + m * 16 + row;
+            if (row >= 16 || t >= a.T) continue;
+            const v4i v = *(__attribute__((address_space(3))) volatile v4i *)(place + row * kRow + n * E);
+            char *p = static_cast<char *>(a.out) + (static_cast<size_t>(t) * units + n0 + n) * E;
+            const int left = units - n0 - n;
+            if (left >= kPer) __builtin_memcpy(p, &v, 16);
+            else if (left > 0) {
+                char b[16];
+                __builtin_memcpy(b, &v, 16);
+#pragma unroll
+                for (int e = 0; e < kPer; ++e)
+                    if (e < left) __builtin_memcpy(p + e * E, b + e * E, E);
+            }
+        }
+    }
+}
+
+template <int MT, int NW, bool ODD>
+__global__ __launch_bounds__(kManyWaves *kWave, MT *NW >= 64 ? 1 : 2) void linear_w8_many_kernel(LinearW8Args a,
+                                                                                             int token_blocks,
+                                                                                             int row_blocks) {
+    constexpr int kStage = MT * 2048, kCopies = MT / 2;  // copies of 1 KB per wave and stage
+    constexpr int kAhead = MT >= 4 ? 4 : 2;              // operands of x on their way from LDS
+    constexpr int kBuffer = kStage > kPlaceBytes<NW> ? kStage : kPlaceBytes<NW>;
+    __shared__ __attribute__((aligned(16))) char s_x0[kBuffer], s_x1[kBuffer], s_x2[kBuffer], s_x3[kBuffer];
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int r = lane & 15, kq = lane >> 4;
+
+    // Workgroups b, b + 8, ... run on one XCD: each gets consecutive tiles, in
+    // groups of 8 token blocks, so that those in flight share both operands in its L2.
+    const int total = token_blocks * row_blocks, b8 = total & ~7;
+    int b = blockIdx.x;
+    if (b < b8) b = (b & 7) * (b8 >> 3) + (b >> 3);
+    const int group = b / (8 * row_blocks), in = b - group * 8 * row_blocks;
+    const int wide = min(8, token_blocks - group * 8);
+    const int t0 = (group * 8 + in % wide) * MT * 16, nt0 = (in / wide * kManyWaves + wave) * NW;
+
+    uint32_t row_off[kCopies];  // of x's rows from token t0's: at most 256 of 2^16 bytes
+    int chunk[kCopies];
+    const int8_t *x = a.x + static_cast<size_t>(t0) * a.K;
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) {
+        const int row = (wave * kCopies + i) * 8 + lane / 8;  // rows past the end: the last one, not stored
+        row_off[i] = static_cast<uint32_t>(min(row, a.T - 1 - t0)) * static_cast<uint32_t>(a.K);
+        chunk[i] = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
+    }
+    const int last = a.k_tiles - 1;
+    auto x_off = [&](int s, int i) {  // k past the end: the row's last, which meets zero weights
+        return row_off[i] + static_cast<uint32_t>(min(s * kTileK + chunk[i], ODD ? a.K - 1 : a.K - 16));
+    };
+    auto copy_x = [&](int s, char *buf) {
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i)
+            __builtin_amdgcn_global_load_lds((glb_void *)(x + x_off(s, i)), (lds_void *)(buf + (wave * kCopies + i) * 1024),
+                                             16, 0, 0);
+    };
+    // ODD: loads that would end behind x are moved back (RowEnd); only the last
+    // stage's bytes are moved in turn, by `place`, so that the loop has none of it.
+    const RowEnd end(a, t0);
+    auto fetch_x = [&](int s, v4i (&v)[kCopies]) {
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) v[i] = load16(x + min(static_cast<int>(x_off(s, i)), end.last));
+    };
+    auto put_x = [&](const v4i (&v)[kCopies], char *buf) {
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) *reinterpret_cast<v4i *>(buf + (wave * kCopies + i) * 1024 + lane * 16) = v[i];
+    };
+    auto bring_x = [&](int s, char *buf) {
+        v4i v[kCopies];
+        fetch_x(s, v);
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) v[i] = end.place(v[i], static_cast<int>(x_off(s, i)));
+        put_x(v, buf);
+    };
+    const int8_t *w[NW];  // rows past the end: the last tile, not stored
+#pragma unroll
+    for (int j = 0; j < NW; ++j)
+        w[j] = a.codes + static_cast<size_t>(min(nt0 + j, a.n_tiles - 1)) * a.k_tiles * kTileBytes + lane * 16;
+    auto fetch_w = [&](int s, v4i (&f)[NW][2]) {
+#pragma unroll
+        for (int j = 0; j < NW; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) f[j][h] = load16(w[j] + static_cast<size_t>(s) * kTileBytes + h * 1024);
+    };
+    v4i acc[NW][MT];
+#pragma unroll
+    for (int j = 0; j < NW; ++j)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[j][m] = v4i{0, 0, 0, 0};
+    v4i xf[kAhead];
+    auto read_x = [&](const char *buf, int q) {  // operand q = half * MT + token tile
+        xf[q % kAhead] = *reinterpret_cast<const v4i *>(buf + (q % MT) * 2048 + x_at(r, q / MT * 4 + kq));
+    };
+    // vmcnt: copies of stage s + 1 have landed when no more than what was issued after them is left
+    constexpr int kLeft = kCopies + 4 * NW;
+    static_assert(kLeft <= 63 && 2 * MT > kAhead, "");
+    constexpr int kWait = (kLeft & 15) | ((kLeft >> 4) << 14) | (7 << 4) | (15 << 8);
+    // Stage s from `cur`, whose first kAhead operands have been read; the next
+    // stage's are read at its end.
+    auto step = [&](int s, const v4i (&now)[NW][2], v4i (&next)[NW][2], v4i (&xr)[kCopies], const char *cur,
+                    char *later, char *ahead) {
+        if constexpr (ODD) fetch_x(min(s + 2, last), xr);
+        else copy_x(min(s + 2, last), ahead);
+        fetch_w(min(s + 1, last), next);
+#pragma unroll
+        for (int q = 0; q < 2 * MT; ++q) {
+            if (q == 2 * MT - kAhead) {
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (!ODD) __builtin_amdgcn_s_waitcnt(kWait);
+                asm volatile("" ::: "memory");  // for the compiler; the LDS takes a wave's accesses in order
+                __builtin_amdgcn_s_barrier();
+                asm volatile("" ::: "memory");
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int j = 0; j < NW; ++j)
+                acc[j][q % MT] = __builtin_amdgcn_mfma_i32_16x16x64_i8(now[j][q / MT], xf[q % kAhead], acc[j][q % MT], 0, 0, 0);
+            if (q + kAhead < 2 * MT) read_x(cur, q + kAhead);
+            else read_x(later, q + kAhead - 2 * MT);
+            // as written: the scheduler would draw the reads together and wait for all of them
+            __builtin_amdgcn_sched_group_barrier(0x8, NW, 0);    // MFMA
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // LDS read
+        }
+        if constexpr (ODD) put_x(xr, ahead);
+    };
+    v4i w0[NW][2], w1[NW][2], xr[kCopies];
+    if constexpr (ODD) {
+        fetch_x(0, xr);
+        put_x(xr, s_x0);
+        fetch_x(min(1, last), xr);
+        put_x(xr, s_x1);
+    } else {
+        copy_x(0, s_x0);
+        copy_x(min(1, last), s_x1);
+    }
+    fetch_w(0, w0);
+    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) read_x(s_x0, q);
+    // Groups of four stages, then the few that are left (an exit inside the
+    // group would cost the sums their registers); for ODD the last stage is
+    // always among these.
+    int s = 0;
+    for (; s + 4 + (ODD ? 1 : 0) <= a.k_tiles; s += 4) {
+        step(s, w0, w1, xr, s_x0, s_x1, s_x2);
+        step(s + 1, w1, w0, xr, s_x1, s_x2, s_x3);
+        step(s + 2, w0, w1, xr, s_x2, s_x3, s_x0);
+        step(s + 3, w1, w0, xr, s_x3, s_x0, s_x1);
+    }
+    if (s < a.k_tiles) {
+        if constexpr (ODD) {
+            __syncthreads();  // the buffers are read until here
+            bring_x(s, s_x0);
+            bring_x(min(s + 1, last), s_x1);
+            bring_x(min(s + 2, last), s_x2);
+            bring_x(min(s + 3, last), s_x3);
+        } else {
+            copy_x(min(s + 2, last), s_x2);
+        }
+        __builtin_amdgcn_s_waitcnt(0x0070);
+        __syncthreads();
+        for (int i = 0; s + i < a.k_tiles; ++i) {
+            const char *buf = i == 0 ? s_x0 : i == 1 ? s_x1 : i == 2 ? s_x2 : s_x3;
+            fetch_w(min(s + i + 1, last), w1);
+#pragma unroll
+            for (int q = 0; q < 2 * MT; ++q) {
+                const v4i v = *reinterpret_cast<const v4i *>(buf + (q % MT) * 2048 + x_at(r, q / MT * 4 + kq));
+#pragma unroll
+                for (int j = 0; j < NW; ++j)
+                    acc[j][q % MT] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w0[j][q / MT], v, acc[j][q % MT], 0, 0, 0);
+            }
+#pragma unroll
+            for (int j = 0; j < NW; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) w0[j][h] = w1[j][h];
+        }
+    }
+    __builtin_amdgcn_s_waitcnt(0x0070);  // copies past the last stage have landed before the LDS is used again
+    __syncthreads();
+    char *place = wave == 0 ? s_x0 : wave == 1 ? s_x1 : wave == 2 ? s_x2 : s_x3;
+    if (a.out_dtype == MOE_DTYPE_FP32) {
+        if (a.gated) write_sums<MT, NW, 4, true>(a, acc, nt0, t0, lane, place);
+        else write_sums<MT, NW, 4, false>(a, acc, nt0, t0, lane, place);
+    } else {
+        if (a.gated) write_sums<MT, NW, 2, true>(a, acc, nt0, t0, lane, place);
+        else write_sums<MT, NW, 2, false>(a, acc, nt0, t0, lane, place);
+    }
+}
+
+template <int MT, int NW>
+hipError_t launch_many(const LinearW8Args &a, hipStream_t s) {
+    const int token_blocks = (a.T + MT * 16 - 1) / (MT * 16), rows = kManyWaves * NW;
+    const int row_blocks = (a.n_tiles + rows - 1) / rows;
+    const dim3 grid(static_cast<unsigned>(row_blocks) * token_blocks), blk(kManyWaves * kWave);
+    if (a.K % 16) hipLaunchKernelGGL((linear_w8_many_kernel<MT, NW, true>), grid, blk, 0, s, a, token_blocks, row_blocks);
+    else hipLaunchKernelGGL((linear_w8_many_kernel<MT, NW, false>), grid, blk, 0, s, a, token_blocks, row_blocks);
+    return hipGetLastError();
+}
+
+template <int ROWS, int R>
 hipError_t launch_few(const LinearW8Args &a, hipStream_t s) {
-    const dim3 grid(a.n_tiles, (a.T + ROWS - 1) / ROWS), blk(8 * kWave);
-    if (a.K % 16) hipLaunchKernelGGL((linear_w8_few_kernel<ROWS, true>), grid, blk, 0, s, a);
-    else hipLaunchKernelGGL((linear_w8_few_kernel<ROWS, false>), grid, blk, 0, s, a);
+    const int token_blocks = (a.T + ROWS - 1) / ROWS, row_blocks = (a.n_tiles + R - 1) / R;
+    const dim3 grid((static_cast<unsigned>(row_blocks) * token_blocks + 7) / 8 * 8), blk(8 * kWave);
+    if (a.K % 16) hipLaunchKernelGGL((linear_w8_few_kernel<ROWS, R, true>), grid, blk, 0, s, a, token_blocks);
+    else hipLaunchKernelGGL((linear_w8_few_kernel<ROWS, R, false>), grid, blk, 0, s, a, token_blocks);
     return hipGetLastError();
 }
 
@@ -241,10 +547,39 @@ hipError_t launch_pack_w8(const int8_t *codes, const float *scale, int8_t *dst_c
     return hipGetLastError();
 }
 
+// Which kernel: the few-token one splits K over a workgroup's waves, so it fills
+// the chip where there are few tiles of outputs, but it reads x for every 16 R
+// weight rows and joins eight sums; it wants one workgroup for each CU, of the
+// least x and weights (16 R rows, ROWS tokens). The other wants two large
+// workgroups a CU, or more small ones; with a short K, small ones, whose ends
+// overlap others' products. In us (bf16 out; few tokens / many, * taken):
+//   T 64, N 4096, K 4096: 32 x 2 *6.3, 64 x 4 10.9 / 12.5   T 128, N 8192: 64 x 4 *11.7 / 13.4
+//   T 37, N 5006, K 4256, gated: 16 x 4 *6.8, 64 x 4 10.7 / 13.7    T 512, N 4096: 19.7 / 64 x 4 *16.8
+//   T 1000, N 1000, K 1000: 7.8 / 32 x 4 *5.4              T 64, N 28672: 33.5 / 64 x 4 *28.2, 64 x 8 32.4
+// many, tokens x row tiles 128 x 16, 128 x 8, 64 x 8, 64 x 4, 32 x 4, K 4096:
+//   T 4096, N 8192 *135 162 176 222 270     T 2048, N 4096 43 *39 43 53 68     T 512, N 8192 39 28 *24 28 35
+//   T 256, N 8192 38 27 21 *17 18           T 256, N 4096 38 27 20 16 13 (few: *10.9)
+//   K 700, T 2500, N 5000: 27 32 *25 31 32
 hipError_t launch_linear_w8(const LinearW8Args &a, hipStream_t s) {
-    if (a.T <= 8) return launch_few<8>(a, s);
-    if (a.T <= 16) return launch_few<16>(a, s);
-    return launch_few<64>(a, s);
+    auto blocks = [&](int tokens, int tiles) {
+        return static_cast<int64_t>((a.T + tokens - 1) / tokens) * ((a.n_tiles + tiles - 1) / tiles);
+    };
+    if (a.T <= 8) return launch_few<8, 1>(a, s);
+    if (a.T <= 16) return a.n_tiles < 512 ? launch_few<16, 1>(a, s) : launch_few<16, 2>(a, s);
+    if (blocks(64, 4) <= 256 && (a.T <= 64 || a.k_tiles >= 16)) {
+        if (blocks(16, 1) <= 256) return launch_few<16, 1>(a, s);
+        if (blocks(16, 2) <= 256) return launch_few<16, 2>(a, s);
+        if (blocks(32, 2) <= 256) return launch_few<32, 2>(a, s);
+        if (blocks(16, 4) <= 256) return launch_few<16, 4>(a, s);
+        if (blocks(32, 4) <= 256) return launch_few<32, 4>(a, s);
+        return launch_few<64, 4>(a, s);
+    }
+    // more than 16 tokens from here: x has the 16 bytes that the kernel for many takes for granted
+    if (a.k_tiles >= 16 && blocks(128, 16) >= 512) return launch_many<8, 4>(a, s);
+    if (a.k_tiles >= 16 && blocks(128, 8) >= 400) return launch_many<8, 2>(a, s);
+    if (blocks(64, 8) >= 400) return launch_many<4, 2>(a, s);
+    if (blocks(64, 4) >= 384) return launch_many<4, 1>(a, s);
+    return launch_many<2, 1>(a, s);
 }
 
 }  // namespace moe
