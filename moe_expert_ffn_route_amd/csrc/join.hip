@@ -13,6 +13,8 @@
 // operators is memory.
 #include "rowwise.h"
 
+#include <type_traits>
+
 #include "../../include/moe_w8a8.h"
 
 namespace moe {
@@ -27,21 +29,23 @@ __device__ __forceinline__ double wave_sum(double v) {  // in every lane
     return v;
 }
 
-// TPR threads per row, CH chunks of kVec elements per thread: H <= TPR * CH *
-// kVec. A workgroup is one row, or four rows of one wave each. TAIL: H is no
+// A workgroup is one row, its threads as many whole waves as CH chunks of kVec
+// elements each need, or (ONE) four rows of one wave each. TAIL: H is no
 // multiple of kVec. Loads stand behind no branch: lanes past the row's end
 // read its last chunk again and count nothing.
-template <typename T, int TPR, int CH, bool TAIL>
-__global__ __launch_bounds__(TPR *kRows<TPR>) void quant_kernel(QuantArgs a) {
-    constexpr int kWaves = TPR / kWave;
-    const int tr = threadIdx.x % TPR, row = blockIdx.x * kRows<TPR> + threadIdx.x / TPR;
-    if (kRows<TPR> > 1 && row >= a.T) return;  // whole waves, and such a row has no barrier
+template <int CH, bool ONE>
+constexpr int kMost = ONE ? 4 * kWave : 1024;
+template <typename T, int CH, bool TAIL, bool ONE>
+__global__ __launch_bounds__((kMost<CH, ONE>)) void quant_kernel(QuantArgs a) {
+    const int tpr = ONE ? kWave : static_cast<int>(blockDim.x), waves = tpr / kWave;
+    const int tr = ONE ? threadIdx.x % kWave : threadIdx.x, row = ONE ? blockIdx.x * 4 + threadIdx.x / kWave : blockIdx.x;
+    if (ONE && row >= a.T) return;  // whole waves, and such a row has no barrier
     const size_t base = static_cast<size_t>(row) * a.H;
     const T *x = static_cast<const T *>(a.x) + base;
     const int chunks = a.H / kVec, rest = a.H % kVec;
     const bool tail = TAIL && tr < rest;
     const int it = TAIL ? chunks * kVec + min(tr, rest - 1) : 0;
-    auto at = [&](int j) { return min(tr + j * TPR, chunks - 1) * kVec; };
+    auto at = [&](int j) { return min(tr + j * tpr, chunks - 1) * kVec; };
     float p[CH][kVec] = {}, pt = 0.0f;
     if (!TAIL || chunks > 0) {
         float g[CH][kVec];
@@ -64,31 +68,31 @@ __global__ __launch_bounds__(TPR *kRows<TPR>) void quant_kernel(QuantArgs a) {
     float mx = fabsf(pt);
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-        const bool in = tr + j * TPR < chunks;
+        if (tr + j * tpr >= chunks) {  // a branch that most waves do not take, not eight selections
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-            if (!in) p[j][e] = 0.0f;
-            mx = fmaxf(mx, fabsf(p[j][e]));
+            for (int e = 0; e < kVec; ++e) p[j][e] = 0.0f;
         }
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) mx = fmaxf(mx, fabsf(p[j][e]));
     }
     if (!a.group) {
         mx = last_lane_max(mx);
-        __shared__ float s_max[kWaves];
-        if constexpr (kWaves == 1) mx = lane63(mx);
-        else mx = join_waves<kWaves>(mx, s_max, tr, [](float u, float v) { return fmaxf(u, v); });
+        __shared__ float s_max[16];
+        if constexpr (ONE) mx = lane63(mx);
+        else mx = join_waves(mx, s_max, tr, waves, 0.0f, [](float u, float v) { return fmaxf(u, v); });
     }
-    write_codes<TPR, CH, TAIL>(p, pt, mx, 1.0f, a.amax_eps, a.quant == MOE_QUANT_E4M3, a.group, a.H, tr, tail, it,
-                               static_cast<uint8_t *>(a.q) + base,
-                               a.q_scale + static_cast<size_t>(row) * (a.group ? a.H / a.group : 1));
+    write_codes<CH, TAIL>(p, pt, mx, 1.0f, a.amax_eps, a.quant == MOE_QUANT_E4M3, a.group, a.H, tr, tpr, tail, it,
+                          static_cast<uint8_t *>(a.q) + base,
+                          a.q_scale + static_cast<size_t>(row) * (a.group ? a.H / a.group : 1));
 }
 
-template <typename T, typename W, int TPR, int CH, bool TAIL>
-__global__ __launch_bounds__(TPR *kRows<TPR>) void join_norm_kernel(JoinNormArgs a) {
-    constexpr int kWaves = TPR / kWave;
-    __shared__ double s_sq[kWaves];
-    __shared__ float s_sum[kWaves], s_max[kWaves];
-    const int tr = threadIdx.x % TPR, row = blockIdx.x * kRows<TPR> + threadIdx.x / TPR;
-    if (kRows<TPR> > 1 && row >= a.T) return;  // whole waves, and such a row has no barrier
+template <typename T, typename W, int CH, bool TAIL, bool ONE>
+__global__ __launch_bounds__((kMost<CH, ONE>)) void join_norm_kernel(JoinNormArgs a) {
+    __shared__ double s_sq[16];
+    __shared__ float s_sum[16], s_max[16];
+    const int tpr = ONE ? kWave : static_cast<int>(blockDim.x), waves = tpr / kWave;
+    const int tr = ONE ? threadIdx.x % kWave : threadIdx.x, row = ONE ? blockIdx.x * 4 + threadIdx.x / kWave : blockIdx.x;
+    if (ONE && row >= a.T) return;  // whole waves, and such a row has no barrier
     const size_t base = static_cast<size_t>(row) * a.H;
     const T *block = static_cast<const T *>(a.block) + base, *share = static_cast<const T *>(a.share) + base;
     const T *res = static_cast<const T *>(a.residual) + base;
@@ -97,7 +101,7 @@ __global__ __launch_bounds__(TPR *kRows<TPR>) void join_norm_kernel(JoinNormArgs
     const int chunks = a.H / kVec, rest = a.H % kVec;
     const bool tail = TAIL && tr < rest, whole = !TAIL || chunks > 0;
     const int it = TAIL ? chunks * kVec + min(tr, rest - 1) : 0;
-    auto at = [&](int j) { return min(tr + j * TPR, chunks - 1) * kVec; };
+    auto at = [&](int j) { return min(tr + j * tpr, chunks - 1) * kVec; };
 
     // b, and what will be needed later on its way
     float p[CH][kVec] = {}, r[CH][kVec] = {}, pt = 0.0f, rt = 0.0f;
@@ -131,15 +135,12 @@ __global__ __launch_bounds__(TPR *kRows<TPR>) void join_norm_kernel(JoinNormArgs
         double sq = tail ? static_cast<double>(pt) * pt : 0.0;
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
-            const bool in = tr + j * TPR < chunks;
+            if (tr + j * tpr >= chunks) continue;
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) {
-                const double v = in ? p[j][e] : 0.0f;
-                sq = __builtin_fma(v, v, sq);
-            }
+            for (int e = 0; e < kVec; ++e) sq = __builtin_fma(static_cast<double>(p[j][e]), static_cast<double>(p[j][e]), sq);
         }
         sq = wave_sum(sq);
-        if constexpr (kWaves > 1) sq = join_waves<kWaves>(sq, s_sq, tr, [](double u, double v) { return u + v; });
+        if constexpr (!ONE) sq = join_waves(sq, s_sq, tr, waves, 0.0, [](double u, double v) { return u + v; });
         const float rstd = static_cast<float>(1.0 / sqrt(sq / a.H + static_cast<double>(a.post_eps)));
         if (pw && whole) {
             float v[CH][kVec];
@@ -184,7 +185,7 @@ __global__ __launch_bounds__(TPR *kRows<TPR>) void join_norm_kernel(JoinNormArgs
         T *out = static_cast<T *>(a.residual_out) + base;
 #pragma unroll
         for (int j = 0; j < CH; ++j)
-            if (tr + j * TPR < chunks) store8(out + at(j), p[j]);
+            if (tr + j * tpr < chunks) store8(out + at(j), p[j]);
         if (tail) from_f32(pt, out[it]);
     }
     if (!a.y && !a.q) return;  // uniform
@@ -195,14 +196,18 @@ __global__ __launch_bounds__(TPR *kRows<TPR>) void join_norm_kernel(JoinNormArgs
     float sum = 0.0f, mx = 0.0f;
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-        const bool in = tr + j * TPR < chunks;
+        if (tr + j * tpr >= chunks) {
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-            if (!in) p[j][e] = 0.0f;
-            sum += p[j][e] * p[j][e];
-            if (in && w) p[j][e] = p[j][e] * r[j][e];
-            mx = fmaxf(mx, fabsf(p[j][e]));
+            for (int e = 0; e < kVec; ++e) p[j][e] = 0.0f;
         }
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) sum += p[j][e] * p[j][e];
+        if (w) {
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) p[j][e] = p[j][e] * r[j][e];
+        }
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) mx = fmaxf(mx, fabsf(p[j][e]));
     }
     if (TAIL) {
         if (!tail) pt = 0.0f;
@@ -212,22 +217,22 @@ __global__ __launch_bounds__(TPR *kRows<TPR>) void join_norm_kernel(JoinNormArgs
     }
     sum = last_lane_sum(sum);
     mx = last_lane_max(mx);
-    if constexpr (kWaves == 1) {
+    if constexpr (ONE) {
         sum = lane63(sum);
         mx = lane63(mx);
     } else {
         if ((tr & (kWave - 1)) == kWave - 1) s_max[tr / kWave] = mx;
-        sum = join_waves<kWaves>(sum, s_sum, tr, [](float u, float v) { return u + v; });
-        mx = s_max[0];
+        sum = join_waves(sum, s_sum, tr, waves, 0.0f, [](float u, float v) { return u + v; });
+        mx = (tr & 15) < waves ? s_max[tr & 15] : 0.0f;
 #pragma unroll
-        for (int i = 1; i < kWaves; ++i) mx = fmaxf(mx, s_max[i]);
+        for (int d = 8; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor(mx, d, kWave));
     }
     const float rstd = 1.0f / sqrtf(sum / static_cast<float>(a.H) + a.rms_eps);
     if (a.y) {
         T *y = static_cast<T *>(a.y) + base;
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
-            if (tr + j * TPR >= chunks) break;
+            if (tr + j * tpr >= chunks) break;
             float v[kVec];
 #pragma unroll
             for (int e = 0; e < kVec; ++e) v[e] = p[j][e] * rstd;
@@ -236,41 +241,44 @@ __global__ __launch_bounds__(TPR *kRows<TPR>) void join_norm_kernel(JoinNormArgs
         if (tail) from_f32(pt * rstd, y[it]);
     }
     if (!a.q) return;
-    write_codes<TPR, CH, TAIL>(p, pt, mx, rstd, a.amax_eps, a.quant == MOE_QUANT_E4M3, a.group, a.H, tr, tail, it,
-                               static_cast<uint8_t *>(a.q) + base,
-                               a.q_scale + static_cast<size_t>(row) * (a.group ? a.H / a.group : 1));
+    write_codes<CH, TAIL>(p, pt, mx, rstd, a.amax_eps, a.quant == MOE_QUANT_E4M3, a.group, a.H, tr, tpr, tail, it,
+                          static_cast<uint8_t *>(a.q) + base,
+                          a.q_scale + static_cast<size_t>(row) * (a.group ? a.H / a.group : 1));
 }
 
-template <typename T, int TPR, int CH>
-hipError_t quant_rows(const QuantArgs &a, hipStream_t s) {
-    const dim3 grid((a.T + kRows<TPR> - 1) / kRows<TPR>), blk(TPR * kRows<TPR>);
-    if (a.H % kVec) hipLaunchKernelGGL((quant_kernel<T, TPR, CH, true>), grid, blk, 0, s, a);
-    else hipLaunchKernelGGL((quant_kernel<T, TPR, CH, false>), grid, blk, 0, s, a);
-    return hipGetLastError();
+// f(CH, ONE) as constants, and the grid and workgroup that go with them. Short
+// rows: one wave. Else as many waves as the row needs with one chunk a thread
+// (few rows: the shortest way through) or two (many: more rows in flight for
+// their registers). In us, one / two / four chunks: joining norm without post
+// norm, bf16, H 4096, T 8 3.6 / 4.0 / 4.9, T 500 6.7 / 6.9 / 8.1, T 8192 68.1 /
+// 67.3 / 73.4; with post norm and gate, fp16 to E4M3, H 5003, T 700 13.8 / 11.2 /
+// 12.2, T 4001 68 / 56 / 59; quantiser, H 8192, T 3000 13.9 / 13.7 / 13.8.
+template <typename F>
+hipError_t by_length(int T, int H, F f) {
+    const int chunks = H / kVec;
+    if (chunks <= kWave) return f(std::integral_constant<int, 1>{}, std::true_type{}, dim3((T + 3) / 4), dim3(4 * kWave));
+    auto wide = [&](auto ch) {
+        const int threads = ((chunks + ch - 1) / ch + kWave - 1) / kWave * kWave;
+        return f(ch, std::false_type{}, dim3(T), dim3(threads));
+    };
+    return T < 512 && chunks <= 1024 ? wide(std::integral_constant<int, 1>{}) : wide(std::integral_constant<int, 2>{});
 }
+
 template <typename T>
 hipError_t quant_of(const QuantArgs &a, hipStream_t s) {
-    if (a.H <= 64 * kVec) return quant_rows<T, 64, 1>(a, s);
-    if (a.H <= 256 * kVec) return quant_rows<T, 256, 1>(a, s);
-    if (a.H <= 512 * kVec) return quant_rows<T, 256, 2>(a, s);
-    if (a.T < 512) return a.H <= 1024 * kVec ? quant_rows<T, 1024, 1>(a, s) : quant_rows<T, 1024, 2>(a, s);
-    return a.H <= 1024 * kVec ? quant_rows<T, 256, 4>(a, s) : quant_rows<T, 256, 8>(a, s);
-}
-
-template <typename T, typename W, int TPR, int CH>
-hipError_t join_rows(const JoinNormArgs &a, hipStream_t s) {
-    const dim3 grid((a.T + kRows<TPR> - 1) / kRows<TPR>), blk(TPR * kRows<TPR>);
-    if (a.H % kVec) hipLaunchKernelGGL((join_norm_kernel<T, W, TPR, CH, true>), grid, blk, 0, s, a);
-    else hipLaunchKernelGGL((join_norm_kernel<T, W, TPR, CH, false>), grid, blk, 0, s, a);
-    return hipGetLastError();
+    return by_length(a.T, a.H, [&](auto ch, auto one, dim3 grid, dim3 blk) {
+        if (a.H % kVec) hipLaunchKernelGGL((quant_kernel<T, ch, true, one>), grid, blk, 0, s, a);
+        else hipLaunchKernelGGL((quant_kernel<T, ch, false, one>), grid, blk, 0, s, a);
+        return hipGetLastError();
+    });
 }
 template <typename T, typename W>
 hipError_t join_of(const JoinNormArgs &a, hipStream_t s) {
-    if (a.H <= 64 * kVec) return join_rows<T, W, 64, 1>(a, s);
-    if (a.H <= 256 * kVec) return join_rows<T, W, 256, 1>(a, s);
-    if (a.H <= 512 * kVec) return join_rows<T, W, 256, 2>(a, s);
-    if (a.T < 512) return a.H <= 1024 * kVec ? join_rows<T, W, 1024, 1>(a, s) : join_rows<T, W, 1024, 2>(a, s);
-    return a.H <= 1024 * kVec ? join_rows<T, W, 256, 4>(a, s) : join_rows<T, W, 256, 8>(a, s);
+    return by_length(a.T, a.H, [&](auto ch, auto one, dim3 grid, dim3 blk) {
+        if (a.H % kVec) hipLaunchKernelGGL((join_norm_kernel<T, W, ch, true, one>), grid, blk, 0, s, a);
+        else hipLaunchKernelGGL((join_norm_kernel<T, W, ch, false, one>), grid, blk, 0, s, a);
+        return hipGetLastError();
+    });
 }
 
 }  // namespace

@@ -127,9 +127,9 @@ __global__ __launch_bounds__(TPR *kRows<TPR>) void norm_kernel(NormArgs a) {
         if (tail) from_f32(pt * rstd, y[it]);
     }
     if (!a.q) return;
-    write_codes<TPR, CH, TAIL>(p, pt, mx, rstd, a.amax_eps, a.quant == MOE_QUANT_E4M3, a.group, a.H, tr, tail, it,
-                               static_cast<uint8_t *>(a.q) + base,
-                               a.q_scale + static_cast<size_t>(row) * (a.group ? a.H / a.group : 1));
+    write_codes<CH, TAIL>(p, pt, mx, rstd, a.amax_eps, a.quant == MOE_QUANT_E4M3, a.group, a.H, tr, TPR, tail, it,
+                          static_cast<uint8_t *>(a.q) + base,
+                          a.q_scale + static_cast<size_t>(row) * (a.group ? a.H / a.group : 1));
 }
 
 template <typename T, typename W, int TPR, int CH>

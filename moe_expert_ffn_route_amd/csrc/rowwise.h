@@ -51,29 +51,61 @@ __device__ __forceinline__ float last_lane_max(float v) {  // of magnitudes
     return v;
 }
 
-// The same for the workgroup of a row: WAVES waves, `slot` its WAVES words of
-// LDS. One wave needs no barrier.
-template <int WAVES, typename V, typename Join>
-__device__ __forceinline__ V join_waves(V v, V *slot, int tr, Join join) {  // v: lane 63's
+// The same for the workgroup of a row, of `waves` waves (at most 16): lane 63's
+// values meet in `slot`, each lane takes one, and four steps join them, in every
+// lane. With a barrier.
+template <typename V, typename Join>
+__device__ __forceinline__ V join_waves(V v, V *slot, int tr, int waves, V none, Join join) {
     if ((tr & (kWave - 1)) == kWave - 1) slot[tr / kWave] = v;
     __syncthreads();
-    v = slot[0];
+    const int i = tr & 15;
+    v = i < waves ? slot[i] : none;
 #pragma unroll
-    for (int i = 1; i < WAVES; ++i) v = join(v, slot[i]);
+    for (int d = 8; d > 0; d >>= 1) v = join(v, __shfl_xor(v, d, kWave));
     return v;
 }
 
-// Eight codes of a row.
+// Eight codes of a row, t = (v * Q) * inv rounded to nearest even as quant4
+// does, for |t| <= Q (but for its own rounding): int8 by an addition whose sum's
+// last bits are the integer, E4M3 by the hardware's conversion, which gives
+// e4m3_code's bits for every fp32 of up to 464 (both compared once, on all).
 __device__ __forceinline__ uint64_t quant8(const float (&v)[kVec], float inv, bool fp8) {
-    uint32_t lo, hi;
+    uint32_t w[2];
     if (fp8) {
-        lo = quant4<true>(v[0], v[1], v[2], v[3], inv);
-        hi = quant4<true>(v[4], v[5], v[6], v[7], inv);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float t[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) t[e] = v[4 * h + e] * kQMax<true> * inv;
+            const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], 0, false);
+            w[h] = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], lo, true));
+        }
     } else {
-        lo = quant4<false>(v[0], v[1], v[2], v[3], inv);
-        hi = quant4<false>(v[4], v[5], v[6], v[7], inv);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t b[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) b[e] = __float_as_uint(v[4 * h + e] * kQMax<false> * inv + 12582912.0f);  // 1.5 * 2^23
+            const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0C0C0400), hi = __builtin_amdgcn_perm(b[3], b[2], 0x04000C0C);
+            w[h] = lo | hi;
+        }
     }
-    return lo | (static_cast<uint64_t>(hi) << 32);
+    return w[0] | (static_cast<uint64_t>(w[1]) << 32);
+}
+
+// Maximum over aligned runs of 8, 16 or 32 lanes, in all of them: DPP swaps of
+// neighbours and of pairs, the mirrors of half rows and rows, and one shuffle.
+template <int CTRL>
+__device__ __forceinline__ float dpp_max(float v) {
+    return fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true)));
+}
+__device__ __forceinline__ float run_max(float v, int lanes) {
+    v = dpp_max<0xB1>(v);
+    v = dpp_max<0x4E>(v);
+    v = dpp_max<0x141>(v);
+    if (lanes >= 16) v = dpp_max<0x140>(v);
+    if (lanes >= 32) v = fmaxf(v, __shfl_xor(v, 16, kWave));
+    return v;
 }
 
 // Rows per workgroup: four of one wave each, or one.
@@ -81,10 +113,10 @@ template <int TPR>
 constexpr int kRows = TPR == kWave ? 4 : 1;
 
 // Codes and scales of the row's p (zero behind its end) times rstd, mx = max|p|.
-// Thread tr holds chunk tr + j * TPR and, TAIL, element `it` if `tail`.
-template <int TPR, int CH, bool TAIL>
+// Thread tr of tpr holds chunks tr + j * tpr and, TAIL, element `it` if `tail`.
+template <int CH, bool TAIL>
 __device__ __forceinline__ void write_codes(const float (&p)[CH][kVec], float pt, float mx, float rstd, float eps,
-                                            bool fp8, int group, int H, int tr, bool tail, int it, uint8_t *q,
+                                            bool fp8, int group, int H, int tr, int tpr, bool tail, int it, uint8_t *q,
                                             float *scale) {
     const int chunks = H / kVec;
     const float top_inv = fp8 ? 1.0f / kQMax<true> : 1.0f / kQMax<false>;
@@ -93,12 +125,12 @@ __device__ __forceinline__ void write_codes(const float (&p)[CH][kVec], float pt
         const int gl = group / kVec;
 #pragma unroll
         for (int j = 0; j < CH; ++j) {
-            if (j * TPR >= chunks) break;  // uniform
+            if (j * tpr >= chunks) break;  // uniform
             float pm = 0.0f;
 #pragma unroll
             for (int e = 0; e < kVec; ++e) pm = fmaxf(pm, fabsf(p[j][e]));
-            for (int d = gl / 2; d > 0; d >>= 1) pm = fmaxf(pm, __shfl_xor(pm, d, kWave));
-            const int c = tr + j * TPR;
+            pm = run_max(pm, gl);
+            const int c = tr + j * tpr;
             if (c >= chunks) continue;
             const float am = pm * rstd;
             const uint64_t code = quant8(p[j], inv_of(pm, am), fp8);
@@ -110,7 +142,7 @@ __device__ __forceinline__ void write_codes(const float (&p)[CH][kVec], float pt
     const float am = mx * rstd, inv = inv_of(mx, am);
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-        const int c = tr + j * TPR;
+        const int c = tr + j * tpr;
         if (c >= chunks) break;
         const uint64_t code = quant8(p[j], inv, fp8);
         __builtin_memcpy(q + c * kVec, &code, sizeof code);

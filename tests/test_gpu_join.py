@@ -333,14 +333,20 @@ def test_join_in_place(T, H):
 
 
 def test_join_is_the_norm_where_the_branch_is_nothing():
-    """Without a branch it is moe_w8a8_norm_quant of x + residual, bit for bit."""
+    """Without a branch it is moe_w8a8_norm_quant of x + residual: the stream
+    and the codes bit for bit; y and the scales but for the order of the sum of
+    squares, each side's rstd off by at most 54 u (see above): 108 u, after
+    which two roundings to bf16 are at most one step (2 eps / 2) apart."""
     for T, H in ((5, 512), (9, 5003), (3, 16384)):
         c = inputs(T, H, BF, BF, share=False, post=False, gate=None, seed=2)
         got = join(c, False, rs=1.0, bs=1.0, eps=(1e-5, 1e-6, EPS))
         want = {k: torch.empty_like(v) for k, v in got.items()}
         moe.moe_w8a8_norm_quant(moe.make_norm_dims(T, H), c["block"], c["weight"], residual=c["residual"], **want)
-        for k in want:
+        for k in ("residual_out", "q"):
             assert torch.equal(got[k].view(torch.uint8), want[k].view(torch.uint8)), k
+        for k, step in (("y", torch.finfo(BF).eps), ("q_scale", 0)):
+            a, b = got[k].double(), want[k].double()
+            assert bool(((a - b).abs() <= (108 * U + step) * torch.maximum(a.abs(), b.abs())).all()), k
 
 
 def test_join_other_rows_of_a_row_that_is_not_finite():
