@@ -3,15 +3,20 @@
 // Dispatch is a stable counting sort of the pairs (t, k) by expert:
 //   row(p) = first(e) + #{pairs q < p of expert e},
 //   first(e) = sum over e' < e of the counts rounded up to row_align
-// and a copy of x's rows. Batches of up to kSmallPairs pairs take one launch,
-// whose workgroups (one per token) each count all ids; larger ones count by
-// blocks of pairs, scan, and place, and copy in a launch of its own. Counts are
-// integers: the order of the LDS atomics does not reach a result.
+// and a copy of x's rows: x's bytes read once, K times as many written, which
+// is what bounds large batches. For small ones it is latency: batches of up to
+// 64 pairs (a decode step) hold all ids in the lanes of every wave and need
+// no LDS and no barrier; up to kSmallPairs one launch still does it, every
+// workgroup counting all pairs. More pairs are counted by blocks in a launch
+// of its own, and each workgroup of the second places and moves the rows of
+// its few tokens from the blocks' counts. Counts are integers: the order of
+// the LDS atomics does not reach a result.
 //
 // Combine sums a token's rows in fp32, k ascending, one rounding per product
 // and sum. The gradient reads a token's dout once for its K rows.
 //
-// All of it is bounded by memory: rows in, rows out.
+// Both ways rows are moved by 16 bytes from their first element, whatever its
+// address (the hardware takes such accesses).
 #include "rowwise.h"
 
 #include "../../include/moe_w8a8.h"
@@ -20,8 +25,10 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kSmallPairs = 2048;
-constexpr int kBlockPairs = 1024;  // pairs per block of the counting pass
+constexpr int kWaves = kThreads / kWave;
+constexpr int kSmallPairs = 1024;
+constexpr int kParts = 16;        // workgroups of the second launch per block of the first
+constexpr int kScanBlocks = 32;   // more blocks are summed in a launch of their own
 
 // The pair's expert, -1 if it is dropped.
 __device__ __forceinline__ int expert_of(const DispatchArgs &a, int p) {
@@ -31,12 +38,20 @@ __device__ __forceinline__ int expert_of(const DispatchArgs &a, int p) {
 }
 __device__ __forceinline__ int round_up(int n, int align) { return (n + align - 1) & -align; }
 
-// s_first[e] = exclusive sum of s_count rounded up to align, e in [0, E].
-// Whole workgroup of NT threads, 1024 / NT experts each; s_wave: NT / kWave
-// words. Ends in a barrier.
-template <int NT>
+// The wave's lanes whose expert is the lane's; of no use where e < 0.
+__device__ __forceinline__ uint64_t same_expert(int e, int E) {
+    uint64_t same = __ballot(e >= 0);
+    for (int bit = 1; bit < E; bit <<= 1) {
+        const uint64_t set = __ballot(e >= 0 && (e & bit));
+        same &= (e & bit) ? set : ~set;
+    }
+    return same;
+}
+
+// s_first[e] = exclusive sum of s_count rounded up to align, e in [0, E], by a
+// whole workgroup; s_wave: kWaves words. Ends in a barrier.
 __device__ __forceinline__ void scan_counts(const int *s_count, int *s_first, int *s_wave, int E, int align) {
-    constexpr int kPer = 1024 / NT;
+    constexpr int kPer = 1024 / kThreads;
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
     int n[kPer], sum = 0;
 #pragma unroll
@@ -61,16 +76,14 @@ __device__ __forceinline__ void scan_counts(const int *s_count, int *s_first, in
         if (e <= E) s_first[e] = at;
         at += n[i];
     }
-    if (tid == NT - 1 && E == 1024) s_first[E] = at;
+    if (tid == kThreads - 1 && E == 1024) s_first[E] = at;
     __syncthreads();
 }
 
-// Bytes of a row, 16 at a time from its start wherever that is, and the bytes
-// after them one by one. By `n` threads, of which this is number i.
-__device__ __forceinline__ void copy_row(uint8_t *dst, const uint8_t *src, size_t bytes, int i, int n) {
-    const int chunks = static_cast<int>(bytes / 16), rest = static_cast<int>(bytes % 16);
-    for (int c = i; c < chunks; c += n) __builtin_memcpy(dst + c * 16, src + c * 16, 16);
-    if (i < rest) dst[chunks * 16 + i] = src[chunks * 16 + i];
+__device__ __forceinline__ uint4 load16(const uint8_t *p) {
+    uint4 v;
+    __builtin_memcpy(&v, p, 16);
+    return v;
 }
 __device__ __forceinline__ void zero_row(uint8_t *dst, size_t bytes, int i, int n) {
     const int chunks = static_cast<int>(bytes / 16), rest = static_cast<int>(bytes % 16);
@@ -78,22 +91,54 @@ __device__ __forceinline__ void zero_row(uint8_t *dst, size_t bytes, int i, int 
     for (int c = i; c < chunks; c += n) __builtin_memcpy(dst + c * 16, &zero, 16);
     if (i < rest) dst[chunks * 16 + i] = 0;
 }
-// Rows [from, to) that fill an expert's last row_align.
-__device__ __forceinline__ void fill_rows(const DispatchArgs &a, int from, int to) {
+// Row r fills an expert's last row_align: by n threads, of which this is number i.
+__device__ __forceinline__ void fill_row(const DispatchArgs &a, int r, int i, int n) {
+    if (i == 0) a.pair_of_row[r] = -1;
+    if (!a.rows) return;
     const size_t bytes = static_cast<size_t>(a.H) * a.elem;
-    for (int r = from; r < to; ++r) {
-        if (!a.rows) break;
-        zero_row(static_cast<uint8_t *>(a.rows) + r * bytes, bytes, threadIdx.x, blockDim.x);
-        for (int g = threadIdx.x; g < a.groups; g += blockDim.x) a.row_scale[static_cast<size_t>(r) * a.groups + g] = 0.0f;
-    }
+    zero_row(static_cast<uint8_t *>(a.rows) + r * bytes, bytes, i, n);
+    for (int g = i; g < a.groups; g += n) a.row_scale[static_cast<size_t>(r) * a.groups + g] = 0.0f;
 }
-// x's row t and its scales to `row`.
-__device__ __forceinline__ void move_row(const DispatchArgs &a, int t, int row) {
+// x's row t and its scales to the rows row(k) >= 0, k < K: 16 bytes at a time,
+// kAhead loads before the first store, and the bytes after them one by one.
+constexpr int kAhead = 4;
+struct Ahead { uint4 v[kAhead]; };
+// The token's chunks c0, c0 + n, ...; none of a row without a whole chunk.
+__device__ __forceinline__ Ahead load_token(const DispatchArgs &a, int t, int c0, int n) {
     const size_t bytes = static_cast<size_t>(a.H) * a.elem;
-    copy_row(static_cast<uint8_t *>(a.rows) + row * bytes, static_cast<const uint8_t *>(a.x) + t * bytes, bytes,
-             threadIdx.x, blockDim.x);
-    for (int g = threadIdx.x; g < a.groups; g += blockDim.x)
-        a.row_scale[static_cast<size_t>(row) * a.groups + g] = a.x_scale[static_cast<size_t>(t) * a.groups + g];
+    const int chunks = static_cast<int>(bytes / 16);
+    const uint8_t *x = static_cast<const uint8_t *>(a.x) + t * bytes;
+    Ahead f = {};
+    if (chunks > 0) {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) f.v[j] = load16(x + min(c0 + j * n, chunks - 1) * 16);
+    }
+    return f;
+}
+template <typename Row>
+__device__ __forceinline__ void move_token(const DispatchArgs &a, int t, Ahead f, Row row, int i, int n) {
+    const size_t bytes = static_cast<size_t>(a.H) * a.elem;
+    const int chunks = static_cast<int>(bytes / 16), rest = static_cast<int>(bytes % 16);
+    const uint8_t *x = static_cast<const uint8_t *>(a.x) + t * bytes;
+    uint8_t *rows = static_cast<uint8_t *>(a.rows);
+    for (int c0 = i; c0 < chunks; c0 += kAhead * n) {
+        if (c0 != i) f = load_token(a, t, c0, n);
+        for (int k = 0; k < a.K; ++k) {
+            const int r = row(k);
+            if (r < 0) continue;
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+                if (c0 + j * n < chunks) __builtin_memcpy(rows + r * bytes + (c0 + j * n) * 16, &f.v[j], 16);
+        }
+    }
+    const uint8_t tail = i < rest ? x[chunks * 16 + i] : 0;
+    for (int k = 0; k < a.K; ++k) {
+        const int r = row(k);
+        if (r < 0) continue;
+        if (i < rest) rows[r * bytes + chunks * 16 + i] = tail;
+        for (int g = i; g < a.groups; g += n)
+            a.row_scale[static_cast<size_t>(r) * a.groups + g] = a.x_scale[static_cast<size_t>(t) * a.groups + g];
+    }
 }
 
 // No token: nothing but the counts.
@@ -104,10 +149,85 @@ __global__ __launch_bounds__(kThreads) void dispatch_none_kernel(DispatchArgs a)
     }
 }
 
+// Up to 64 pairs: lane p of every wave holds pair p's expert. Workgroups [0,
+// T): a token's rows. The next `count_blocks`: the counts and offsets of kThreads
+// experts each, and what pair_of_row holds behind the last row. The others:
+// the rows that fill an expert's last row_align. In loops where it can be: a
+// short launch pays for fetching its code (unrolled, 6.1 us instead of 4.8).
+__global__ __launch_bounds__(kThreads) void dispatch_tiny_kernel(DispatchArgs a, int count_blocks) {
+    const int P = a.T * a.K, lane = threadIdx.x & (kWave - 1), b = blockIdx.x;
+    Ahead ahead = {};
+    if (a.rows && b < a.T) ahead = load_token(a, b, threadIdx.x, kThreads);  // on its way beside the ids
+    const int e = lane < P ? expert_of(a, lane) : -1;
+    const uint64_t kept = __ballot(e >= 0);
+    const int top = 1 << (31 - __builtin_clz(a.E));
+    // the pairs of experts below `value`, and of `value`: by bits, from the highest
+    auto compare = [&](int value, uint64_t &less, uint64_t &same) {
+        less = 0;
+        same = kept;
+#pragma unroll 1
+        for (int bit = top; bit > 0; bit >>= 1) {
+            const uint64_t set = __ballot(e & bit), want = value & bit ? ~0ull : 0ull;
+            less |= same & want & ~set;
+            same &= ~(set ^ want);
+        }
+    };
+    // an expert's rows are counted at its first pair
+    uint64_t less, same, firsts = kept;
+    int takes = e >= 0 ? 1 : 0;
+    if (a.align > 1) {
+        compare(max(e, 0), less, same);
+        takes = e >= 0 && (same & ((1ull << lane) - 1)) == 0 ? round_up(__popcll(same), a.align) : 0;
+        firsts = __ballot(takes > 0);
+    }
+    auto rows_of = [&](uint64_t pairs) {  // those that the experts of these pairs take
+        if (a.align == 1) return static_cast<int>(__popcll(pairs));
+        int n = 0;
+#pragma unroll 1
+        for (uint64_t left = firsts; left; left &= left - 1) {
+            const int q = __builtin_ctzll(left);
+            n += (pairs >> q) & 1 ? __builtin_amdgcn_readlane(takes, q) : 0;
+        }
+        return n;
+    };
+    if (b < a.T) {
+        compare(max(e, 0), less, same);
+        const int row = e < 0 ? -1 : rows_of(less) + static_cast<int>(__popcll(same & ((1ull << lane) - 1)));
+        if (threadIdx.x < kWave && lane / a.K == b && lane < P) {
+            a.row_of_pair[lane] = row;
+            if (row >= 0) a.pair_of_row[row] = lane;
+        }
+        if (a.rows)
+            move_token(a, b, ahead, [&](int k) { return __builtin_amdgcn_readlane(row, b * a.K + k); }, threadIdx.x, kThreads);
+        return;
+    }
+    const int total = rows_of(kept);
+    if (b < a.T + count_blocks) {
+        const int mine = (b - a.T) * kThreads + threadIdx.x;
+        compare(min(mine, a.E), less, same);
+        const int at = rows_of(less);
+        if (mine < a.E) a.counts[mine] = static_cast<int>(__popcll(same));
+        if (mine <= a.E) a.offset[mine] = at;
+        for (int64_t r = total + mine; r < a.R; r += count_blocks * kThreads) a.pair_of_row[r] = -1;
+        return;
+    }
+    compare(max(e, 0), less, same);
+    const int at = rows_of(less), used = static_cast<int>(__popcll(same));
+    const int first = b - a.T - count_blocks, step = gridDim.x - a.T - count_blocks;
+    for (uint64_t left = firsts; left; left &= left - 1) {
+        const int q = __builtin_ctzll(left);
+        const int from = __builtin_amdgcn_readlane(at, q), n = __builtin_amdgcn_readlane(takes, q);
+        for (int r = from + __builtin_amdgcn_readlane(used, q) + first; r < from + n; r += step)
+            fill_row(a, r, threadIdx.x, kThreads);
+    }
+}
+
 // One workgroup per token, each of which counts every pair.
 __global__ __launch_bounds__(kThreads) void dispatch_small_kernel(DispatchArgs a) {
-    __shared__ int s_count[1024], s_first[1025], s_wave[kThreads / kWave], s_mine[kMaxTopK], s_rank[kMaxTopK];
+    __shared__ int s_count[1024], s_first[1025], s_wave[kWaves], s_mine[kMaxTopK], s_rank[kMaxTopK], s_row[kMaxTopK];
     const int t = blockIdx.x, tid = threadIdx.x, P = a.T * a.K;
+    Ahead ahead = {};
+    if (a.rows) ahead = load_token(a, t, tid, kThreads);
     for (int e = tid; e < a.E; e += kThreads) s_count[e] = 0;
     if (tid < a.K) {
         s_mine[tid] = expert_of(a, t * a.K + tid);
@@ -122,11 +242,12 @@ __global__ __launch_bounds__(kThreads) void dispatch_small_kernel(DispatchArgs a
             if (s_mine[k] == e && p < t * a.K + k) atomicAdd(&s_rank[k], 1);
     }
     __syncthreads();
-    scan_counts<kThreads>(s_count, s_first, s_wave, a.E, a.align);
+    scan_counts(s_count, s_first, s_wave, a.E, a.align);
     if (tid < a.K) {
         const int e = s_mine[tid], p = t * a.K + tid, row = e < 0 ? -1 : s_first[e] + s_rank[tid];
         a.row_of_pair[p] = row;
         if (row >= 0) a.pair_of_row[row] = p;
+        s_row[tid] = row;
     }
     if (t == 0)
         for (int e = tid; e <= a.E; e += kThreads) {
@@ -136,103 +257,136 @@ __global__ __launch_bounds__(kThreads) void dispatch_small_kernel(DispatchArgs a
     for (int64_t r = s_first[a.E] + t * kThreads + tid; r < a.R; r += static_cast<int64_t>(a.T) * kThreads)
         a.pair_of_row[r] = -1;
     if (a.align > 1)
-        for (int e = t; e < a.E; e += a.T) {
-            const int from = s_first[e] + s_count[e], to = s_first[e + 1];
-            for (int r = from + tid; r < to; r += kThreads) a.pair_of_row[r] = -1;
-            fill_rows(a, from, to);
-        }
-    if (a.rows)
-        for (int k = 0; k < a.K; ++k)
-            if (s_mine[k] >= 0) move_row(a, t, s_first[s_mine[k]] + s_rank[k]);
+        for (int e = t; e < a.E; e += a.T)
+            for (int r = s_first[e] + s_count[e]; r < s_first[e + 1]; ++r) fill_row(a, r, tid, kThreads);
+    __syncthreads();
+    if (a.rows) move_token(a, t, ahead, [&](int k) { return s_row[k]; }, tid, kThreads);
 }
 
-// ws[b][e] = pairs of expert e in block b of kBlockPairs pairs
+// Larger batches: tokens of a workgroup of the second launch (at most 64
+// pairs), and of a block of kParts of them, which the first one counts.
+__host__ __device__ __forceinline__ int tokens_of(int K) { return kWave / K; }
+
+// ws[b][e] = pairs of expert e in block b
 __global__ __launch_bounds__(kThreads) void dispatch_count_kernel(DispatchArgs a) {
     __shared__ int s_count[1024];
-    const int P = a.T * a.K;
+    const int P = a.T * a.K, pairs = kParts * tokens_of(a.K) * a.K, from = blockIdx.x * pairs;
     for (int e = threadIdx.x; e < a.E; e += kThreads) s_count[e] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < kBlockPairs; i += kThreads) {
-        const int p = blockIdx.x * kBlockPairs + i;
-        const int e = p < P ? expert_of(a, p) : -1;
+    for (int p = from + threadIdx.x; p < min(from + pairs, P); p += kThreads) {
+        const int e = expert_of(a, p);
         if (e >= 0) atomicAdd(&s_count[e], 1);
     }
     __syncthreads();
     for (int e = threadIdx.x; e < a.E; e += kThreads) a.workspace[static_cast<size_t>(blockIdx.x) * a.E + e] = s_count[e];
 }
-// ws[b][e] = pairs of e in the blocks before b, and counts[e] = all of them
-__global__ __launch_bounds__(kWave) void dispatch_scan_kernel(DispatchArgs a, int blocks) {
-    const int e = blockIdx.x * kWave + threadIdx.x;
-    if (e >= a.E) return;
+// ws[b][e] = pairs of e in the blocks before b, and counts[e] = all of them.
+// A wave per quarter of the blocks, a lane per expert.
+__global__ __launch_bounds__(kThreads) void dispatch_scan_kernel(DispatchArgs a, int blocks) {
+    constexpr int kBatch = 8;
+    __shared__ int s_sum[kWaves][kWave];
+    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, e = blockIdx.x * kWave + lane;
+    const int per = (blocks + kWaves - 1) / kWaves, lo = min(wave * per, blocks), hi = min(lo + per, blocks);
+    int *ws = a.workspace + min(e, a.E - 1);
     int sum = 0;
-    for (int b = 0; b < blocks; ++b) {
-        int *at = a.workspace + static_cast<size_t>(b) * a.E + e;
-        const int n = *at;
-        *at = sum;
-        sum += n;
+#pragma unroll 8
+    for (int b = lo; b < hi; ++b) sum += ws[static_cast<size_t>(b) * a.E];
+    s_sum[wave][lane] = sum;
+    __syncthreads();
+    if (e >= a.E) return;
+    int at = 0;
+    for (int w = 0; w < wave; ++w) at += s_sum[w][lane];
+    if (wave == kWaves - 1) a.counts[e] = at + sum;
+    for (int b0 = lo; b0 < hi; b0 += kBatch) {
+        int n[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) n[i] = ws[static_cast<size_t>(min(b0 + i, hi - 1)) * a.E];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (b0 + i < hi) ws[static_cast<size_t>(b0 + i) * a.E] = at;
+            at += n[i];
+        }
     }
-    a.counts[e] = sum;
 }
-// The maps. One thread per pair of the block.
-__global__ __launch_bounds__(kBlockPairs) void dispatch_place_kernel(DispatchArgs a) {
-    constexpr int kWaves = kBlockPairs / kWave;
-    __shared__ int s_count[1024], s_first[1025], s_wave[kWaves];
-    __shared__ uint16_t s_here[kWaves][1024];  // pairs of an expert in each wave
+// The maps, and the rows. SCANNED: ws and counts are dispatch_scan_kernel's;
+// else ws is the counting launch's.
+template <bool SCANNED>
+__global__ __launch_bounds__(kThreads) void dispatch_place_kernel(DispatchArgs a, int blocks) {
+    __shared__ int s_count[1024], s_first[1025], s_before[1024], s_wave[kWaves], s_row[kWave];
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave, P = a.T * a.K;
-    const int p = blockIdx.x * kBlockPairs + tid;
-    for (int e = tid; e < a.E; e += kBlockPairs) s_count[e] = a.counts[e];
-    for (int i = tid; i < kWaves * a.E; i += kBlockPairs) s_here[i / a.E][i % a.E] = 0;
-    const int e = p < P ? expert_of(a, p) : -1;
-    __syncthreads();
-    scan_counts<kBlockPairs>(s_count, s_first, s_wave, a.E, a.align);
-    uint64_t same = __ballot(e >= 0);  // the wave's lanes with this expert
-    for (int bit = 1; bit < a.E; bit <<= 1) {
-        const uint64_t set = __ballot(e >= 0 && (e & bit));
-        same &= (e & bit) ? set : ~set;
+    const int tokens = tokens_of(a.K), t0 = blockIdx.x * tokens, p0 = t0 * a.K;
+    const int block = blockIdx.x / kParts, from = block * kParts * tokens * a.K;
+    // what comes before in the block: at most kParts * kWave pairs
+    constexpr int kPairs = kParts * kWave / kThreads;
+    int early[kPairs];
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+        const int p = from + i * kThreads + tid;
+        early[i] = p < p0 ? expert_of(a, p) : -1;
     }
-    const uint64_t before = same & ((1ull << lane) - 1);
-    if (e >= 0 && before == 0) s_here[wave][e] = static_cast<uint16_t>(__popcll(same));
+    for (int e = tid; e < a.E; e += kThreads) {
+        int all = 0, before = 0;
+        if (SCANNED) {
+            all = a.counts[e];
+            before = a.workspace[static_cast<size_t>(block) * a.E + e];
+        } else {
+            constexpr int kBatch = kScanBlocks / 2;
+            for (int b0 = 0; b0 < blocks; b0 += kBatch) {
+                int n[kBatch];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) n[i] = a.workspace[static_cast<size_t>(min(b0 + i, blocks - 1)) * a.E + e];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    all += b0 + i < blocks ? n[i] : 0;
+                    before += b0 + i < block ? n[i] : 0;
+                }
+            }
+        }
+        s_count[e] = all;
+        s_before[e] = before;
+    }
     __syncthreads();
-    if (p < P) {
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i)
+        if (early[i] >= 0) atomicAdd(&s_before[early[i]], 1);
+    scan_counts(s_count, s_first, s_wave, a.E, a.align);
+    if (wave == 0) {
+        const int p = p0 + lane;
+        const bool here = lane < tokens * a.K && p < P;
+        const int e = here ? expert_of(a, p) : -1;
+        const uint64_t same = same_expert(e, a.E);
         int row = -1;
         if (e >= 0) {
-            row = s_first[e] + a.workspace[static_cast<size_t>(blockIdx.x) * a.E + e] + __popcll(before);
-            for (int w = 0; w < wave; ++w) row += s_here[w][e];
+            row = s_first[e] + s_before[e] + __popcll(same & ((1ull << lane) - 1));
             a.pair_of_row[row] = p;
         }
-        a.row_of_pair[p] = row;
+        if (here) a.row_of_pair[p] = row;
+        s_row[lane] = row;
     }
     if (blockIdx.x == 0)
-        for (int i = tid; i <= a.E; i += kBlockPairs) a.offset[i] = s_first[i];
-    for (int64_t r = s_first[a.E] + static_cast<int64_t>(blockIdx.x) * kBlockPairs + tid; r < a.R;
-         r += static_cast<int64_t>(gridDim.x) * kBlockPairs)
+        for (int e = tid; e <= a.E; e += kThreads) {
+            if (e < a.E) a.counts[e] = s_count[e];
+            a.offset[e] = s_first[e];
+        }
+    for (int64_t r = s_first[a.E] + static_cast<int64_t>(blockIdx.x) * kThreads + tid; r < a.R;
+         r += static_cast<int64_t>(gridDim.x) * kThreads)
         a.pair_of_row[r] = -1;
     if (a.align > 1)
-        for (int i = blockIdx.x * kWaves + wave; i < a.E; i += gridDim.x * kWaves)
-            for (int r = s_first[i] + s_count[i] + lane; r < s_first[i + 1]; r += kWave) a.pair_of_row[r] = -1;
-}
-// Workgroups [0, T): the rows of a token; the others: the rows that fill an
-// expert's last row_align.
-__global__ __launch_bounds__(kThreads) void dispatch_move_kernel(DispatchArgs a) {
-    const int b = blockIdx.x;
-    if (b >= a.T) {
-        const int e = b - a.T;
-        fill_rows(a, a.offset[e] + a.counts[e], a.offset[e + 1]);
-        return;
-    }
-    for (int k = 0; k < a.K; ++k) {
-        const int row = a.row_of_pair[b * a.K + k];
-        if (row >= 0) move_row(a, b, row);
-    }
+        for (int e = blockIdx.x; e < a.E; e += gridDim.x)
+            for (int r = s_first[e] + s_count[e] + wave; r < s_first[e + 1]; r += kWaves) fill_row(a, r, lane, kWave);
+    __syncthreads();
+    if (a.rows)
+        for (int i = wave; i < tokens && t0 + i < a.T; i += kWaves)
+            move_token(a, t0 + i, load_token(a, t0 + i, lane, kWave), [&](int k) { return s_row[i * a.K + k]; }, lane, kWave);
 }
 
 // ------------------------------------------------------------------ back
 
 // Thread c of a token's takes elements [8 c, 8 c + 8), or, behind the row's
 // whole chunks, one element each.
-template <typename T, typename O>
+// kG rows are on their way at once.
+template <typename T, typename O, int kG>
 __global__ __launch_bounds__(kThreads) void combine_rows_kernel(RowsArgs a) {
-    constexpr int kAhead = 8;  // rows on their way at once
     const int t = blockIdx.x, c = blockIdx.y * kThreads + threadIdx.x;
     const int chunks = a.H / kVec, rest = a.H % kVec;
     if (c >= chunks + rest) return;
@@ -241,15 +395,15 @@ __global__ __launch_bounds__(kThreads) void combine_rows_kernel(RowsArgs a) {
     const O *addend = static_cast<const O *>(a.addend) + out_at;
     O *out = static_cast<O *>(a.out) + out_at;
     auto sum = [&](auto load, auto &acc) {
-        for (int k0 = 0; k0 < a.K && a.R > 0; k0 += kAhead) {
-            decltype(load(rows)) v[kAhead];
+        for (int k0 = 0; k0 < a.K && a.R > 0; k0 += kG) {
+            decltype(load(rows)) v[kG];
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) {  // dropped pairs, and k past the end: some row, not counted
+            for (int j = 0; j < kG; ++j) {  // dropped pairs, and k past the end: some row, not counted
                 const int r = a.row_of_pair[t * a.K + min(k0 + j, a.K - 1)];
                 v[j] = load(rows + static_cast<size_t>(static_cast<unsigned>(r) < static_cast<unsigned>(a.R) ? r : 0) * a.H);
             }
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
+            for (int j = 0; j < kG; ++j) {
                 if (k0 + j >= a.K) break;
                 const int r = a.row_of_pair[t * a.K + k0 + j];
                 if (static_cast<unsigned>(r) >= static_cast<unsigned>(a.R)) continue;
@@ -301,10 +455,10 @@ __device__ __forceinline__ float product(float d, float w) {
     return p;
 }
 
-// Workgroups [0, T): a token's K rows. The others: rows without a pair.
+// Workgroups [0, T): a token's K rows, kAhead of them on their way at once. The
+// others: rows without a pair.
 template <typename T, typename O>
 __global__ __launch_bounds__(kThreads) void combine_grad_kernel(RowsArgs a) {
-    constexpr int kWaves = kThreads / kWave;
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
     const int chunks = a.H / kVec, rest = a.H % kVec;
     if (static_cast<int>(blockIdx.x) >= a.T) {
@@ -322,54 +476,89 @@ __global__ __launch_bounds__(kThreads) void combine_grad_kernel(RowsArgs a) {
         }
         return;
     }
-    __shared__ float s_dot[kWaves][kMaxTopK];
+    __shared__ float s_dot[kWaves][kMaxTopK], s_scale[kMaxTopK];
+    __shared__ int s_row[kMaxTopK];
     const int t = blockIdx.x;
+    if (tid < a.K) {
+        s_row[tid] = own_row(a, t * a.K + tid);
+        s_scale[tid] = a.scales ? a.scales[t * a.K + tid] : 1.0f;
+    }
+    __syncthreads();
     const O *dout = static_cast<const O *>(a.dout) + static_cast<size_t>(t) * a.H;
     const T *rows = static_cast<const T *>(a.rows);
     T *drows = static_cast<T *>(a.drows);
-    for (int k = 0; k < a.K; ++k) {
-        const int r = own_row(a, t * a.K + k);
-        float dot = 0.0f;
-        if (r >= 0) {
-            const size_t at = static_cast<size_t>(r) * a.H;
-            const float w = a.scales ? a.scales[t * a.K + k] : 1.0f;
-            for (int c = tid; c < chunks; c += kThreads) {
-                float d[kVec], v[kVec];
-                load8(dout + c * kVec, d);
-                if (a.dscales) {
-                    load8(rows + at + c * kVec, v);
+    float dot[kMaxTopK] = {};
+    struct Eight { T v[kVec]; };
+    for (int c = tid; c < chunks; c += kThreads) {
+        float d[kVec];
+        load8(dout + c * kVec, d);
 #pragma unroll
-                    for (int i = 0; i < kVec; ++i) dot += v[i] * d[i];
+        for (int k0 = 0; k0 < kMaxTopK; k0 += kAhead) {
+            if (k0 >= a.K) break;
+            Eight v[kAhead];
+            if (a.dscales) {
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) {  // dropped pairs, and k past the end: some row, not counted
+                    const int r = max(s_row[min(k0 + j, a.K - 1)], 0);
+                    if (a.R > 0) __builtin_memcpy(&v[j], rows + static_cast<size_t>(r) * a.H + c * kVec, sizeof v[j]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const int k = k0 + j, r = __builtin_amdgcn_readfirstlane(k < a.K ? s_row[k] : -1);
+                if (r < 0) continue;
+                if (a.dscales) {
+#pragma unroll
+                    for (int i = 0; i < kVec; ++i) dot[k] += to_f32(v[j].v[i]) * d[i];
                 }
                 if (a.drows) {
+                    const float w = s_scale[k];
+                    float o[kVec];
 #pragma unroll
-                    for (int i = 0; i < kVec; ++i) d[i] = product(d[i], w);
-                    store8(drows + at + c * kVec, d);
+                    for (int i = 0; i < kVec; ++i) o[i] = product(d[i], w);
+                    store8(drows + static_cast<size_t>(r) * a.H + c * kVec, o);
                 }
             }
-            if (tid < rest) {
-                const int i = chunks * kVec + tid;
-                const float d = to_f32(dout[i]);
-                if (a.dscales) dot += to_f32(rows[at + i]) * d;
-                if (a.drows) from_f32(product(d, w), drows[at + i]);
-            }
         }
-        dot = last_lane_sum(dot);
-        if (lane == kWave - 1) s_dot[wave][k] = dot;
+    }
+    const int at = chunks * kVec + tid;
+    const float dt = tid < rest ? to_f32(dout[at]) : 0.0f;
+#pragma unroll
+    for (int k = 0; k < kMaxTopK; ++k) {
+        if (k >= a.K) break;
+        const int r = s_row[k];
+        if (r >= 0 && tid < rest) {
+            if (a.dscales) dot[k] += to_f32(rows[static_cast<size_t>(r) * a.H + at]) * dt;
+            if (a.drows) from_f32(product(dt, s_scale[k]), drows[static_cast<size_t>(r) * a.H + at]);
+        }
+        if (a.dscales) {
+            const float sum = last_lane_sum(dot[k]);
+            if (lane == kWave - 1) s_dot[wave][k] = sum;
+        }
     }
     __syncthreads();
     if (a.dscales && tid < a.K) {
-        float dot = 0.0f;
+        float sum = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) dot += s_dot[w][tid];
-        a.dscales[t * a.K + tid] = dot;
+        for (int w = 0; w < kWaves; ++w) sum += s_dot[w][tid];
+        a.dscales[t * a.K + tid] = sum;
     }
 }
 
 template <typename T, typename O>
 hipError_t combine_of(const RowsArgs &a, hipStream_t s) {
-    const int items = a.H / kVec + a.H % kVec;
-    hipLaunchKernelGGL((combine_rows_kernel<T, O>), dim3(a.T, (items + kThreads - 1) / kThreads), dim3(kThreads), 0, s, a);
+    const int items = a.H / kVec + a.H % kVec, passes = (a.K + 7) / 8;
+    const dim3 grid(a.T, (items + kThreads - 1) / kThreads), blk(kThreads);
+    switch ((a.K + passes - 1) / passes) {
+        case 1: hipLaunchKernelGGL((combine_rows_kernel<T, O, 1>), grid, blk, 0, s, a); break;
+        case 2: hipLaunchKernelGGL((combine_rows_kernel<T, O, 2>), grid, blk, 0, s, a); break;
+        case 3: hipLaunchKernelGGL((combine_rows_kernel<T, O, 3>), grid, blk, 0, s, a); break;
+        case 4: hipLaunchKernelGGL((combine_rows_kernel<T, O, 4>), grid, blk, 0, s, a); break;
+        case 5: hipLaunchKernelGGL((combine_rows_kernel<T, O, 5>), grid, blk, 0, s, a); break;
+        case 6: hipLaunchKernelGGL((combine_rows_kernel<T, O, 6>), grid, blk, 0, s, a); break;
+        case 7: hipLaunchKernelGGL((combine_rows_kernel<T, O, 7>), grid, blk, 0, s, a); break;
+        default: hipLaunchKernelGGL((combine_rows_kernel<T, O, 8>), grid, blk, 0, s, a); break;
+    }
     return hipGetLastError();
 }
 template <typename T, typename O>
@@ -382,26 +571,36 @@ hipError_t grad_of(const RowsArgs &a, hipStream_t s) {
 }  // namespace
 
 size_t dispatch_workspace(int T, int K, int E) {
-    const int64_t P = static_cast<int64_t>(T) * K;
-    return P <= kSmallPairs ? 0 : static_cast<size_t>((P + kBlockPairs - 1) / kBlockPairs) * E * sizeof(int32_t);
+    if (static_cast<int64_t>(T) * K <= kSmallPairs) return 0;
+    const int per = kParts * tokens_of(K);
+    return static_cast<size_t>((T + per - 1) / per) * E * sizeof(int32_t);
 }
 
 hipError_t launch_dispatch(const DispatchArgs &a, hipStream_t s) {
+    const dim3 blk(kThreads);
     if (a.T == 0) {
-        hipLaunchKernelGGL(dispatch_none_kernel, dim3(1), dim3(kThreads), 0, s, a);
+        hipLaunchKernelGGL(dispatch_none_kernel, dim3(1), blk, 0, s, a);
         return hipGetLastError();
     }
     const int P = a.T * a.K;
-    if (P <= kSmallPairs) {
-        hipLaunchKernelGGL(dispatch_small_kernel, dim3(a.T), dim3(kThreads), 0, s, a);
+    if (P <= kWave) {
+        const int count_blocks = (a.E + kThreads) / kThreads;  // of E + 1 offsets
+        hipLaunchKernelGGL(dispatch_tiny_kernel, dim3(a.T + count_blocks + (a.align > 1 ? 128 : 0)), blk, 0, s, a, count_blocks);
         return hipGetLastError();
     }
-    const int blocks = (P + kBlockPairs - 1) / kBlockPairs;
-    hipLaunchKernelGGL(dispatch_count_kernel, dim3(blocks), dim3(kThreads), 0, s, a);
-    hipLaunchKernelGGL(dispatch_scan_kernel, dim3((a.E + kWave - 1) / kWave), dim3(kWave), 0, s, a, blocks);
-    hipLaunchKernelGGL(dispatch_place_kernel, dim3(blocks), dim3(kBlockPairs), 0, s, a);
-    if (a.rows)
-        hipLaunchKernelGGL(dispatch_move_kernel, dim3(a.T + (a.align > 1 ? a.E : 0)), dim3(kThreads), 0, s, a);
+    if (P <= kSmallPairs) {
+        hipLaunchKernelGGL(dispatch_small_kernel, dim3(a.T), blk, 0, s, a);
+        return hipGetLastError();
+    }
+    const int tokens = tokens_of(a.K), blocks = (a.T + kParts * tokens - 1) / (kParts * tokens);
+    const dim3 grid((a.T + tokens - 1) / tokens);
+    hipLaunchKernelGGL(dispatch_count_kernel, dim3(blocks), blk, 0, s, a);
+    if (blocks <= kScanBlocks) {
+        hipLaunchKernelGGL(dispatch_place_kernel<false>, grid, blk, 0, s, a, blocks);
+    } else {
+        hipLaunchKernelGGL(dispatch_scan_kernel, dim3((a.E + kWave - 1) / kWave), blk, 0, s, a, blocks);
+        hipLaunchKernelGGL(dispatch_place_kernel<true>, grid, blk, 0, s, a, blocks);
+    }
     return hipGetLastError();
 }
 
