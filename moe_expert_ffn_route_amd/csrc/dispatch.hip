@@ -88,7 +88,7 @@ __device__ __forceinline__ uint4 load16(const uint8_t *p) {
 __device__ __forceinline__ void zero_row(uint8_t *dst, size_t bytes, int i, int n) {
     const int chunks = static_cast<int>(bytes / 16), rest = static_cast<int>(bytes % 16);
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    for (int c = i; c < chunks; c += n) __builtin_memcpy(dst + c * 16, &zero, 16);
+    for (int c = i; c < chunks; c += n) stream(dst + c * 16, zero);
     if (i < rest) dst[chunks * 16 + i] = 0;
 }
 // Row r fills an expert's last row_align: by n threads, of which this is number i.
@@ -128,7 +128,7 @@ __device__ __forceinline__ void move_token(const DispatchArgs &a, int t, Ahead f
             if (r < 0) continue;
 #pragma unroll
             for (int j = 0; j < kAhead; ++j)
-                if (c0 + j * n < chunks) __builtin_memcpy(rows + r * bytes + (c0 + j * n) * 16, &f.v[j], 16);
+                if (c0 + j * n < chunks) stream(rows + r * bytes + (c0 + j * n) * 16, f.v[j]);
         }
     }
     const uint8_t tail = i < rest ? x[chunks * 16 + i] : 0;
@@ -273,12 +273,18 @@ __global__ __launch_bounds__(kThreads) void dispatch_count_kernel(DispatchArgs a
     const int P = a.T * a.K, pairs = kParts * tokens_of(a.K) * a.K, from = blockIdx.x * pairs;
     for (int e = threadIdx.x; e < a.E; e += kThreads) s_count[e] = 0;
     __syncthreads();
-    for (int p = from + threadIdx.x; p < min(from + pairs, P); p += kThreads) {
-        const int e = expert_of(a, p);
-        if (e >= 0) atomicAdd(&s_count[e], 1);
+    constexpr int kPairs = kParts * kWave / kThreads;  // at most, of a thread: loaded together
+    int e[kPairs];
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+        const int p = i * kThreads + threadIdx.x;
+        e[i] = p < pairs && from + p < P ? expert_of(a, from + p) : -1;
     }
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i)
+        if (e[i] >= 0) atomicAdd(&s_count[e[i]], 1);
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += kThreads) a.workspace[static_cast<size_t>(blockIdx.x) * a.E + e] = s_count[e];
+    for (int i = threadIdx.x; i < a.E; i += kThreads) a.workspace[static_cast<size_t>(blockIdx.x) * a.E + i] = s_count[i];
 }
 // ws[b][e] = pairs of e in the blocks before b, and counts[e] = all of them.
 // A wave per quarter of the blocks, a lane per expert.
@@ -455,6 +461,7 @@ __device__ __forceinline__ float product(float d, float w) {
     return p;
 }
 
+constexpr int kLook = 16;
 // Workgroups [0, T): a token's K rows, kAhead of them on their way at once. The
 // others: rows without a pair.
 template <typename T, typename O>
@@ -462,17 +469,20 @@ __global__ __launch_bounds__(kThreads) void combine_grad_kernel(RowsArgs a) {
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
     const int chunks = a.H / kVec, rest = a.H % kVec;
     if (static_cast<int>(blockIdx.x) >= a.T) {
+        // every wave looks at kLook rows and takes each kWaves-th of those without a pair
         const size_t bytes = static_cast<size_t>(a.H) * sizeof(T);
-        const int waves = (gridDim.x - a.T) * kWaves, first = (blockIdx.x - a.T) * kWaves + wave;
-        for (int64_t r0 = static_cast<int64_t>(first) * kWave; r0 < a.R; r0 += static_cast<int64_t>(waves) * kWave) {
+        for (int64_t r0 = static_cast<int64_t>(blockIdx.x - a.T) * kLook; r0 < a.R;
+             r0 += static_cast<int64_t>(gridDim.x - a.T) * kLook) {
             const int r = static_cast<int>(r0) + lane;
             bool none = false;
-            if (r < a.R) {
+            if (lane < kLook && r < a.R) {
                 const int p = a.pair_of_row[r];
                 none = static_cast<unsigned>(p) >= static_cast<unsigned>(a.T * a.K) || a.row_of_pair[p] != r;
             }
-            for (uint64_t left = __ballot(none); left; left &= left - 1)
-                zero_row(static_cast<uint8_t *>(a.drows) + (r0 + __builtin_ctzll(left)) * bytes, bytes, lane, kWave);
+            int i = 0;
+            for (uint64_t left = __ballot(none); left; left &= left - 1, ++i)
+                if (i % kWaves == wave)
+                    zero_row(static_cast<uint8_t *>(a.drows) + (r0 + __builtin_ctzll(left)) * bytes, bytes, lane, kWave);
         }
         return;
     }
@@ -563,8 +573,8 @@ hipError_t combine_of(const RowsArgs &a, hipStream_t s) {
 }
 template <typename T, typename O>
 hipError_t grad_of(const RowsArgs &a, hipStream_t s) {
-    const int others = a.drows ? (a.R + kThreads - 1) / kThreads : 0;
-    hipLaunchKernelGGL((combine_grad_kernel<T, O>), dim3(a.T + (others < 2048 ? others : 2048)), dim3(kThreads), 0, s, a);
+    const int others = a.drows ? (a.R + kLook - 1) / kLook : 0;
+    hipLaunchKernelGGL((combine_grad_kernel<T, O>), dim3(a.T + (others < 8192 ? others : 8192)), dim3(kThreads), 0, s, a);
     return hipGetLastError();
 }
 

@@ -23,7 +23,7 @@ __device__ __forceinline__ void store8(T *p, const float (&v)[kVec]) {
     T raw[kVec];
 #pragma unroll
     for (int e = 0; e < kVec; ++e) from_f32(v[e], raw[e]);
-    __builtin_memcpy(p, raw, sizeof raw);
+    stream(p, raw);
 }
 // Sum and maximum over the wave: DPP shifts within rows of 16 lanes, then the
 // row ends to the following rows; lane 63 holds the result.
@@ -134,7 +134,7 @@ __device__ __forceinline__ void write_codes(const float (&p)[CH][kVec], float pt
             if (c >= chunks) continue;
             const float am = pm * rstd;
             const uint64_t code = quant8(p[j], inv_of(pm, am), fp8);
-            __builtin_memcpy(q + c * kVec, &code, sizeof code);
+            stream(q + c * kVec, code);
             if ((tr & (gl - 1)) == 0) scale[c * kVec / group] = fmaxf(am, eps) * top_inv;
         }
         return;
@@ -145,7 +145,8 @@ __device__ __forceinline__ void write_codes(const float (&p)[CH][kVec], float pt
         const int c = tr + j * tpr;
         if (c >= chunks) break;
         const uint64_t code = quant8(p[j], inv, fp8);
-        __builtin_memcpy(q + c * kVec, &code, sizeof code);
+        stream(q + c * kVec, code);
+
     }
     if (TAIL && tail)
         q[it] = static_cast<uint8_t>(fp8 ? quant4<true>(pt, 0.0f, 0.0f, 0.0f, inv) : quant4<false>(pt, 0.0f, 0.0f, 0.0f, inv));
