@@ -128,6 +128,13 @@ bool all_aligned(const void *const (&p)[N], size_t to) {
         if (!aligned(q, to)) return false;
     return true;
 }
+// What a call writes is stored as a stream (ops.h).
+template <int O>
+bool is_much(const Range (&out)[O]) {
+    size_t bytes = 0;
+    for (const Range &o : out) bytes += o.p ? o.bytes : 0;
+    return bytes >= kStreamBytes;
+}
 // No output meets an input or another output.
 template <int O, int I>
 bool apart(const Range (&out)[O], const Range (&in)[I]) {
@@ -182,6 +189,7 @@ extern "C" moe_status_t moe_w8a8_linear_w8(const moe_w8a8_linear_w8_dims_t *d, c
     a.x_scale = x_scale;
     a.bias = bias;
     a.out = out;
+    a.streamed = is_much(to);
     return of_launch(launch_linear_w8(a, static_cast<hipStream_t>(stream)));
 }
 
@@ -208,6 +216,7 @@ extern "C" moe_status_t moe_w8a8_quant(const moe_w8a8_quant_dims_t *d, const voi
     a.quant = d->quant;
     a.group = d->quant_group;
     a.amax_eps = d->amax_eps;
+    a.streamed = is_much(out);
     return of_launch(launch_quant(a, static_cast<hipStream_t>(stream)));
 }
 
@@ -269,6 +278,7 @@ extern "C" moe_status_t moe_w8a8_join_norm(const moe_w8a8_join_norm_dims_t *d, c
     a.post_eps = d->post_eps;
     a.rms_eps = d->rms_eps;
     a.amax_eps = d->amax_eps;
+    a.streamed = is_much(out);
     return of_launch(launch_join_norm(a, static_cast<hipStream_t>(stream)));
 }
 
@@ -338,6 +348,7 @@ extern "C" moe_status_t moe_w8a8_dispatch(const moe_w8a8_dispatch_dims_t *d, con
     a.groups = rows ? d->scale_groups : 0;
     a.align = d->row_align;
     a.R = static_cast<int64_t>(R);
+    a.streamed = is_much(out);
     return of_launch(launch_dispatch(a, static_cast<hipStream_t>(stream)));
 }
 
@@ -362,6 +373,7 @@ extern "C" moe_status_t moe_w8a8_combine(const moe_w8a8_combine_dims_t *d, const
     a.scales = expert_scales;
     a.addend = addend;
     a.out = out;
+    a.streamed = is_much(to);
     return of_launch(launch_combine_rows(a, static_cast<hipStream_t>(stream)));
 }
 
@@ -390,5 +402,6 @@ extern "C" moe_status_t moe_w8a8_combine_grad(const moe_w8a8_combine_dims_t *d, 
     a.scales = expert_scales;
     a.drows = drows;
     a.dscales = dscales;
+    a.streamed = is_much(to);
     return of_launch(launch_combine_grad(a, static_cast<hipStream_t>(stream)));
 }

@@ -85,10 +85,10 @@ __device__ __forceinline__ uint4 load16(const uint8_t *p) {
     __builtin_memcpy(&v, p, 16);
     return v;
 }
-__device__ __forceinline__ void zero_row(uint8_t *dst, size_t bytes, int i, int n) {
+__device__ __forceinline__ void zero_row(uint8_t *dst, size_t bytes, int i, int n, bool streamed) {
     const int chunks = static_cast<int>(bytes / 16), rest = static_cast<int>(bytes % 16);
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    for (int c = i; c < chunks; c += n) stream(dst + c * 16, zero);
+    for (int c = i; c < chunks; c += n) store_out(dst + c * 16, zero, streamed);
     if (i < rest) dst[chunks * 16 + i] = 0;
 }
 // Row r fills an expert's last row_align: by n threads, of which this is number i.
@@ -96,7 +96,7 @@ __device__ __forceinline__ void fill_row(const DispatchArgs &a, int r, int i, in
     if (i == 0) a.pair_of_row[r] = -1;
     if (!a.rows) return;
     const size_t bytes = static_cast<size_t>(a.H) * a.elem;
-    zero_row(static_cast<uint8_t *>(a.rows) + r * bytes, bytes, i, n);
+    zero_row(static_cast<uint8_t *>(a.rows) + r * bytes, bytes, i, n, a.streamed);
     for (int g = i; g < a.groups; g += n) a.row_scale[static_cast<size_t>(r) * a.groups + g] = 0.0f;
 }
 // x's row t and its scales to the rows row(k) >= 0, k < K: 16 bytes at a time,
@@ -128,7 +128,7 @@ __device__ __forceinline__ void move_token(const DispatchArgs &a, int t, Ahead f
             if (r < 0) continue;
 #pragma unroll
             for (int j = 0; j < kAhead; ++j)
-                if (c0 + j * n < chunks) stream(rows + r * bytes + (c0 + j * n) * 16, f.v[j]);
+                if (c0 + j * n < chunks) store_out(rows + r * bytes + (c0 + j * n) * 16, f.v[j], a.streamed);
         }
     }
     const uint8_t tail = i < rest ? x[chunks * 16 + i] : 0;
@@ -435,7 +435,7 @@ __global__ __launch_bounds__(kThreads) void combine_rows_kernel(RowsArgs a) {
 #pragma unroll
             for (int i = 0; i < kVec; ++i) acc[i] = acc[i] + add[i];
         }
-        store8(out + c * kVec, acc);
+        store8(out + c * kVec, acc, a.streamed);
     } else {
         const int i = chunks * kVec + c - chunks;
         float acc = 0.0f;
@@ -482,7 +482,7 @@ __global__ __launch_bounds__(kThreads) void combine_grad_kernel(RowsArgs a) {
             int i = 0;
             for (uint64_t left = __ballot(none); left; left &= left - 1, ++i)
                 if (i % kWaves == wave)
-                    zero_row(static_cast<uint8_t *>(a.drows) + (r0 + __builtin_ctzll(left)) * bytes, bytes, lane, kWave);
+                    zero_row(static_cast<uint8_t *>(a.drows) + (r0 + __builtin_ctzll(left)) * bytes, bytes, lane, kWave, a.streamed);
         }
         return;
     }
@@ -526,7 +526,7 @@ __global__ __launch_bounds__(kThreads) void combine_grad_kernel(RowsArgs a) {
                     float o[kVec];
 #pragma unroll
                     for (int i = 0; i < kVec; ++i) o[i] = product(d[i], w);
-                    store8(drows + static_cast<size_t>(r) * a.H + c * kVec, o);
+                    store8(drows + static_cast<size_t>(r) * a.H + c * kVec, o, a.streamed);
                 }
             }
         }

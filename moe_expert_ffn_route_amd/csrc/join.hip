@@ -83,7 +83,7 @@ __global__ __launch_bounds__((kMost<CH, ONE>)) void quant_kernel(QuantArgs a) {
     }
     write_codes<CH, TAIL>(p, pt, mx, 1.0f, a.amax_eps, a.quant == MOE_QUANT_E4M3, a.group, a.H, tr, tpr, tail, it,
                           static_cast<uint8_t *>(a.q) + base,
-                          a.q_scale + static_cast<size_t>(row) * (a.group ? a.H / a.group : 1));
+                          a.q_scale + static_cast<size_t>(row) * (a.group ? a.H / a.group : 1), a.streamed);
 }
 
 template <typename T, typename W, int CH, bool TAIL, bool ONE>
@@ -185,7 +185,7 @@ __global__ __launch_bounds__((kMost<CH, ONE>)) void join_norm_kernel(JoinNormArg
         T *out = static_cast<T *>(a.residual_out) + base;
 #pragma unroll
         for (int j = 0; j < CH; ++j)
-            if (tr + j * tpr < chunks) store8(out + at(j), p[j]);
+            if (tr + j * tpr < chunks) store8(out + at(j), p[j], a.streamed);
         if (tail) from_f32(pt, out[it]);
     }
     if (!a.y && !a.q) return;  // uniform
@@ -236,14 +236,14 @@ __global__ __launch_bounds__((kMost<CH, ONE>)) void join_norm_kernel(JoinNormArg
             float v[kVec];
 #pragma unroll
             for (int e = 0; e < kVec; ++e) v[e] = p[j][e] * rstd;
-            store8(y + at(j), v);
+            store8(y + at(j), v, a.streamed);
         }
         if (tail) from_f32(pt * rstd, y[it]);
     }
     if (!a.q) return;
     write_codes<CH, TAIL>(p, pt, mx, rstd, a.amax_eps, a.quant == MOE_QUANT_E4M3, a.group, a.H, tr, tpr, tail, it,
                           static_cast<uint8_t *>(a.q) + base,
-                          a.q_scale + static_cast<size_t>(row) * (a.group ? a.H / a.group : 1));
+                          a.q_scale + static_cast<size_t>(row) * (a.group ? a.H / a.group : 1), a.streamed);
 }
 
 // f(CH, ONE) as constants, and the grid and workgroup that go with them. Short

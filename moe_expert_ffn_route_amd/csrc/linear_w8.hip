@@ -328,7 +328,7 @@ __device__ __forceinline__ void write_sums(const LinearW8Args &a, const v4i (&ac
             const v4i v = *(__attribute__((address_space(3))) volatile v4i *)(place + row * kRow + n * E);
             char *p = static_cast<char *>(a.out) + (static_cast<size_t>(t) * units + n0 + n) * E;
             const int left = units - n0 - n;
-            if (left >= kPer) stream(p, v);
+            if (left >= kPer) store_out(p, v, a.streamed);
             else if (left > 0) {
                 char b[16];
                 __builtin_memcpy(b, &v, 16);

@@ -43,7 +43,7 @@ struct LinearW8Args {
     const float *scale;
     const float *bias;
     void *out;
-    int T, N, K, out_dtype, gated;
+    int T, N, K, out_dtype, gated, streamed;
     int n_tiles, k_tiles;    // 16 rows, 128 k
 };
 struct QuantArgs {
@@ -51,7 +51,7 @@ struct QuantArgs {
     const float *smooth;
     void *q;
     float *q_scale;
-    int T, H, dtype, quant;
+    int T, H, dtype, quant, streamed;
     int group;  // elements per scale, 0 = one per row
     float amax_eps;
 };
@@ -60,7 +60,7 @@ struct JoinNormArgs {
     const float *share_scale;
     void *residual_out, *y, *q;
     float *q_scale;
-    int T, H, dtype, weight_dtype, quant, group, post_norm;
+    int T, H, dtype, weight_dtype, quant, group, post_norm, streamed;
     size_t gate_stride;  // elements between the tokens' rows of gate
     float residual_scale, branch_scale, post_eps, rms_eps, amax_eps;
 };
@@ -73,7 +73,7 @@ struct DispatchArgs {
     float *row_scale;
     int32_t *counts, *offset, *row_of_pair, *pair_of_row;
     int32_t *workspace;
-    int T, K, E, H, elem, groups, align;  // elem: bytes of an element
+    int T, K, E, H, elem, groups, align, streamed;  // elem: bytes of an element
     int64_t R;                            // rows of `rows` and pair_of_row
 };
 struct RowsArgs {  // sorted rows back to tokens, and the gradient
@@ -82,7 +82,7 @@ struct RowsArgs {  // sorted rows back to tokens, and the gradient
     const float *scales;
     void *out, *drows;
     float *dscales;
-    int T, K, H, R, dtype, out_dtype;
+    int T, K, H, R, dtype, out_dtype, streamed;
 };
 hipError_t launch_norm_quant(const NormArgs &a, hipStream_t s);
 size_t gate_workspace(int T, int E, int H);
@@ -100,18 +100,25 @@ hipError_t launch_dispatch(const DispatchArgs &a, hipStream_t s);
 hipError_t launch_combine_rows(const RowsArgs &a, hipStream_t s);
 hipError_t launch_combine_grad(const RowsArgs &a, hipStream_t s);
 
-// Outputs go to memory as a stream (non-temporal): they do not push what is
-// still being read out of L2, and the next launch could not find them there
-// anyway, since each XCD's L2 is written back at a launch's end. 16-byte stores
-// to any address; in us, plain / streamed: int8 product T 4096, N 8192, K 4096
-// 134 / 123, joining norm T 4001, H 5003 56 / 44, quantiser T 8192, H 4096 19.9 /
-// 16.1, dispatch T 4096, K 8, H 4096 66 / 53, combine T 4096 68.0 / 64.9; T 8
-// the same.
+// Calls that write much store it as a stream (non-temporal): it does not push
+// out of L2 what is still being read. In us, plain / streamed: int8 product T
+// 4096, N 8192, K 4096 134 / 123, joining norm T 4001, H 5003 56 / 44, quantiser T
+// 8192, H 4096 19.9 / 16.1, dispatch T 4096, K 8, H 4096 66 / 53, combine T 4096
+// 68.0 / 64.9. What the next launch could still find in the cache behind the
+// L2s is stored plainly: joining norm, product (N 8192) and quantiser in a row, T
+// 512 (4 to 8 MB each) 34.6 / 38.1, T 2048 (16 to 32 MB) 96 / 91, T 8192 329 / 328.
+constexpr size_t kStreamBytes = 16u << 20;
+// 8 or 16-byte stores to any address.
 template <typename V>
-__device__ __forceinline__ void stream(void *p, const V &v) {
+__device__ __forceinline__ void store_out(void *p, const V &v, bool streamed) {
     static_assert(sizeof(V) == 8 || sizeof(V) % 16 == 0, "whole stores");
     typedef int v4 __attribute__((ext_vector_type(4), aligned(1)));
     typedef int v2 __attribute__((ext_vector_type(2), aligned(1)));
+    if (!streamed) {
+        __builtin_memcpy(p, &v, sizeof(V));
+        return;
+    }
+    asm volatile("");  // with nothing before and behind it, the compiler makes one plain store of both
     if constexpr (sizeof(V) == 8) {
         v2 w;
         __builtin_memcpy(&w, &v, 8);
@@ -122,6 +129,7 @@ __device__ __forceinline__ void stream(void *p, const V &v) {
 #pragma unroll
         for (unsigned i = 0; i < sizeof(V) / 16; ++i) __builtin_nontemporal_store(w[i], static_cast<v4 *>(p) + i);
     }
+    asm volatile("");
 }
 
 // One element of a MOE_DTYPE_* array to fp32, and back with one rounding to

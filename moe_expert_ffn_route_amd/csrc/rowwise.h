@@ -19,11 +19,11 @@ __device__ __forceinline__ void load8(const T *p, float (&v)[kVec]) {
     for (int e = 0; e < kVec; ++e) v[e] = to_f32(raw[e]);
 }
 template <typename T>
-__device__ __forceinline__ void store8(T *p, const float (&v)[kVec]) {
+__device__ __forceinline__ void store8(T *p, const float (&v)[kVec], bool streamed = false) {
     T raw[kVec];
 #pragma unroll
     for (int e = 0; e < kVec; ++e) from_f32(v[e], raw[e]);
-    stream(p, raw);
+    store_out(p, raw, streamed);
 }
 // Sum and maximum over the wave: DPP shifts within rows of 16 lanes, then the
 // row ends to the following rows; lane 63 holds the result.
@@ -117,7 +117,7 @@ constexpr int kRows = TPR == kWave ? 4 : 1;
 template <int CH, bool TAIL>
 __device__ __forceinline__ void write_codes(const float (&p)[CH][kVec], float pt, float mx, float rstd, float eps,
                                             bool fp8, int group, int H, int tr, int tpr, bool tail, int it, uint8_t *q,
-                                            float *scale) {
+                                            float *scale, bool streamed = false) {
     const int chunks = H / kVec;
     const float top_inv = fp8 ? 1.0f / kQMax<true> : 1.0f / kQMax<false>;
     auto inv_of = [&](float pm, float am) { return am >= eps ? 1.0f / pm : rstd * (1.0f / eps); };
@@ -134,7 +134,7 @@ __device__ __forceinline__ void write_codes(const float (&p)[CH][kVec], float pt
             if (c >= chunks) continue;
             const float am = pm * rstd;
             const uint64_t code = quant8(p[j], inv_of(pm, am), fp8);
-            stream(q + c * kVec, code);
+            store_out(q + c * kVec, code, streamed);
             if ((tr & (gl - 1)) == 0) scale[c * kVec / group] = fmaxf(am, eps) * top_inv;
         }
         return;
@@ -145,7 +145,7 @@ __device__ __forceinline__ void write_codes(const float (&p)[CH][kVec], float pt
         const int c = tr + j * tpr;
         if (c >= chunks) break;
         const uint64_t code = quant8(p[j], inv, fp8);
-        stream(q + c * kVec, code);
+        store_out(q + c * kVec, code, streamed);
 
     }
     if (TAIL && tail)
