@@ -19,6 +19,8 @@
 // address (the hardware takes such accesses).
 #include "rowwise.h"
 
+#include <type_traits>
+
 #include "../../include/moe_w8a8.h"
 
 namespace moe {
@@ -26,9 +28,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
-constexpr int kSmallPairs = 1024;
+constexpr int kSmallPairs = 4096;  // K 8, H 4096, int8: T 256 9.1 us in one launch, 13.7 in two; T 512 10.5 / 15.3
 constexpr int kParts = 16;        // workgroups of the second launch per block of the first
-constexpr int kScanBlocks = 32;   // more blocks are summed in a launch of their own
+constexpr int kScanBlocks = 64;   // more blocks are summed in a launch of their own
 
 // The pair's expert, -1 if it is dropped.
 __device__ __forceinline__ int expert_of(const DispatchArgs &a, int p) {
@@ -98,6 +100,15 @@ __device__ __forceinline__ void fill_row(const DispatchArgs &a, int r, int i, in
     const size_t bytes = static_cast<size_t>(a.H) * a.elem;
     zero_row(static_cast<uint8_t *>(a.rows) + r * bytes, bytes, i, n, a.streamed);
     for (int g = i; g < a.groups; g += n) a.row_scale[static_cast<size_t>(r) * a.groups + g] = 0.0f;
+}
+// The rows that fill the experts' last row_align, by workgroup f of F: where
+// there are more workgroups than experts, several an expert.
+__device__ __forceinline__ void fill_share(const DispatchArgs &a, const int *s_count, const int *s_first, int f, int F) {
+    const int each = F > a.E ? F / a.E : 1, experts = F / each, wave = threadIdx.x / kWave;
+    if (f >= experts * each) return;
+    for (int e = f / each; e < a.E; e += experts)
+        for (int r = s_first[e] + s_count[e] + f % each * kWaves + wave; r < s_first[e + 1]; r += each * kWaves)
+            fill_row(a, r, threadIdx.x & (kWave - 1), kWave);
 }
 // x's row t and its scales to the rows row(k) >= 0, k < K: 16 bytes at a time,
 // kAhead loads before the first store, and the bytes after them one by one.
@@ -222,43 +233,59 @@ __global__ __launch_bounds__(kThreads) void dispatch_tiny_kernel(DispatchArgs a,
     }
 }
 
-// One workgroup per token, each of which counts every pair.
+// One workgroup per token, each of which counts every pair, and apart those of
+// the tokens before its own; the workgroups behind them share the rows that
+// fill an expert's last row_align.
+template <int kPairs>  // of a thread, at most
 __global__ __launch_bounds__(kThreads) void dispatch_small_kernel(DispatchArgs a) {
-    __shared__ int s_count[1024], s_first[1025], s_wave[kWaves], s_mine[kMaxTopK], s_rank[kMaxTopK], s_row[kMaxTopK];
-    const int t = blockIdx.x, tid = threadIdx.x, P = a.T * a.K;
+    __shared__ int s_count[1024], s_before[1024], s_first[1025], s_wave[kWaves], s_mine[kMaxTopK], s_row[kMaxTopK];
+    const int t = blockIdx.x, tid = threadIdx.x, P = a.T * a.K, p0 = t * a.K;
     Ahead ahead = {};
-    if (a.rows) ahead = load_token(a, t, tid, kThreads);
-    for (int e = tid; e < a.E; e += kThreads) s_count[e] = 0;
-    if (tid < a.K) {
-        s_mine[tid] = expert_of(a, t * a.K + tid);
-        s_rank[tid] = 0;
+    if (a.rows && t < a.T) ahead = load_token(a, t, tid, kThreads);
+    int e[kPairs];  // loaded together
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+        const int p = i * kThreads + tid;
+        e[i] = p < P ? expert_of(a, p) : -1;
+    }
+    for (int i = tid; i < a.E; i += kThreads) {
+        s_count[i] = 0;
+        s_before[i] = 0;
     }
     __syncthreads();
-    for (int p = tid; p < P; p += kThreads) {
-        const int e = expert_of(a, p);
-        if (e < 0) continue;
-        atomicAdd(&s_count[e], 1);
-        for (int k = 0; k < a.K; ++k)
-            if (s_mine[k] == e && p < t * a.K + k) atomicAdd(&s_rank[k], 1);
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+        const int p = i * kThreads + tid;
+        if (e[i] >= 0) {
+            atomicAdd(&s_count[e[i]], 1);
+            if (p < p0) atomicAdd(&s_before[e[i]], 1);
+        }
+        if (p >= p0 && p < p0 + a.K) s_mine[p - p0] = e[i];
     }
     __syncthreads();
     scan_counts(s_count, s_first, s_wave, a.E, a.align);
+    if (t >= a.T) {
+        fill_share(a, s_count, s_first, t - a.T, gridDim.x - a.T);
+        return;
+    }
     if (tid < a.K) {
-        const int e = s_mine[tid], p = t * a.K + tid, row = e < 0 ? -1 : s_first[e] + s_rank[tid];
-        a.row_of_pair[p] = row;
-        if (row >= 0) a.pair_of_row[row] = p;
+        const int of = s_mine[tid];
+        int row = -1;
+        if (of >= 0) {
+            row = s_first[of] + s_before[of];
+            for (int k = 0; k < tid; ++k) row += s_mine[k] == of;
+            a.pair_of_row[row] = p0 + tid;
+        }
+        a.row_of_pair[p0 + tid] = row;
         s_row[tid] = row;
     }
     if (t == 0)
-        for (int e = tid; e <= a.E; e += kThreads) {
-            if (e < a.E) a.counts[e] = s_count[e];
-            a.offset[e] = s_first[e];
+        for (int i = tid; i <= a.E; i += kThreads) {
+            if (i < a.E) a.counts[i] = s_count[i];
+            a.offset[i] = s_first[i];
         }
     for (int64_t r = s_first[a.E] + t * kThreads + tid; r < a.R; r += static_cast<int64_t>(a.T) * kThreads)
         a.pair_of_row[r] = -1;
-    if (a.align > 1)
-        for (int e = t; e < a.E; e += a.T)
-            for (int r = s_first[e] + s_count[e]; r < s_first[e + 1]; ++r) fill_row(a, r, tid, kThreads);
     __syncthreads();
     if (a.rows) move_token(a, t, ahead, [&](int k) { return s_row[k]; }, tid, kThreads);
 }
@@ -336,7 +363,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_place_kernel(DispatchArgs a
             all = a.counts[e];
             before = a.workspace[static_cast<size_t>(block) * a.E + e];
         } else {
-            constexpr int kBatch = kScanBlocks / 2;
+            constexpr int kBatch = 16;
             for (int b0 = 0; b0 < blocks; b0 += kBatch) {
                 int n[kBatch];
 #pragma unroll
@@ -377,9 +404,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_place_kernel(DispatchArgs a
     for (int64_t r = s_first[a.E] + static_cast<int64_t>(blockIdx.x) * kThreads + tid; r < a.R;
          r += static_cast<int64_t>(gridDim.x) * kThreads)
         a.pair_of_row[r] = -1;
-    if (a.align > 1)
-        for (int e = blockIdx.x; e < a.E; e += gridDim.x)
-            for (int r = s_first[e] + s_count[e] + wave; r < s_first[e + 1]; r += kWaves) fill_row(a, r, lane, kWave);
+    if (a.align > 1) fill_share(a, s_count, s_first, blockIdx.x, gridDim.x);
     __syncthreads();
     if (a.rows)
         for (int i = wave; i < tokens && t0 + i < a.T; i += kWaves)
@@ -389,13 +414,20 @@ __global__ __launch_bounds__(kThreads) void dispatch_place_kernel(DispatchArgs a
 // ------------------------------------------------------------------ back
 
 // Thread c of a token's takes elements [8 c, 8 c + 8), or, behind the row's
-// whole chunks, one element each.
+// whole chunks, one element each. SHORT rows: `tokens` tokens a workgroup (else a
+// wave's token is one, and its rows are found by scalar loads).
 // kG rows are on their way at once.
-template <typename T, typename O, int kG>
-__global__ __launch_bounds__(kThreads) void combine_rows_kernel(RowsArgs a) {
-    const int t = blockIdx.x, c = blockIdx.y * kThreads + threadIdx.x;
-    const int chunks = a.H / kVec, rest = a.H % kVec;
-    if (c >= chunks + rest) return;
+template <typename T, typename O, int kG, bool SHORT>
+__global__ __launch_bounds__(kThreads) void combine_rows_kernel(RowsArgs a, int tokens) {
+    const int chunks = a.H / kVec, rest = a.H % kVec, items = chunks + rest;
+    int t = blockIdx.x, c = blockIdx.y * kThreads + threadIdx.x;
+    if constexpr (SHORT) {
+        const int mine = threadIdx.x / items;
+        if (mine >= tokens) return;
+        t = t * tokens + mine;
+        c = threadIdx.x - mine * items;
+    }
+    if (c >= items || t >= a.T) return;
     const T *rows = static_cast<const T *>(a.rows);
     const size_t out_at = static_cast<size_t>(t) * a.H;
     const O *addend = static_cast<const O *>(a.addend) + out_at;
@@ -462,17 +494,18 @@ __device__ __forceinline__ float product(float d, float w) {
 }
 
 constexpr int kLook = 16;
-// Workgroups [0, T): a token's K rows, kAhead of them on their way at once. The
-// others: rows without a pair.
-template <typename T, typename O>
+// Workgroups [0, T * parts): KM of a token's K rows, kAhead of them on their way
+// at once. The others: rows without a pair.
+template <typename T, typename O, int KM>
 __global__ __launch_bounds__(kThreads) void combine_grad_kernel(RowsArgs a) {
+    const int parts = (a.K + KM - 1) / KM, working = a.T * parts;
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
     const int chunks = a.H / kVec, rest = a.H % kVec;
-    if (static_cast<int>(blockIdx.x) >= a.T) {
+    if (static_cast<int>(blockIdx.x) >= working) {
         // every wave looks at kLook rows and takes each kWaves-th of those without a pair
         const size_t bytes = static_cast<size_t>(a.H) * sizeof(T);
-        for (int64_t r0 = static_cast<int64_t>(blockIdx.x - a.T) * kLook; r0 < a.R;
-             r0 += static_cast<int64_t>(gridDim.x - a.T) * kLook) {
+        for (int64_t r0 = static_cast<int64_t>(blockIdx.x - working) * kLook; r0 < a.R;
+             r0 += static_cast<int64_t>(gridDim.x - working) * kLook) {
             const int r = static_cast<int>(r0) + lane;
             bool none = false;
             if (lane < kLook && r < a.R) {
@@ -486,36 +519,37 @@ __global__ __launch_bounds__(kThreads) void combine_grad_kernel(RowsArgs a) {
         }
         return;
     }
-    __shared__ float s_dot[kWaves][kMaxTopK], s_scale[kMaxTopK];
-    __shared__ int s_row[kMaxTopK];
-    const int t = blockIdx.x;
-    if (tid < a.K) {
-        s_row[tid] = own_row(a, t * a.K + tid);
-        s_scale[tid] = a.scales ? a.scales[t * a.K + tid] : 1.0f;
+    __shared__ float s_dot[kWaves][KM], s_scale[KM];
+    __shared__ int s_row[KM];
+    const int t = blockIdx.x / parts, k_first = blockIdx.x % parts * KM, count = min(a.K - k_first, KM);
+    const int p0 = t * a.K + k_first;
+    if (tid < count) {
+        s_row[tid] = own_row(a, p0 + tid);
+        s_scale[tid] = a.scales ? a.scales[p0 + tid] : 1.0f;
     }
     __syncthreads();
     const O *dout = static_cast<const O *>(a.dout) + static_cast<size_t>(t) * a.H;
     const T *rows = static_cast<const T *>(a.rows);
     T *drows = static_cast<T *>(a.drows);
-    float dot[kMaxTopK] = {};
+    float dot[KM] = {};
     struct Eight { T v[kVec]; };
     for (int c = tid; c < chunks; c += kThreads) {
         float d[kVec];
         load8(dout + c * kVec, d);
 #pragma unroll
-        for (int k0 = 0; k0 < kMaxTopK; k0 += kAhead) {
-            if (k0 >= a.K) break;
+        for (int k0 = 0; k0 < KM; k0 += kAhead) {
+            if (k0 >= count) break;
             Eight v[kAhead];
             if (a.dscales) {
 #pragma unroll
                 for (int j = 0; j < kAhead; ++j) {  // dropped pairs, and k past the end: some row, not counted
-                    const int r = max(s_row[min(k0 + j, a.K - 1)], 0);
+                    const int r = max(s_row[min(k0 + j, count - 1)], 0);
                     if (a.R > 0) __builtin_memcpy(&v[j], rows + static_cast<size_t>(r) * a.H + c * kVec, sizeof v[j]);
                 }
             }
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
-                const int k = k0 + j, r = __builtin_amdgcn_readfirstlane(k < a.K ? s_row[k] : -1);
+                const int k = k0 + j, r = __builtin_amdgcn_readfirstlane(k < count ? s_row[k] : -1);
                 if (r < 0) continue;
                 if (a.dscales) {
 #pragma unroll
@@ -534,8 +568,8 @@ __global__ __launch_bounds__(kThreads) void combine_grad_kernel(RowsArgs a) {
     const int at = chunks * kVec + tid;
     const float dt = tid < rest ? to_f32(dout[at]) : 0.0f;
 #pragma unroll
-    for (int k = 0; k < kMaxTopK; ++k) {
-        if (k >= a.K) break;
+    for (int k = 0; k < KM; ++k) {
+        if (k >= count) break;
         const int r = s_row[k];
         if (r >= 0 && tid < rest) {
             if (a.dscales) dot[k] += to_f32(rows[static_cast<size_t>(r) * a.H + at]) * dt;
@@ -547,34 +581,42 @@ __global__ __launch_bounds__(kThreads) void combine_grad_kernel(RowsArgs a) {
         }
     }
     __syncthreads();
-    if (a.dscales && tid < a.K) {
+    if (a.dscales && tid < count) {
         float sum = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) sum += s_dot[w][tid];
-        a.dscales[t * a.K + tid] = sum;
+        a.dscales[p0 + tid] = sum;
     }
 }
 
 template <typename T, typename O>
 hipError_t combine_of(const RowsArgs &a, hipStream_t s) {
     const int items = a.H / kVec + a.H % kVec, passes = (a.K + 7) / 8;
-    const dim3 grid(a.T, (items + kThreads - 1) / kThreads), blk(kThreads);
+    const int tokens = kThreads / items > 1 ? kThreads / items : 1;
+    const dim3 grid((a.T + tokens - 1) / tokens, (items + kThreads - 1) / kThreads), blk(kThreads);
+    auto launch = [&](auto g) {
+        if (tokens > 1) hipLaunchKernelGGL((combine_rows_kernel<T, O, g, true>), grid, blk, 0, s, a, tokens);
+        else hipLaunchKernelGGL((combine_rows_kernel<T, O, g, false>), grid, blk, 0, s, a, tokens);
+    };
     switch ((a.K + passes - 1) / passes) {
-        case 1: hipLaunchKernelGGL((combine_rows_kernel<T, O, 1>), grid, blk, 0, s, a); break;
-        case 2: hipLaunchKernelGGL((combine_rows_kernel<T, O, 2>), grid, blk, 0, s, a); break;
-        case 3: hipLaunchKernelGGL((combine_rows_kernel<T, O, 3>), grid, blk, 0, s, a); break;
-        case 4: hipLaunchKernelGGL((combine_rows_kernel<T, O, 4>), grid, blk, 0, s, a); break;
-        case 5: hipLaunchKernelGGL((combine_rows_kernel<T, O, 5>), grid, blk, 0, s, a); break;
-        case 6: hipLaunchKernelGGL((combine_rows_kernel<T, O, 6>), grid, blk, 0, s, a); break;
-        case 7: hipLaunchKernelGGL((combine_rows_kernel<T, O, 7>), grid, blk, 0, s, a); break;
-        default: hipLaunchKernelGGL((combine_rows_kernel<T, O, 8>), grid, blk, 0, s, a); break;
+        case 1: launch(std::integral_constant<int, 1>{}); break;
+        case 2: launch(std::integral_constant<int, 2>{}); break;
+        case 3: launch(std::integral_constant<int, 3>{}); break;
+        case 4: launch(std::integral_constant<int, 4>{}); break;
+        case 5: launch(std::integral_constant<int, 5>{}); break;
+        case 6: launch(std::integral_constant<int, 6>{}); break;
+        case 7: launch(std::integral_constant<int, 7>{}); break;
+        default: launch(std::integral_constant<int, 8>{}); break;
     }
     return hipGetLastError();
 }
+// Few tokens: four rows a workgroup, for a shorter way through.
 template <typename T, typename O>
 hipError_t grad_of(const RowsArgs &a, hipStream_t s) {
-    const int others = a.drows ? (a.R + kLook - 1) / kLook : 0;
-    hipLaunchKernelGGL((combine_grad_kernel<T, O>), dim3(a.T + (others < 8192 ? others : 8192)), dim3(kThreads), 0, s, a);
+    const int looks = a.drows ? (a.R + kLook - 1) / kLook : 0, others = looks < 8192 ? looks : 8192;
+    const dim3 blk(kThreads);
+    if (a.T < 512) hipLaunchKernelGGL((combine_grad_kernel<T, O, 4>), dim3(a.T * ((a.K + 3) / 4) + others), blk, 0, s, a);
+    else hipLaunchKernelGGL((combine_grad_kernel<T, O, kMaxTopK>), dim3(a.T + others), blk, 0, s, a);
     return hipGetLastError();
 }
 
@@ -599,7 +641,9 @@ hipError_t launch_dispatch(const DispatchArgs &a, hipStream_t s) {
         return hipGetLastError();
     }
     if (P <= kSmallPairs) {
-        hipLaunchKernelGGL(dispatch_small_kernel, dim3(a.T), blk, 0, s, a);
+        const dim3 grid(a.T + (a.align > 1 ? 512 : 0));
+        if (P <= 4 * kThreads) hipLaunchKernelGGL(dispatch_small_kernel<4>, grid, blk, 0, s, a);
+        else hipLaunchKernelGGL(dispatch_small_kernel<kSmallPairs / kThreads>, grid, blk, 0, s, a);
         return hipGetLastError();
     }
     const int tokens = tokens_of(a.K), blocks = (a.T + kParts * tokens - 1) / (kParts * tokens);
