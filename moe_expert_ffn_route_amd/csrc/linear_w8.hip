@@ -12,6 +12,8 @@
 // behind a row's end (the next row's codes) meets zeros.
 #include "ops.h"
 
+#include <type_traits>
+#include <utility>
 #include "../../include/moe_w8a8.h"
 
 namespace moe {
@@ -257,11 +259,17 @@ __global__ __launch_bounds__(kFewWaves *kWave) void linear_w8_few_kernel(LinearW
 // bytes a cycle, half of the time with NW = 4. (With both operands in LDS and
 // 64 x 64 sums per wave, reading LDS would take all of it.)
 //
-// x lies in four buffers, stage s in buffer s % 4, copied straight to LDS two
+// x lies in NB buffers, stage s in buffer s % NB, copied straight to LDS NB - 2
 // stages ahead (into a buffer whose operands every wave has multiplied by the
 // last barrier, not only asked for), eight rows of 128 bytes an instruction: a lane fetches the
 // 16-byte chunk that belongs at its place (x_at). Rows of ODD length are not
-// aligned for such copies: they go through registers, a stage ahead.
+// aligned for such copies: they go through registers.
+//
+// Measured (T, N, K 8192, bf16 out): 2.45 POP/s, the library's int8 product 2.13;
+// the matrix units are busy 67 % of the cycles, at the 1.75 GHz that the clock
+// falls to under this load; reading LDS takes 18 %, and what is loaded is 30
+// bytes a cycle and CU. 256 tokens a workgroup (one wave per SIMD) was 35 %
+// slower.
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(1))) void glb_void;
 constexpr int kManyWaves = 4;
@@ -343,14 +351,37 @@ __device__ __forceinline__ void write_sums(const LinearW8Args &a, const v4i (&ac
     }
 }
 
-template <int MT, int NW, bool ODD>
-__global__ __launch_bounds__(kManyWaves *kWave, MT *NW >= 64 ? 1 : 2) void linear_w8_many_kernel(LinearW8Args a,
-                                                                                             int token_blocks,
-                                                                                             int row_blocks) {
+template <int... I, typename F>
+__device__ __forceinline__ void unrolled(std::integer_sequence<int, I...>, F f) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+
+template <int MT, int NW, int NB, int WR, bool ODD>
+__global__ __launch_bounds__(kManyWaves *kWave, 2) void linear_w8_many_kernel(LinearW8Args a, int token_blocks,
+                                                                            int row_blocks) {
+    static_assert((NB == 4 && WR == 2) || (NB == 8 && WR == 4), "");
+    constexpr int XA = NB - 2;           // stages that x is copied ahead
+    constexpr int XO = WR == 4 ? 4 : 2;  // ODD: that it is loaded ahead, to be put two ahead
+    constexpr int XR = XO == 4 ? 4 : 1;  // sets of registers for that
+    constexpr auto kGroup = std::make_integer_sequence<int, NB>{};
     constexpr int kStage = MT * 2048, kCopies = MT / 2;  // copies of 1 KB per wave and stage
     constexpr int kAhead = MT >= 4 ? 4 : 2;              // operands of x on their way from LDS
     constexpr int kBuffer = kStage > kPlaceBytes<NW> ? kStage : kPlaceBytes<NW>;
+    constexpr int kMore = NB == 8 ? kBuffer : 16;
+    // arrays of their own, by which the compiler tells copies into one from reads of another
     __shared__ __attribute__((aligned(16))) char s_x0[kBuffer], s_x1[kBuffer], s_x2[kBuffer], s_x3[kBuffer];
+    __shared__ __attribute__((aligned(16))) char s_x4[kMore], s_x5[kMore], s_x6[kMore], s_x7[kMore];
+    auto buffer = [&](auto i) -> char * {
+        constexpr int n = decltype(i)::value % NB;
+        if constexpr (n == 0) return s_x0;
+        else if constexpr (n == 1) return s_x1;
+        else if constexpr (n == 2) return s_x2;
+        else if constexpr (n == 3) return s_x3;
+        else if constexpr (n == 4) return s_x4;
+        else if constexpr (n == 5) return s_x5;
+        else if constexpr (n == 6) return s_x6;
+        else return s_x7;
+    };
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int r = lane & 15, kq = lane >> 4;
@@ -421,16 +452,18 @@ __global__ __launch_bounds__(kManyWaves *kWave, MT *NW >= 64 ? 1 : 2) void linea
         xf[q % kAhead] = *reinterpret_cast<const v4i *>(buf + (q % MT) * 2048 + x_at(r, q / MT * 4 + kq));
     };
     // vmcnt: copies of stage s + 1 have landed when no more than what was issued after them is left
-    constexpr int kLeft = kCopies + 4 * NW;
+    constexpr int kLeft = 2 * NW + (XA - 1) * (kCopies + 2 * NW);
     static_assert(kLeft <= 63 && 2 * MT > kAhead, "");
     constexpr int kWait = (kLeft & 15) | ((kLeft >> 4) << 14) | (7 << 4) | (15 << 8);
-    // Stage s from `cur`, whose first kAhead operands have been read; the next
-    // stage's are read at its end.
-    auto step = [&](int s, const v4i (&now)[NW][2], v4i (&next)[NW][2], v4i (&xr)[kCopies], const char *cur,
-                    char *later, char *ahead) {
-        if constexpr (ODD) fetch_x(min(s + 2, last), xr);
-        else copy_x(min(s + 2, last), ahead);
-        fetch_w(min(s + 1, last), next);
+    v4i wr[WR][NW][2], xr[XR][kCopies];
+    // Stage s, the group's u-th, whose first kAhead operands have been read; the
+    // next stage's are read at its end.
+    auto step = [&](auto at, int s) {
+        constexpr int u = decltype(at)::value;
+        const char *cur = buffer(at), *later = buffer(std::integral_constant<int, u + 1>{});
+        if constexpr (ODD) fetch_x(min(s + XO, last), xr[(u + XO) % XR]);
+        else copy_x(min(s + XA, last), buffer(std::integral_constant<int, u + XA>{}));
+        fetch_w(min(s + WR - 1, last), wr[(u + WR - 1) % WR]);
 #pragma unroll
         for (int q = 0; q < 2 * MT; ++q) {
             if (q == 2 * MT - kAhead) {
@@ -443,66 +476,72 @@ __global__ __launch_bounds__(kManyWaves *kWave, MT *NW >= 64 ? 1 : 2) void linea
             }
 #pragma unroll
             for (int j = 0; j < NW; ++j)
-                acc[j][q % MT] = __builtin_amdgcn_mfma_i32_16x16x64_i8(now[j][q / MT], xf[q % kAhead], acc[j][q % MT], 0, 0, 0);
+                acc[j][q % MT] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wr[u % WR][j][q / MT], xf[q % kAhead], acc[j][q % MT], 0, 0, 0);
             if (q + kAhead < 2 * MT) read_x(cur, q + kAhead);
             else read_x(later, q + kAhead - 2 * MT);
             // as written: the scheduler would draw the reads together and wait for all of them
             __builtin_amdgcn_sched_group_barrier(0x8, NW, 0);    // MFMA
             __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // LDS read
         }
-        if constexpr (ODD) put_x(xr, ahead);
+        if constexpr (ODD) put_x(xr[(u + 2) % XR], buffer(std::integral_constant<int, u + 2>{}));
     };
-    v4i w0[NW][2], w1[NW][2], xr[kCopies];
-    if constexpr (ODD) {
-        fetch_x(0, xr);
-        put_x(xr, s_x0);
-        fetch_x(min(1, last), xr);
-        put_x(xr, s_x1);
-    } else {
-        copy_x(0, s_x0);
-        copy_x(min(1, last), s_x1);
-    }
-    fetch_w(0, w0);
+    // A stage of the last ones, all of whose x lies in LDS.
+    auto multiply = [&](const char *buf, const v4i (&w)[NW][2]) {
+#pragma unroll
+        for (int q = 0; q < 2 * MT; ++q) {
+            const v4i v = *reinterpret_cast<const v4i *>(buf + (q % MT) * 2048 + x_at(r, q / MT * 4 + kq));
+#pragma unroll
+            for (int j = 0; j < NW; ++j)
+                acc[j][q % MT] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[j][q / MT], v, acc[j][q % MT], 0, 0, 0);
+        }
+    };
+    unrolled(kGroup, [&](auto at) {
+        constexpr int u = decltype(at)::value;
+        if constexpr (ODD) {
+            if constexpr (u < XO) fetch_x(min(u, last), xr[u % XR]);
+            if constexpr (u < 2) put_x(xr[u % XR], buffer(at));
+        } else if constexpr (u < XA) {
+            copy_x(min(u, last), buffer(at));
+        }
+        if constexpr (u < WR - 1) fetch_w(min(u, last), wr[u]);
+    });
     __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
     __syncthreads();
 #pragma unroll
     for (int q = 0; q < kAhead; ++q) read_x(s_x0, q);
-    // Groups of four stages, then the few that are left (an exit inside the
-    // group would cost the sums their registers); for ODD the last stage is
-    // always among these.
+    // Groups of NB stages, then the few that are left (an exit inside the group
+    // would cost the sums their registers); for ODD the last stage is always
+    // among these.
     int s = 0;
-    for (; s + 4 + (ODD ? 1 : 0) <= a.k_tiles; s += 4) {
-        step(s, w0, w1, xr, s_x0, s_x1, s_x2);
-        step(s + 1, w1, w0, xr, s_x1, s_x2, s_x3);
-        step(s + 2, w0, w1, xr, s_x2, s_x3, s_x0);
-        step(s + 3, w1, w0, xr, s_x3, s_x0, s_x1);
-    }
+    for (; s + NB + (ODD ? 1 : 0) <= a.k_tiles; s += NB) unrolled(kGroup, [&](auto at) { step(at, s + decltype(at)::value); });
     if (s < a.k_tiles) {
         if constexpr (ODD) {
             __syncthreads();  // the buffers are read until here
-            bring_x(s, s_x0);
-            bring_x(min(s + 1, last), s_x1);
-            bring_x(min(s + 2, last), s_x2);
-            bring_x(min(s + 3, last), s_x3);
-        } else {
-            copy_x(min(s + 2, last), s_x2);
+            unrolled(kGroup, [&](auto at) {
+                if (s + decltype(at)::value < a.k_tiles) bring_x(s + decltype(at)::value, buffer(at));
+            });
+        } else {  // the group's last buffer but one: what was read of it has been multiplied
+            copy_x(min(s + NB - 2, last), buffer(std::integral_constant<int, NB - 2>{}));
         }
         __builtin_amdgcn_s_waitcnt(0x0070);
         __syncthreads();
-        for (int i = 0; s + i < a.k_tiles; ++i) {
-            const char *buf = i == 0 ? s_x0 : i == 1 ? s_x1 : i == 2 ? s_x2 : s_x3;
-            fetch_w(min(s + i + 1, last), w1);
-#pragma unroll
-            for (int q = 0; q < 2 * MT; ++q) {
-                const v4i v = *reinterpret_cast<const v4i *>(buf + (q % MT) * 2048 + x_at(r, q / MT * 4 + kq));
+        if constexpr (NB == 8) {
+            unrolled(kGroup, [&](auto at) {
+                constexpr int u = decltype(at)::value;
+                if (s + u < a.k_tiles) {
+                    fetch_w(min(s + u + WR - 1, last), wr[(u + WR - 1) % WR]);
+                    multiply(buffer(at), wr[u % WR]);
+                }
+            });
+        } else {
+            for (int i = 0; s + i < a.k_tiles; ++i) {
+                fetch_w(min(s + i + 1, last), wr[1]);
+                multiply(i == 0 ? s_x0 : i == 1 ? s_x1 : i == 2 ? s_x2 : s_x3, wr[0]);
 #pragma unroll
                 for (int j = 0; j < NW; ++j)
-                    acc[j][q % MT] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w0[j][q / MT], v, acc[j][q % MT], 0, 0, 0);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) wr[0][j][h] = wr[1][j][h];
             }
-#pragma unroll
-            for (int j = 0; j < NW; ++j)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) w0[j][h] = w1[j][h];
         }
     }
     __builtin_amdgcn_s_waitcnt(0x0070);  // copies past the last stage have landed before the LDS is used again
@@ -517,13 +556,13 @@ __global__ __launch_bounds__(kManyWaves *kWave, MT *NW >= 64 ? 1 : 2) void linea
     }
 }
 
-template <int MT, int NW>
+template <int MT, int NW, int NB = 4, int WR = 2>
 hipError_t launch_many(const LinearW8Args &a, hipStream_t s) {
     const int token_blocks = (a.T + MT * 16 - 1) / (MT * 16), rows = kManyWaves * NW;
     const int row_blocks = (a.n_tiles + rows - 1) / rows;
     const dim3 grid(static_cast<unsigned>(row_blocks) * token_blocks), blk(kManyWaves * kWave);
-    if (a.K % 16) hipLaunchKernelGGL((linear_w8_many_kernel<MT, NW, true>), grid, blk, 0, s, a, token_blocks, row_blocks);
-    else hipLaunchKernelGGL((linear_w8_many_kernel<MT, NW, false>), grid, blk, 0, s, a, token_blocks, row_blocks);
+    if (a.K % 16) hipLaunchKernelGGL((linear_w8_many_kernel<MT, NW, NB, WR, true>), grid, blk, 0, s, a, token_blocks, row_blocks);
+    else hipLaunchKernelGGL((linear_w8_many_kernel<MT, NW, NB, WR, false>), grid, blk, 0, s, a, token_blocks, row_blocks);
     return hipGetLastError();
 }
 
@@ -555,14 +594,15 @@ hipError_t launch_pack_w8(const int8_t *codes, const float *scale, int8_t *dst_c
 // weight rows and joins eight sums; it wants one workgroup for each CU, of the
 // least x and weights (16 R rows, ROWS tokens). The other wants two large
 // workgroups a CU, or more small ones; with a short K, small ones, whose ends
-// overlap others' products. In us (bf16 out; few tokens / many, * taken):
-//   T 64, N 4096, K 4096: 32 x 2 *6.3, 64 x 4 10.9 / 12.5   T 128, N 8192: 64 x 4 *11.7 / 13.4
-//   T 37, N 5006, K 4256, gated: 16 x 4 *6.8, 64 x 4 10.7 / 13.7    T 512, N 4096: 19.7 / 64 x 4 *16.8
-//   T 1000, N 1000, K 1000: 7.8 / 32 x 4 *5.4              T 64, N 28672: 33.5 / 64 x 4 *28.2, 64 x 8 32.4
-// many, tokens x row tiles 128 x 16, 128 x 8, 64 x 8, 64 x 4, 32 x 4, K 4096:
-//   T 4096, N 8192 *135 162 176 222 270     T 2048, N 4096 43 *39 43 53 68     T 512, N 8192 39 28 *24 28 35
-//   T 256, N 8192 38 27 21 *17 18           T 256, N 4096 38 27 20 16 13 (few: *10.9)
-//   K 700, T 2500, N 5000: 27 32 *25 31 32
+// overlap others' products; with less than two a CU, eight stages under way
+// instead of four. In us (bf16 out; few tokens / many, * taken):
+//   T 64, N 4096, K 4096: 32 x 2 *6.3, 64 x 4 10.9 / 12.5   T 128, N 8192: 64 x 4 *11.8 / 12.2
+//   T 37, N 5006, K 4256, gated: 16 x 4 *6.8, 64 x 4 10.7 / 13.7    T 512, N 4096: 19.7 / 64 x 8 *16.9
+//   T 1000, N 1000, K 1000: 7.8 / 32 x 4 *5.4              T 64, N 28672: 33.5 / 64 x 8 *29.7
+// many, tokens x row tiles 128 x 16, 128 x 8, 64 x 8, 64 x 4, 32 x 4, K 4096 (eight stages in brackets):
+//   T 4096, N 8192 *121 146 153 201 258     T 2048, N 4096 40 *38 41 52 67 (64 x 8 46)
+//   T 512, N 8192 38 28 *23 27 35 (25)      T 256, N 8192 38 27 20 20 19 (64 x 8 *16.9, 64 x 4 17.2, 32 x 4 20.2)
+//   K 700, T 2500, N 5000: 27 32 *25 31 32  K 8429, T 636, N 2332: 64 x 8 36 (*31), 32 x 4 37 (37)
 hipError_t launch_linear_w8(const LinearW8Args &a, hipStream_t s) {
     auto blocks = [&](int tokens, int tiles) {
         return static_cast<int64_t>((a.T + tokens - 1) / tokens) * ((a.n_tiles + tiles - 1) / tiles);
@@ -581,8 +621,8 @@ hipError_t launch_linear_w8(const LinearW8Args &a, hipStream_t s) {
     if (a.k_tiles >= 16 && blocks(128, 16) >= 512) return launch_many<8, 4>(a, s);
     if (a.k_tiles >= 16 && blocks(128, 8) >= 400) return launch_many<8, 2>(a, s);
     if (blocks(64, 8) >= 384) return launch_many<4, 2>(a, s);
-    if (blocks(64, 4) >= 384) return launch_many<4, 1>(a, s);
-    return launch_many<2, 1>(a, s);
+    if (a.k_tiles >= 16) return blocks(64, 8) >= 160 ? launch_many<4, 2, 8, 4>(a, s) : launch_many<2, 1, 8, 4>(a, s);
+    return blocks(64, 4) >= 384 ? launch_many<4, 1>(a, s) : launch_many<2, 1>(a, s);
 }
 
 }  // namespace moe
