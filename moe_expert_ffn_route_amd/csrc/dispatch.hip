@@ -398,7 +398,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_place_kernel(DispatchArgs a
     }
     if (blockIdx.x == 0)
         for (int e = tid; e <= a.E; e += kThreads) {
-            if (e < a.E) a.counts[e] = s_count[e];
+            if (!SCANNED && e < a.E) a.counts[e] = s_count[e];
             a.offset[e] = s_first[e];
         }
     for (int64_t r = s_first[a.E] + static_cast<int64_t>(blockIdx.x) * kThreads + tid; r < a.R;
@@ -435,18 +435,18 @@ __global__ __launch_bounds__(kThreads) void combine_rows_kernel(RowsArgs a, int 
     auto sum = [&](auto load, auto &acc) {
         for (int k0 = 0; k0 < a.K && a.R > 0; k0 += kG) {
             decltype(load(rows)) v[kG];
+            bool kept[kG];
+            float w[kG];
 #pragma unroll
             for (int j = 0; j < kG; ++j) {  // dropped pairs, and k past the end: some row, not counted
-                const int r = a.row_of_pair[t * a.K + min(k0 + j, a.K - 1)];
-                v[j] = load(rows + static_cast<size_t>(static_cast<unsigned>(r) < static_cast<unsigned>(a.R) ? r : 0) * a.H);
+                const int p = t * a.K + min(k0 + j, a.K - 1), r = a.row_of_pair[p];
+                w[j] = a.scales ? a.scales[p] : 1.0f;
+                kept[j] = k0 + j < a.K && static_cast<unsigned>(r) < static_cast<unsigned>(a.R);
+                v[j] = load(rows + static_cast<size_t>(kept[j] ? r : 0) * a.H);
             }
 #pragma unroll
-            for (int j = 0; j < kG; ++j) {
-                if (k0 + j >= a.K) break;
-                const int r = a.row_of_pair[t * a.K + k0 + j];
-                if (static_cast<unsigned>(r) >= static_cast<unsigned>(a.R)) continue;
-                acc(v[j], a.scales ? a.scales[t * a.K + k0 + j] : 1.0f);
-            }
+            for (int j = 0; j < kG; ++j)
+                if (kept[j]) acc(v[j], w[j]);
         }
     };
     struct Eight { T v[kVec]; };

@@ -432,3 +432,52 @@ def test_captured(T, K):
         step()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(kept, (*out.values(), back, dr, ds)))
+
+
+@pytest.mark.parametrize("T,K", [(1500, 4), (40000, 2)])
+def test_two_graphs_share_a_workspace(T, K):
+    """Batches that use it; replayed in turn, with other ids each time."""
+    E, H = 40, 24
+    d = moe.make_dispatch_dims(T, H, E, K, dtype=I8, row_align=8)
+    need = moe.moe_w8a8_dispatch_workspace_size(d)
+    assert need > 0
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    R = moe.moe_w8a8_dispatch_rows(d)
+    x = data(T, H, I8)
+    sides = []
+    for _ in range(2):
+        ids = ids_of(T, E, K).cuda()
+        out = dict(rows=torch.zeros(R, H, dtype=I8, device="cuda"), expert_token_nums=torch.empty(E, dtype=torch.int32, device="cuda"),
+                   expert_offset=torch.empty(E + 1, dtype=torch.int32, device="cuda"),
+                   row_of_pair=torch.empty(T, K, dtype=torch.int32, device="cuda"),
+                   pair_of_row=torch.empty(R, dtype=torch.int32, device="cuda"))
+        moe.moe_w8a8_dispatch(d, ids, x=x, workspace=ws, **out)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            moe.moe_w8a8_dispatch(d, ids, x=x, workspace=ws, **out)
+        sides.append((ids, out, graph))
+    for seed in range(3):
+        new = [ids_of(T, E, K, seed=10 * seed + i, kind="dropped" if seed else "random") for i in range(2)]
+        for (ids, _, _), i in zip(sides, new):
+            ids.copy_(i)
+        for _, _, graph in sides:
+            graph.replay()
+        torch.cuda.synchronize()
+        for (_, out, _), i in zip(sides, new):
+            rp, _, counts, offset = plain(i, E, 8)
+            assert torch.equal(out["row_of_pair"].cpu().long(), rp)
+            assert torch.equal(out["expert_token_nums"].cpu().long(), counts)
+            assert torch.equal(out["expert_offset"].cpu().long(), offset)
+            at = out["row_of_pair"].view(-1).long()
+            kept = at >= 0
+            assert torch.equal(out["rows"][at[kept]], x.repeat_interleave(K, 0)[kept])
+
+
+@pytest.mark.parametrize("T,K", [(8, 8), (16, 4), (17, 4), (33, 2), (500, 8), (513, 8), (70, 16)])
+def test_dispatch_at_the_borders_of_its_launches(T, K):
+    """64 and 4096 pairs, and one more, with and without padded tiles."""
+    for align in (1, 16):
+        for kind in ("random", "dropped"):
+            check_dispatch(ids_of(T, 48, K, kind=kind), 48, 200, I8, groups=3, align=align)
+            check_dispatch(ids_of(T, 48, K, kind=kind), 48, 1, I8, align=align)

@@ -93,6 +93,30 @@ def test_shapes(T, N, K):
     check(c, run(c, FP, packed=packed), acc=acc)
 
 
+# long contractions: the large tiles, eight stages under way, and row tiles of four; odd and even, K just past a group of stages
+LARGE = [(4096, 4096, 2064), (4100, 4100, 2053), (2050, 4100, 2064), (2060, 4090, 2181), (512, 4096, 2048), (520, 4090, 2065),
+         (1100, 1000, 2176), (1100, 1000, 3001), (256, 4096, 2064), (250, 4090, 3071), (128, 4096, 1920), (100, 3000, 4000)]
+
+
+@pytest.mark.parametrize("T,N,K", LARGE)
+def test_large(T, N, K):
+    c = make(T, N, K, bias=True)
+    acc, packed = sums(c), pack(c)
+    check(c, run(c, F32, packed=packed), acc=acc)
+    c["bias"] = None
+    check(c, run(c, BF, packed=packed), acc=acc)
+    check(c, run(c, FP, gated=True), gated=True, acc=acc)
+
+
+def test_a_token_is_the_same_in_every_kernel():
+    for K in (2064, 2069):
+        c = make(4200, 4112, K, bias=False, seed=19)
+        packed = pack(c)
+        whole = run(c, F32, packed=packed)
+        for T in (1, 16, 40, 100, 300, 700, 2100):
+            assert torch.equal(run(dict(c, x=c["x"][-T:], xs=c["xs"][-T:]), F32, packed=packed), whole[-T:]), (T, K)
+
+
 @pytest.mark.parametrize("T,N,K", [(1, 2, 1), (1, 4096, 1024), (7, 34, 193), (20, 512, 2048), (64, 258, 416), (100, 1042, 515),
                                    (260, 640, 768), (513, 1026, 1000), (1029, 2048, 260), (2000, 18, 48)])
 @pytest.mark.parametrize("dt", [BF, FP, F32], ids=["bf16", "fp16", "fp32"])
