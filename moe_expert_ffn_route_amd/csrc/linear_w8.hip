@@ -161,11 +161,17 @@ __global__ __launch_bounds__(kFewWaves *kWave) void linear_w8_few_kernel(LinearW
     const int r = lane & 15, kq = lane >> 4;
     // Workgroups b, b + 8, ... run on one XCD: each gets consecutive pairs of a
     // row block and a token block, token blocks first, so that the weights of a
-    // row block come from one XCD's L2.
-    const int row_blocks = (a.n_tiles + R - 1) / R, share = gridDim.x >> 3;
-    const int pair = static_cast<int>(blockIdx.x & 7) * share + static_cast<int>(blockIdx.x >> 3);
-    if (pair >= row_blocks * token_blocks) return;
-    const int nt0 = pair / token_blocks * R, t0 = pair % token_blocks * ROWS;
+    // row block come from one XCD's L2. With one token block nothing is shared,
+    // and there is no division to wait for.
+    const int row_blocks = (a.n_tiles + R - 1) / R, b = static_cast<int>(blockIdx.x);
+    int row_block = b, token_block = 0;
+    if (token_blocks > 1) {
+        const int pair = (b & 7) * static_cast<int>(gridDim.x >> 3) + (b >> 3);
+        row_block = pair / token_blocks;
+        token_block = pair - row_block * token_blocks;
+    }
+    if (row_block >= row_blocks) return;
+    const int nt0 = row_block * R, t0 = token_block * ROWS;
     char *place = lds + wave * kBufs * 2048;
     const int8_t *x = a.x + static_cast<size_t>(t0) * a.K;
     const RowEnd end(a, t0);
