@@ -42,9 +42,15 @@ __global__ __launch_bounds__(256) void pack_codes8_kernel(const int8_t *__restri
     bool ok;
     const int64_t row = source_row(a, nt, l & 15, ok);
     const int k0 = kt * kTileK + h * 64 + (l >> 4) * 16;
-    int8_t v[16];
+    int8_t v[16] = {};
+    const int8_t *from = src + row * a.K + k0;
+    if (ok && k0 + 16 <= a.K) {
+        __builtin_memcpy(v, from, 16);
+    } else if (ok) {
 #pragma unroll
-    for (int b = 0; b < 16; ++b) v[b] = ok && k0 + b < a.K ? src[row * a.K + k0 + b] : static_cast<int8_t>(0);
+        for (int b = 0; b < 16; ++b)
+            if (k0 + b < a.K) v[b] = from[b];
+    }
     __builtin_memcpy(dst + o * 16, v, 16);
 }
 __global__ __launch_bounds__(256) void pack_scales8_kernel(const float *__restrict__ scale, float *__restrict__ dst,
@@ -104,7 +110,16 @@ struct RowEnd {
 };
 
 __device__ __forceinline__ uint16_t bits16(float v, bool fp16) {
-    return fp16 ? __builtin_bit_cast(uint16_t, static_cast<_Float16>(v)) : f32_to_bf16(v);
+    return fp16 ? __builtin_bit_cast(uint16_t, static_cast<_Float16>(v)) : __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+}
+// Two outputs of type O (MOE_DTYPE_BF16 or FP16) in a word.
+template <int O>
+__device__ __forceinline__ int pair16(float u, float v) {
+    typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+    typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+    typedef float v2f __attribute__((ext_vector_type(2)));
+    if constexpr (O == MOE_DTYPE_FP16) return __builtin_bit_cast(int, v2h{static_cast<_Float16>(u), static_cast<_Float16>(v)});
+    else return __builtin_bit_cast(int, __builtin_convertvector((v2f{u, v}), v2bf));
 }
 
 // The finished sums of rows 4 * kq ..+3 of tile nt for token t.
@@ -281,20 +296,20 @@ typedef __attribute__((address_space(1))) void glb_void;
 constexpr int kManyWaves = 4;
 
 // The sums of a wave, NW row tiles from nt0 by MT token tiles from t0, to out
-// in elements of E bytes. Lanes hold up to four neighbouring outputs of a token
+// of type O. Lanes hold up to four neighbouring outputs of a token
 // each; through LDS of the wave's own (its lanes' accesses in order, for the
 // compiler too) they become 16 bytes of a row that neighbouring lanes continue.
 template <int NW>
 constexpr int kPlaceBytes = 16 * (NW * 16 * 4 + 16);
-template <int MT, int NW, int E, bool GATED>
+template <int MT, int NW, int O, bool GATED>
 __device__ __forceinline__ void write_sums(const LinearW8Args &a, const v4i (&acc)[NW][MT], int nt0, int t0, int lane,
                                            char *place) {
     typedef int v2i __attribute__((ext_vector_type(2)));
+    constexpr int E = O == MOE_DTYPE_FP32 ? 4 : 2;
     constexpr int kUnits = NW * (GATED ? 8 : 16), kRow = kUnits * E + 16;  // outputs of a token, and their bytes in LDS
     constexpr int kPer = 16 / E, kLanes = kUnits / kPer, kTokens = kWave / kLanes;
     const int r = lane & 15, kq = lane >> 4;
     const int units = GATED ? a.N / 2 : a.N, n0 = nt0 * (GATED ? 8 : 16);
-    const bool fp16 = a.out_dtype == MOE_DTYPE_FP16;
     float ws[NW][4], bias[NW][4] = {};
 #pragma unroll
     for (int j = 0; j < NW; ++j) {
@@ -327,15 +342,14 @@ __device__ __forceinline__ void write_sums(const LinearW8Args &a, const v4i (&ac
                         v2i{__float_as_int(u), __float_as_int(v)};
                 } else {
                     *(__attribute__((address_space(3))) volatile int *)(at + j * 16 + kq * 4) =
-                        bits16(u, fp16) | static_cast<int>(bits16(v, fp16)) << 16;
+                        pair16<O>(u, v);
                 }
             } else if constexpr (E == 4) {
                 *(__attribute__((address_space(3))) volatile v4i *)(at + j * 64 + kq * 16) =
                     v4i{__float_as_int(o[0]), __float_as_int(o[1]), __float_as_int(o[2]), __float_as_int(o[3])};
             } else {
                 *(__attribute__((address_space(3))) volatile v2i *)(at + j * 32 + kq * 8) =
-                    v2i{bits16(o[0], fp16) | static_cast<int>(bits16(o[1], fp16)) << 16,
-                        bits16(o[2], fp16) | static_cast<int>(bits16(o[3], fp16)) << 16};
+                    v2i{pair16<O>(o[0], o[1]), pair16<O>(o[2], o[3])};
             }
         }
 #pragma unroll
@@ -553,13 +567,13 @@ __global__ __launch_bounds__(kManyWaves *kWave, 2) void linear_w8_many_kernel(Li
     __builtin_amdgcn_s_waitcnt(0x0070);  // copies past the last stage have landed before the LDS is used again
     __syncthreads();
     char *place = wave == 0 ? s_x0 : wave == 1 ? s_x1 : wave == 2 ? s_x2 : s_x3;
-    if (a.out_dtype == MOE_DTYPE_FP32) {
-        if (a.gated) write_sums<MT, NW, 4, true>(a, acc, nt0, t0, lane, place);
-        else write_sums<MT, NW, 4, false>(a, acc, nt0, t0, lane, place);
-    } else {
-        if (a.gated) write_sums<MT, NW, 2, true>(a, acc, nt0, t0, lane, place);
-        else write_sums<MT, NW, 2, false>(a, acc, nt0, t0, lane, place);
-    }
+    auto write = [&](auto type) {
+        if (a.gated) write_sums<MT, NW, decltype(type)::value, true>(a, acc, nt0, t0, lane, place);
+        else write_sums<MT, NW, decltype(type)::value, false>(a, acc, nt0, t0, lane, place);
+    };
+    if (a.out_dtype == MOE_DTYPE_FP32) write(std::integral_constant<int, MOE_DTYPE_FP32>{});
+    else if (a.out_dtype == MOE_DTYPE_FP16) write(std::integral_constant<int, MOE_DTYPE_FP16>{});
+    else write(std::integral_constant<int, MOE_DTYPE_BF16>{});
 }
 
 template <int MT, int NW, int NB = 4, int WR = 2>
