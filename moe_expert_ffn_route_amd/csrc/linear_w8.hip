@@ -471,10 +471,15 @@ __global__ __launch_bounds__(kManyWaves *kWave, 2) void linear_w8_many_kernel(Li
     auto read_x = [&](const char *buf, int q) {  // operand q = half * MT + token tile
         xf[q % kAhead] = *reinterpret_cast<const v4i *>(buf + (q % MT) * 2048 + x_at(r, q / MT * 4 + kq));
     };
-    // vmcnt: copies of stage s + 1 have landed when no more than what was issued after them is left
-    constexpr int kLeft = 2 * NW + (XA - 1) * (kCopies + 2 * NW);
+    // What a wave waits for before the barrier that lets others read stage s + 1.
+    // Copies: of the XA - 1 steps since, nothing crosses the barriers between, but
+    // within a step the compiler may put the weights' loads before or after the
+    // copies: only those steps' loads may be left. ODD: every write to LDS, since
+    // the barrier by itself waits for none.
+    constexpr int kLeft = (XA - 1) * (kCopies + 2 * NW);
     static_assert(kLeft <= 63 && 2 * MT > kAhead, "");
-    constexpr int kWait = (kLeft & 15) | ((kLeft >> 4) << 14) | (7 << 4) | (15 << 8);
+    constexpr int kWait = ODD ? 15 | (3 << 14) | (7 << 4)                                    // lgkmcnt(0)
+                              : (kLeft & 15) | ((kLeft >> 4) << 14) | (7 << 4) | (15 << 8);  // vmcnt(kLeft)
     v4i wr[WR][NW][2], xr[XR][kCopies];
     // Stage s, the group's u-th, whose first kAhead operands have been read; the
     // next stage's are read at its end.
@@ -488,8 +493,8 @@ __global__ __launch_bounds__(kManyWaves *kWave, 2) void linear_w8_many_kernel(Li
         for (int q = 0; q < 2 * MT; ++q) {
             if (q == 2 * MT - kAhead) {
                 __builtin_amdgcn_sched_barrier(0);
-                if constexpr (!ODD) __builtin_amdgcn_s_waitcnt(kWait);
-                asm volatile("" ::: "memory");  // for the compiler; the LDS takes a wave's accesses in order
+                __builtin_amdgcn_s_waitcnt(kWait);
+                asm volatile("" ::: "memory");  // for the compiler
                 __builtin_amdgcn_s_barrier();
                 asm volatile("" ::: "memory");
                 __builtin_amdgcn_sched_barrier(0);
