@@ -587,7 +587,8 @@ MOE_W8A8_API moe_status_t moe_w8a8_linear_w4(const moe_w8a8_linear_w4_dims_t *di
  * stream, and tokens sorted by expert (for other ranks' experts, or for a
  * program's own) and back. The conventions at the top of this file hold; with
  * num_tokens == 0 a call does nothing, whatever its pointers, but that
- * moe_w8a8_dispatch writes its counts and offsets.
+ * moe_w8a8_dispatch writes its counts and offsets, and moe_w8a8_combine_grad
+ * zeros to drows.
  * ------------------------------------------------------------------------ */
 
 typedef struct {

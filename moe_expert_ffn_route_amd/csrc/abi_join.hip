@@ -382,7 +382,14 @@ extern "C" moe_status_t moe_w8a8_combine_grad(const moe_w8a8_combine_dims_t *d, 
                                               const float *expert_scales, void *drows, float *dscales, void *stream) {
     const moe_status_t st = check_combine(d);
     if (st != MOE_OK) return st;
-    if (d->num_tokens == 0) return MOE_OK;
+    if (d->num_tokens == 0) {  // no row has a pair
+        if (!drows || d->num_rows == 0) return MOE_OK;
+        if (!aligned(drows, 16)) return MOE_ERR_INVALID_ARG;
+        RowsArgs a = rows_args(d);
+        a.drows = drows;
+        a.streamed = is_much({Range{drows, d->num_rows * static_cast<size_t>(d->hidden) * dtype_bytes(d->dtype)}});
+        return of_launch(launch_combine_grad(a, static_cast<hipStream_t>(stream)));
+    }
     if (!dout || !row_of_pair || (d->num_rows > 0 && (!pair_of_row || (rows != nullptr) != (dscales != nullptr))) ||
         (!drows && !dscales) || !all_aligned({dout, rows, static_cast<const void *>(drows)}, 16) ||
         !all_aligned({static_cast<const void *>(row_of_pair), static_cast<const void *>(pair_of_row),

@@ -508,7 +508,9 @@ __global__ __launch_bounds__(kThreads) void combine_grad_kernel(RowsArgs a) {
              r0 += static_cast<int64_t>(gridDim.x - working) * kLook) {
             const int r = static_cast<int>(r0) + lane;
             bool none = false;
-            if (lane < kLook && r < a.R) {
+            if (a.T == 0) {  // no maps either
+                none = lane < kLook && r < a.R;
+            } else if (lane < kLook && r < a.R) {
                 const int p = a.pair_of_row[r];
                 none = static_cast<unsigned>(p) >= static_cast<unsigned>(a.T * a.K) || a.row_of_pair[p] != r;
             }

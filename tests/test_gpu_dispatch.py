@@ -330,6 +330,23 @@ def test_no_rows():
     assert bool((ds == 0).all())
 
 
+@pytest.mark.parametrize("dt", [BF, torch.float32])
+@pytest.mark.parametrize("R,H", [(1, 5), (50, 100), (2100, 4096)])
+def test_no_tokens(R, H, dt):
+    """No row has a pair: zeros, whatever the maps hold."""
+    buf = torch.full((R + 2, H), 3, dtype=dt, device="cuda")
+    if H % 8 == 0:
+        dr = buf[1:R + 1]
+    else:
+        dr = torch.full((R, H), 3, dtype=dt, device="cuda")
+    maps = torch.zeros(R, dtype=torch.int32, device="cuda")
+    ids = torch.empty(0, 4, dtype=torch.int32, device="cuda")
+    moe.moe_w8a8_combine_grad(moe.make_combine_dims(0, H, 4, R, dtype=dt), torch.empty(0, H, dtype=dt, device="cuda"), ids, maps,
+                              drows=dr)
+    assert bool((dr == 0).all())
+    assert bool((buf[0] == 3).all()) and bool((buf[R + 1] == 3).all())
+
+
 @pytest.mark.parametrize("T", [6, 600])
 def test_rows_outside_are_dropped(T):
     """Rows past the end or below 0 add nothing; a row that two pairs claim is

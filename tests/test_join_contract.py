@@ -235,7 +235,11 @@ def grad(lib, over=None, **kw):
     (dict(num_tokens=65537), UNS), (dict(hidden=16385), UNS), (dict(num_rows=(1 << 22) + 1), UNS), (dict(num_tokens=0), OK)])
 def test_combine_refuses_bad_dims(lib, over, code):
     assert combine(lib, over) == code
-    assert grad(lib, over) == code
+    # (without tokens drows is written all the same: zeros)
+    assert grad(lib, over, **({} if code != OK else dict(drows=None))) == code
+    if code == OK:
+        assert grad(lib, dict(over, num_rows=0)) == OK
+        assert grad(lib, over, drows=6 * MB + 8) == INV
 
 
 @pytest.mark.parametrize("kw", [dict(rows=None), dict(row_of_pair=None), dict(out=None), dict(rows=MB + 8),
