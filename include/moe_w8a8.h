@@ -14,8 +14,10 @@
  * Options of the same call (moe_w8a8_dims_t): the routing weight folded into
  * GEMM2's row scale (fuse_route_scale), group-wise activation scales
  * (quant_mode 2), and FP4 weights with FP8 activations (weight_format).
- * Around it: the pre-norm with 8-bit output, the router, and dense products
- * with 4-bit weights (at the end of this file).
+ * Around it (at the end of this file): the pre-norm with 8-bit output, the
+ * router, and dense products with 4-bit weights; dense products in 8-bit
+ * integers, the quantiser of an activation, the norm that joins the block's
+ * outputs to the residual stream, and tokens sorted by expert and back.
  *
  * Passages that define the operation (pages, by title):
  *   "FusedDeepMoE Kernel 深度分析报告": sec. 1.2 (inputs, outputs, attributes),

@@ -1,6 +1,6 @@
 """Build libmoe_w8a8.so (gfx950) in-tree with hipcc (one compile per source,
 in parallel, then a link), and _pycall.so, the Python entry of the operators
-around the block (host code, against the installed torch).
+beside the block (host code, against the installed torch).
 
     python -m moe_expert_ffn_route_amd.build
     python moe_expert_ffn_route_amd/build.py --library

