@@ -65,27 +65,41 @@ __device__ __forceinline__ V join_waves(V v, V *slot, int tr, int waves, V none,
     return v;
 }
 
-// Eight codes of a row, t = (v * Q) * inv rounded to nearest even as quant4
-// does, for |t| <= Q (but for its own rounding): int8 by an addition whose sum's
-// last bits are the integer, E4M3 by the hardware's conversion, which gives
-// e4m3_code's bits for every fp32 of up to 464 (both compared once, on all).
+// Eight codes of a row, quant4's bits: t = (v * Q) * inv, brought to [-Q, Q]
+// (where v * Q leaves fp32) and rounded to nearest even, int8 by an addition
+// whose sum's last bits are the integer, E4M3 by the hardware's conversion,
+// which gives e4m3_code's bits for every fp32 of up to 464 (both compared once,
+// on all). A NaN gives -127 (the median of three is the smaller one then), or
+// E4M3's NaN without a sign, for which a lane that has one takes quant4.
 __device__ __forceinline__ uint64_t quant8(const float (&v)[kVec], float inv, bool fp8) {
     uint32_t w[2];
     if (fp8) {
+        float t[kVec];
+        bool nan = false;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) t[e] = v[e] * kQMax<true> * inv;
+#pragma unroll
+        for (int e = 0; e < kVec; e += 2) nan |= __builtin_isunordered(t[e], t[e + 1]);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) t[e] = __builtin_amdgcn_fmed3f(t[e], -kQMax<true>, kQMax<true>);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            float t[4];
+            const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(t[4 * h], t[4 * h + 1], 0, false);
+            w[h] = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(t[4 * h + 2], t[4 * h + 3], lo, true));
+        }
+        if (nan) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) t[e] = v[4 * h + e] * kQMax<true> * inv;
-            const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], 0, false);
-            w[h] = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], lo, true));
+            for (int h = 0; h < 2; ++h) w[h] = quant4<true>(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3], inv);
         }
     } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             uint32_t b[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) b[e] = __float_as_uint(v[4 * h + e] * kQMax<false> * inv + 12582912.0f);  // 1.5 * 2^23
+            for (int e = 0; e < 4; ++e) {
+                const float t = __builtin_amdgcn_fmed3f(v[4 * h + e] * kQMax<false> * inv, -kQMax<false>, kQMax<false>);
+                b[e] = __float_as_uint(t + 12582912.0f);  // 1.5 * 2^23
+            }
             const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0C0C0400), hi = __builtin_amdgcn_perm(b[3], b[2], 0x04000C0C);
             w[h] = lo | hi;
         }

@@ -152,6 +152,42 @@ def test_quant_other_rows_of_a_row_that_is_not_finite():
     assert torch.equal(got[0][rows], want[0][rows]) and torch.equal(got[1][rows], want[1][rows])
 
 
+def codes_by_the_rule(v, inv, quant):
+    """(v * Q) * inv in fp32 as the block's quantiser takes it, any v."""
+    t = (v * (127.0 if quant == "int8" else 448.0)) * inv
+    if quant == "int8":
+        return torch.where(t.isnan(), -127.0, t.round().clamp(-127, 127)).to(torch.int8).view(torch.uint8)
+    c = t.nan_to_num(0.0, 448.0, -448.0).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    return torch.where(t.isnan(), torch.tensor(0x7F, dtype=torch.uint8), c)
+
+
+@pytest.mark.parametrize("quant", ["int8", "fp8"])
+def test_codes_of_any_value_follow_the_rule(quant):
+    """NaN, infinities and values whose product with 127 or 448 leaves fp32: the
+    same codes within whole chunks and behind them, from the quantiser and from
+    a norm whose weights are that large."""
+    nan, inf, top = float("nan"), float("inf"), 3.0e38
+    special = [nan, -nan, inf, -inf, top, -top, 1e36, -1e36, 1.0, -1.0, 0.0, 5e35, -4e36]
+    x = torch.randn(len(special) + 1, 205, generator=gen(2)) * 1e35
+    for i, v in enumerate(special):
+        x[i, 11] = x[i, 131] = x[i, 203] = v
+    x[-1, :13] = x[-1, 192:205] = torch.tensor(special)
+    q, s = quantise(x.cuda(), quant)
+    am = torch.where(x.isnan(), 0.0, x.abs()).amax(1, keepdim=True).clamp(min=EPS)
+    assert torch.equal(q.cpu().view(torch.uint8), codes_by_the_rule(x, 1.0 / am, quant))
+
+    # x = 1 and x^2 an exact sum: rstd = 1 / sqrt(1 + eps), y = w * rstd
+    T, H = 3, 256
+    w = torch.randn(H, generator=gen(3)) * 1e36
+    w[9], w[77], w[200] = 3e38, -2e38, 1e37
+    qd = moe.MOE_QUANT_INT8 if quant == "int8" else moe.MOE_QUANT_E4M3
+    out = torch.empty(T, H, dtype=torch.int8 if quant == "int8" else torch.float8_e4m3fn, device="cuda")
+    moe.moe_w8a8_norm_quant(moe.make_norm_dims(T, H, dtype=F32, quant=qd), torch.ones(T, H, device="cuda"), w.cuda(), q=out,
+                            q_scale=torch.empty(T, device="cuda"))
+    want = codes_by_the_rule(w, 1.0 / w.abs().max(), quant)
+    assert bool((out.cpu().view(torch.uint8) == want).all())
+
+
 # --------------------------------------------------------------- joining norm
 
 def inputs(T, H, dt, wt, share=True, ss=True, residual=True, post=True, pw=True, gate="row", weight=True, seed=0):
