@@ -16,7 +16,7 @@
 // and sum. The gradient reads a token's dout once for its K rows.
 //
 // In us, with the rate of what has to be read and written (a copy: 4.9 TB/s):
-// dispatch T 4096, E 256, K 8, H 4096, bf16, row_align 16 53.8 (4.7), T 8 4.8,
+// dispatch T 4096, E 256, K 8, H 4096, bf16, row_align 16 54 (4.7), T 8 4.8,
 // a launch; combine T 2047, K 6, H 5003, bf16 to fp32 28.2 (5.0), T 8 4.1; the
 // gradient T 4096, K 8, H 4096 118 (4.9).
 //
