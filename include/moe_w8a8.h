@@ -693,9 +693,10 @@ typedef struct {
  *   y and the codes: those of moe_w8a8_norm_quant's norm of r (before its
  *   rounding) by weight
  *
- * fp32 operations in this order, each rounded by itself; mean(b^2) is summed
- * in fp64 and 1 / sqrt(...) rounded once. So r, and the codes as in
- * moe_w8a8_norm_quant, do not depend on the order of a sum.
+ * fp32 operations in this order, each rounded by itself; mean(b^2), and
+ * mean(r^2) here, are summed in fp64 and 1 / sqrt(...) is rounded once. So no
+ * output depends on the order of a sum: a token's are the same bits in every
+ * batch.
  *
  *  block         [T, H]
  *  share         [T, H] or NULL; share_scale fp32 [T] or NULL (all ones; NULL

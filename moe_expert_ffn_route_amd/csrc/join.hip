@@ -3,10 +3,13 @@
 //
 // Codes follow the block's rule (rowquant.h). As in norm.hip, those of y = p *
 // rstd come from p and max|p| alone, so that rstd enters only the scales (and
-// the codes of rows under the amax floor). The branch's own norm does enter p;
-// its mean square is summed in fp64 and 1 / sqrt rounded once to fp32, so that
-// the codes are the same whatever the order of that sum (it decides only sums
-// within 2^-50 or so of a rounding border of 1 / sqrt).
+// the codes of rows under the amax floor). The branch's own norm does enter p.
+// Both mean squares are summed in fp64 and 1 / sqrt rounded once to fp32, so
+// that every output is the same whatever the order of these sums, which is the
+// batch's (it decides only sums within 2^-50 or so of a rounding border of
+// 1 / sqrt). An fp32 sum of the second changed y with the batch and was no
+// faster than by 2 % (us, fp64 / fp32, H 4096: T 8 3.6 / 3.7, T 500 7.0 / 6.9, T
+// 8192 64.8 / 64.8).
 //
 // A row of up to 16384 elements stays in the registers of one workgroup
 // between the one read of its inputs and the writes: what bounds both
@@ -26,10 +29,23 @@ namespace {
 __device__ __forceinline__ float lane63(float v) {
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), kWave - 1));
 }
-__device__ __forceinline__ double wave_sum(double v) {  // in every lane
+__device__ __forceinline__ double lane63(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(b), kWave - 1);
+    const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(b >> 32), kWave - 1);
+    return __builtin_bit_cast(double, lo | (static_cast<uint64_t>(hi) << 32));
+}
+// 1 / sqrt(v), rounded once to fp32: the hardware's fp64 estimate y, off by
+// some 2^-23, and with e = 1 - v y^2 three terms of y (1 - e)^(-1/2), whose rest
+// (5/16 e^3) is under 2^-65: what is left are fp64 roundings. (With a root and a
+// division, and sums by shuffles instead of DPP: T 8, H 4096 4.03 us, now 3.65.)
+__device__ __forceinline__ float root_of(double v) {
+    const double y = __builtin_amdgcn_rsq(v), e = __builtin_fma(-v * y, y, 1.0);
+    return static_cast<float>(__builtin_fma(y * e, __builtin_fma(e, 0.375, 0.5), y));
+}
+__device__ __forceinline__ void add_squares(const float (&v)[kVec], double &sum) {
 #pragma unroll
-    for (int d = kWave / 2; d > 0; d >>= 1) v += __shfl_xor(v, d, kWave);
-    return v;
+    for (int e = 0; e < kVec; ++e) sum = __builtin_fma(static_cast<double>(v[e]), static_cast<double>(v[e]), sum);
 }
 
 // A workgroup is one row, its threads as many whole waves as CH chunks of kVec
@@ -91,8 +107,8 @@ __global__ __launch_bounds__((kMost<CH, ONE>)) void quant_kernel(QuantArgs a) {
 
 template <typename T, typename W, int CH, bool TAIL, bool ONE>
 __global__ __launch_bounds__((kMost<CH, ONE>)) void join_norm_kernel(JoinNormArgs a) {
-    __shared__ double s_sq[16];
-    __shared__ float s_sum[16], s_max[16];
+    __shared__ double s_sq[2][16];
+    __shared__ float s_max[16];
     const int tpr = ONE ? kWave : static_cast<int>(blockDim.x), waves = tpr / kWave;
     const int tr = ONE ? threadIdx.x % kWave : threadIdx.x, row = ONE ? blockIdx.x * 4 + threadIdx.x / kWave : blockIdx.x;
     if (ONE && row >= a.T) return;  // whole waves, and such a row has no barrier
@@ -108,6 +124,7 @@ __global__ __launch_bounds__((kMost<CH, ONE>)) void join_norm_kernel(JoinNormArg
 
     // b, and what will be needed later on its way
     float p[CH][kVec] = {}, r[CH][kVec] = {}, pt = 0.0f, rt = 0.0f;
+    const double inv_h = 1.0 / a.H;  // while the loads are under way
     const float ss = a.share_scale ? a.share_scale[row] : 1.0f;
     if (whole) {
 #pragma unroll
@@ -137,14 +154,12 @@ __global__ __launch_bounds__((kMost<CH, ONE>)) void join_norm_kernel(JoinNormArg
     if (a.post_norm) {
         double sq = tail ? static_cast<double>(pt) * pt : 0.0;
 #pragma unroll
-        for (int j = 0; j < CH; ++j) {
-            if (tr + j * tpr >= chunks) continue;
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) sq = __builtin_fma(static_cast<double>(p[j][e]), static_cast<double>(p[j][e]), sq);
-        }
-        sq = wave_sum(sq);
-        if constexpr (!ONE) sq = join_waves(sq, s_sq, tr, waves, 0.0, [](double u, double v) { return u + v; });
-        const float rstd = static_cast<float>(1.0 / sqrt(sq / a.H + static_cast<double>(a.post_eps)));
+        for (int j = 0; j < CH; ++j)
+            if (tr + j * tpr < chunks) add_squares(p[j], sq);
+        sq = last_lane_sum(sq);
+        if constexpr (ONE) sq = lane63(sq);
+        else sq = join_waves(sq, s_sq[0], tr, waves, 0.0, [](double u, double v) { return u + v; });
+        const float rstd = root_of(sq * inv_h + static_cast<double>(a.post_eps));
         if (pw && whole) {
             float v[CH][kVec];
 #pragma unroll
@@ -196,15 +211,15 @@ __global__ __launch_bounds__((kMost<CH, ONE>)) void join_norm_kernel(JoinNormArg
 #pragma unroll
         for (int j = 0; j < CH; ++j) load8(w + at(j), r[j]);
     }
-    float sum = 0.0f, mx = 0.0f;
+    double sum = 0.0;
+    float mx = 0.0f;
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
         if (tr + j * tpr >= chunks) {
 #pragma unroll
             for (int e = 0; e < kVec; ++e) p[j][e] = 0.0f;
         }
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) sum += p[j][e] * p[j][e];
+        add_squares(p[j], sum);
         if (w) {
 #pragma unroll
             for (int e = 0; e < kVec; ++e) p[j][e] = p[j][e] * r[j][e];
@@ -214,7 +229,7 @@ __global__ __launch_bounds__((kMost<CH, ONE>)) void join_norm_kernel(JoinNormArg
     }
     if (TAIL) {
         if (!tail) pt = 0.0f;
-        sum += pt * pt;
+        sum = __builtin_fma(static_cast<double>(pt), static_cast<double>(pt), sum);
         if (tail && w) pt = pt * to_f32(w[it]);
         mx = fmaxf(mx, fabsf(pt));
     }
@@ -225,12 +240,10 @@ __global__ __launch_bounds__((kMost<CH, ONE>)) void join_norm_kernel(JoinNormArg
         mx = lane63(mx);
     } else {
         if ((tr & (kWave - 1)) == kWave - 1) s_max[tr / kWave] = mx;
-        sum = join_waves(sum, s_sum, tr, waves, 0.0f, [](float u, float v) { return u + v; });
-        mx = (tr & 15) < waves ? s_max[tr & 15] : 0.0f;
-#pragma unroll
-        for (int d = 8; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor(mx, d, kWave));
+        sum = join_waves(sum, s_sq[1], tr, waves, 0.0, [](double u, double v) { return u + v; });
+        mx = join_lanes((tr & 15) < waves ? s_max[tr & 15] : 0.0f, [](float u, float v) { return fmaxf(u, v); });
     }
-    const float rstd = 1.0f / sqrtf(sum / static_cast<float>(a.H) + a.rms_eps);
+    const float rstd = root_of(sum * inv_h + static_cast<double>(a.rms_eps));
     if (a.y) {
         T *y = static_cast<T *>(a.y) + base;
 #pragma unroll

@@ -50,19 +50,46 @@ __device__ __forceinline__ float last_lane_max(float v) {  // of magnitudes
     v = fmaxf(v, dpp_or<0x143>(v, 0.0f));
     return v;
 }
+// DPP on both words of an fp64; lanes that nothing reaches take zero.
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ double dpp_or_zero(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(b), CTRL, ROWS, 0xF, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(b >> 32), CTRL, ROWS, 0xF, false);
+    return __builtin_bit_cast(double, lo | (static_cast<uint64_t>(hi) << 32));
+}
+__device__ __forceinline__ double last_lane_sum(double v) {
+    v += dpp_or_zero<0x111>(v);
+    v += dpp_or_zero<0x112>(v);
+    v += dpp_or_zero<0x114>(v);
+    v += dpp_or_zero<0x118>(v);
+    v += dpp_or_zero<0x142, 0xA>(v);
+    v += dpp_or_zero<0x143, 0xC>(v);
+    return v;
+}
+
+// The join of the values of a row of 16 lanes, in each of them: mirrors of the
+// row and of its halves, pairs, neighbours.
+template <int CTRL>
+__device__ __forceinline__ float swapped(float v) { return dpp_or<CTRL>(v, 0.0f); }
+template <int CTRL>
+__device__ __forceinline__ double swapped(double v) { return dpp_or_zero<CTRL>(v); }
+template <typename V, typename Join>
+__device__ __forceinline__ V join_lanes(V v, Join join) {
+    v = join(v, swapped<0x140>(v));
+    v = join(v, swapped<0x141>(v));
+    v = join(v, swapped<0x4E>(v));
+    return join(v, swapped<0xB1>(v));
+}
 
 // The same for the workgroup of a row, of `waves` waves (at most 16): lane 63's
-// values meet in `slot`, each lane takes one, and four steps join them, in every
-// lane. With a barrier.
+// values meet in `slot`, and each lane of a row of 16 takes one. With a barrier.
 template <typename V, typename Join>
 __device__ __forceinline__ V join_waves(V v, V *slot, int tr, int waves, V none, Join join) {
     if ((tr & (kWave - 1)) == kWave - 1) slot[tr / kWave] = v;
     __syncthreads();
     const int i = tr & 15;
-    v = i < waves ? slot[i] : none;
-#pragma unroll
-    for (int d = 8; d > 0; d >>= 1) v = join(v, __shfl_xor(v, d, kWave));
-    return v;
+    return join_lanes(i < waves ? slot[i] : none, join);
 }
 
 // Eight codes of a row, quant4's bits: t = (v * Q) * inv, brought to [-Q, Q]

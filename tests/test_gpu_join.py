@@ -442,3 +442,36 @@ def test_no_token():
     q, s = moe.moe_w8a8_quant(moe.make_quant_dims(0, 64), x)
     assert q.shape == (0, 64) and s.shape == (0,)
     moe.moe_w8a8_join_norm(moe.make_join_norm_dims(0, 64), x, y=x)
+
+
+@pytest.mark.parametrize("H", [4200, 5003, 9000])
+@pytest.mark.parametrize("post", [False, True])
+def test_every_output_is_the_same_in_every_batch(H, post):
+    """fp32, so that the last bit of 1 / sqrt of either mean square shows in y
+    and in q_scale; a third of the rows lie under the floor, and their codes go
+    by that root too. 100 and 700 rows take unlike workgroups."""
+    c = inputs(700, H, F32, F32, post=post, gate=None if post else "token", seed=23)
+    for k in ("block", "share", "residual"):
+        c[k][::3] *= 1e-8
+    part = {k: v if v is None or v.shape[0] != 700 else v[:100].contiguous() for k, v in c.items()}
+    for quant, group in (("int8", 0), ("e4m3", 0)):
+        eps = (1e-5, 1e-6, 1e-3)
+        whole, few = join(c, post, quant, group, eps=eps), join(part, post, quant, group, eps=eps)
+        for k in whole:
+            assert torch.equal(whole[k][:100].view(torch.uint8), few[k].view(torch.uint8)), (k, quant)
+
+
+@pytest.mark.parametrize("T,H", [(5, 512), (33, 5003), (600, 4096), (520, 16384), (3, 16381)])
+def test_the_norm_of_the_stream_is_rounded_once(T, H):
+    """r = block exactly. In units of u = 2^-24: y is a product by the weight,
+    one by 1 / sqrt(...) and that root, each rounded once: 3 u. q_scale is the
+    largest of these times 1 / Q, one product and one constant more: 5 u. (And
+    what is summed in 64 bits, under 2^-40.)"""
+    c = inputs(T, H, F32, F32, share=False, residual=False, post=False, gate=None, seed=29)
+    out = join(c, False, rs=1.0, bs=1.0)
+    r, w = c["block"].double(), c["weight"].double()
+    y = r * w / torch.sqrt((r * r).mean(1, keepdim=True) + float(f32(1e-6)))
+    more = 1 + 2.0 ** -16  # products of the bounds
+    assert bool(((out["y"].double() - y).abs() <= 3 * U * more * y.abs()).all())
+    s = y.abs().amax(1) / 127
+    assert bool(((out["q_scale"].double() - s).abs() <= 5 * U * more * s).all())
