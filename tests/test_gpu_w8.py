@@ -221,3 +221,31 @@ def test_no_token():
     c = make(1, 32, 64, bias=False)
     out = moe.moe_w8a8_linear_w8(moe.make_linear_w8_dims(0, 32, 64), c["x"][:0].cuda(), c["xs"][:0].cuda(), pack(c))
     assert out.shape == (0, 32)
+
+
+# One shape at least for every kernel that a product can take, with whole and odd rows (test_w8_rule.py checks that they do)
+EVERY = [(5, 100, 512), (7, 90, 515), (12, 200, 1024), (16, 330, 1001), (9, 8300, 256), (14, 8202, 263), (40, 500, 2000),
+         (33, 610, 777), (40, 2000, 640), (45, 2018, 1037), (64, 4096, 4096), (64, 4096, 4099), (40, 4800, 2048),
+         (37, 4810, 1155), (64, 6000, 512), (100, 3000, 3999), (64, 10000, 528), (63, 9990, 531), (4096, 4096, 1936),
+         (4090, 4102, 1933), (2048, 3200, 2064), (2040, 3206, 2061), (1088, 2944, 208), (1080, 2950, 201),
+         (1088, 2944, 2064), (1080, 2950, 2071), (2500, 5000, 704), (2500, 5000, 700), (640, 2048, 2064), (630, 2050, 2057),
+         (640, 1920, 2064), (630, 1910, 2059), (640, 2560, 272), (630, 2570, 261), (100, 1000, 112), (90, 1010, 101)]
+
+
+@pytest.mark.parametrize("T,N,K", EVERY)
+def test_every_kernel(T, N, K):
+    c = make(T, N, K, bias=True, seed=31)
+    acc, packed, gated = sums(c), pack(c), pack(c, True)
+    for dt in (BF, FP, F32):
+        check(c, run(c, dt, packed=packed), acc=acc)
+        check(c, run(c, dt, gated=True, packed=gated), gated=True, acc=acc)
+        c["bias"] = None
+
+
+def test_short_rows_and_a_wide_output():
+    """Outputs of 240 MB, streamed, of two tiles of k."""
+    c = make(6000, 20000, 100, bias=True, seed=37)
+    out = run(c, BF)
+    for t in range(0, 6000, 2000):  # fp64 values of a part at a time
+        part = dict(c, x=c["x"][t:t + 2000], xs=c["xs"][t:t + 2000])
+        check(part, out[t:t + 2000])
