@@ -498,3 +498,37 @@ def test_dispatch_at_the_borders_of_its_launches(T, K):
         for kind in ("random", "dropped"):
             check_dispatch(ids_of(T, 48, K, kind=kind), 48, 200, I8, groups=3, align=align)
             check_dispatch(ids_of(T, 48, K, kind=kind), 48, 1, I8, align=align)
+
+
+# Calls that write 16 MB or more, whose stores are streamed: every launch of dispatch, rows that end inside 16 bytes
+
+@pytest.mark.parametrize("T,E,K,H,dt,groups,align", [
+    (8, 64, 8, 4100, I8, 3, 256), (12, 40, 5, 8200, BF, 0, 256), (500, 20, 8, 5003, BF, 0, 16), (480, 70, 8, 5003, I8, 2, 16),
+    (2100, 20, 4, 1003, BF, 0, 16), (2100, 20, 4, 2051, I8, 1, 16), (17000, 60, 4, 515, FP, 0, 16), (17000, 60, 4, 517, I8, 5, 1),
+    (4100, 33, 6, 333, F32, 0, 64), (1030, 8, 4, 4096, F8, 32, 16)])
+def test_dispatch_streamed(T, E, K, H, dt, groups, align):
+    for kind in ("random", "dropped"):
+        d, out = check_dispatch(ids_of(T, E, K, kind=kind), E, H, dt, groups=groups, align=align)
+    assert out["rows"].numel() * out["rows"].element_size() >= 16 << 20
+
+
+@pytest.mark.parametrize("T,E,K,H", [(2047, 72, 6, 5003), (2048, 64, 8, 4104), (4100, 20, 1, 2501), (1100, 40, 12, 8200),
+                                     (40000, 50, 2, 217), (1030, 30, 3, 8193)])
+@pytest.mark.parametrize("dt,out_dt", TYPES, ids=TYPE_IDS)
+def test_combine_streamed(T, E, K, H, dt, out_dt):
+    assert T * H * out_dt.itemsize >= 16 << 20
+    c = case(T, E, K, H, dt, out_dt, "dropped", seed=3)
+    assert torch.equal(combine(c, out_dt, addend=False), combined(c, out_dt, addend=False))
+    assert torch.equal(combine(c, out_dt, in_place=True), combined(c, out_dt))
+    assert torch.equal(combine(c, out_dt, weights=False), combined(c, out_dt, weights=False))
+
+
+@pytest.mark.parametrize("T,E,K,H", [(600, 40, 8, 2003), (520, 30, 5, 4104), (300, 50, 12, 4099), (400, 20, 16, 2056),
+                                     (9000, 20, 2, 501)])
+@pytest.mark.parametrize("dt,out_dt", TYPES, ids=TYPE_IDS)
+def test_grad_streamed(T, E, K, H, dt, out_dt):
+    c = case(T, E, K, H, dt, out_dt, "dropped", align=16, seed=4)
+    assert c["rows"].numel() * dt.itemsize >= 16 << 20
+    check_grads(c, *grads(c))
+    dr, _ = grads(c, weights=False, dscales=False)
+    check_grads(c, dr, None, weights=False)

@@ -475,3 +475,24 @@ def test_the_norm_of_the_stream_is_rounded_once(T, H):
     assert bool(((out["y"].double() - y).abs() <= 3 * U * more * y.abs()).all())
     s = y.abs().amax(1) / 127
     assert bool(((out["q_scale"].double() - s).abs() <= 5 * U * more * s).all())
+
+
+@pytest.mark.parametrize("T,H,group", [(4200, 4096, 128), (4001, 5003, 0), (40000, 500, 0), (40000, 448, 64), (1100, 16381, 0),
+                                       (1030, 16384, 256)])
+@pytest.mark.parametrize("dt", [BF, FP, F32], ids=NAMES.get)
+def test_rows_streamed(T, H, group, dt):
+    """16 MB of codes or more."""
+    assert T * H >= 16 << 20
+    g = torch.Generator("cuda").manual_seed(T + H)
+    x = (torch.randn(T, H, generator=g, device="cuda") * 3).to(dt)
+    sm = 0.5 + torch.rand(H, generator=g, device="cuda")
+    check_quant(x, *quantise(x, "int8", group, sm), "int8", group, sm)
+    check_quant(x, *quantise(x, "e4m3", group), "e4m3", group, None)
+
+
+@pytest.mark.parametrize("T,H,group", [(1100, 5003, 0), (1030, 8192, 128), (20000, 500, 0), (400, 16381, 0)])
+@pytest.mark.parametrize("dt", [BF, FP, F32], ids=NAMES.get)
+def test_join_streamed(T, H, group, dt):
+    for quant, gate in (("int8", "row"), ("e4m3", "token")):
+        c = inputs(T, H, dt, F32, gate=gate, seed=31)
+        check_join(c, join(c, True, quant, group), True, quant, group)
