@@ -707,7 +707,9 @@ def moe_w8a8_combine(dims: CombineDims, rows, row_of_pair, expert_scales=None, a
     """Sorted rows [R, H] back to their tokens, weighted by expert_scales fp32
     [T, K] if given, plus addend [T, H] if given (may be out). Returns out
     [T, H] (dims.out_dtype), allocated if None. Without expert_scales it is
-    the gradient of moe_w8a8_dispatch."""
+    the gradient of moe_w8a8_dispatch. As with every call here, autograd does
+    not record it: out is detached from rows, expert_scales and addend, and a
+    program that trains calls moe_w8a8_combine_grad in its own backward."""
     if out is None:
         _tensor(rows, "rows")
         if dims.num_tokens < 0 or dims.hidden <= 0:  # dims that no buffer can have

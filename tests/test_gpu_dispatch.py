@@ -532,3 +532,66 @@ def test_grad_streamed(T, E, K, H, dt, out_dt):
     check_grads(c, *grads(c))
     dr, _ = grads(c, weights=False, dscales=False)
     check_grads(c, dr, None, weights=False)
+
+
+class Dispatched(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, d, ids):
+        out = moe.moe_w8a8_dispatch(d, ids, x=x, rows=torch.zeros(moe.moe_w8a8_dispatch_rows(d), x.shape[1], device="cuda"))
+        ctx.row_of_pair = out["row_of_pair"]
+        ctx.mark_non_differentiable(out["row_of_pair"], out["pair_of_row"])
+        return out["rows"], out["row_of_pair"], out["pair_of_row"]
+
+    @staticmethod
+    def backward(ctx, drows, *_):
+        (T, K), (R, H) = ctx.row_of_pair.shape, drows.shape
+        return moe.moe_w8a8_combine(moe.make_combine_dims(T, H, K, R, dtype=F32), drows.contiguous(), ctx.row_of_pair), None, None
+
+
+class Combined(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, rows, weights, addend, row_of_pair, pair_of_row):
+        ctx.save_for_backward(rows, weights, row_of_pair, pair_of_row)
+        T, K = row_of_pair.shape
+        d = moe.make_combine_dims(T, rows.shape[1], K, rows.shape[0], dtype=F32)
+        return moe.moe_w8a8_combine(d, rows, row_of_pair, expert_scales=weights, addend=addend)
+
+    @staticmethod
+    def backward(ctx, dout):
+        rows, weights, row_of_pair, pair_of_row = ctx.saved_tensors
+        T, K = row_of_pair.shape
+        d = moe.make_combine_dims(T, rows.shape[1], K, rows.shape[0], dtype=F32)
+        drows, dweights, dout = torch.empty_like(rows), torch.empty_like(weights), dout.contiguous()
+        moe.moe_w8a8_combine_grad(d, dout, row_of_pair, pair_of_row, rows=rows, expert_scales=weights, drows=drows,
+                                  dscales=dweights)
+        return drows, dweights, dout, None, None
+
+
+def test_inside_autograd():
+    """A layer of a program's own experts (scales by expert) that trains, and
+    the same by torch's indexing in 64 bits. A gradient is a sum of products of
+    three factors, of at most T = 70 terms (scales: an expert's pairs; rows that
+    fill a tile add zeros) or H = 130 (weights): in any order 130 u of the terms'
+    magnitudes, and 3 u for the products."""
+    T, E, K, H = 70, 11, 4, 130
+    ids = ids_of(T, E, K, kind="dropped")
+    g = torch.Generator().manual_seed(8)
+    leaf = lambda *s: torch.randn(*s, generator=g).cuda().requires_grad_()  # noqa: E731
+    x, w, a, scale = leaf(T, H), leaf(T, K), leaf(T, H), leaf(E, H)
+    dout = torch.randn(T, H, generator=g).cuda()
+    d = moe.make_dispatch_dims(T, H, E, K, dtype=F32, row_align=4)
+    rows, row_of_pair, pair_of_row = Dispatched.apply(x, d, ids.cuda())
+    expert = ids.cuda().flatten().long()[pair_of_row.long().clamp(min=0)].clamp(0, E - 1)
+    out = Combined.apply(rows * scale[expert], w, a, row_of_pair, pair_of_row)
+    got = torch.autograd.grad(out, (x, w, a, scale), dout)
+
+    def plain_layer(x, w, a, scale):
+        kept = ((ids >= 0) & (ids < E)).cuda()
+        z = x[:, None] * scale[ids.cuda().long().clamp(0, E - 1)]
+        return (z * (w * kept)[..., None]).sum(1) + a
+    wide = [t.detach().double().requires_grad_() for t in (x, w, a, scale)]
+    want = torch.autograd.grad(plain_layer(*wide), wide, dout.double())
+    size = [t.detach().double().abs().requires_grad_() for t in (x, w, a, scale)]
+    mag = torch.autograd.grad(plain_layer(*size), size, dout.double().abs())
+    for one, two, m in zip(got, want, mag):
+        assert bool(((one.double() - two).abs() <= 133 * U * (1 + 2.0 ** -14) * m).all())
