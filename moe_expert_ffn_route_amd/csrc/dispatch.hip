@@ -33,7 +33,13 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
-constexpr int kSmallPairs = 4096;  // K 8, H 4096, int8: T 256 9.1 us in one launch, 13.7 in two; T 512 10.5 / 15.3
+// One launch up to here. In us, one / two (int8, H 4096, E 256; E 8 in brackets):
+//   512 pairs: K 8 6.7 / 13.4 (6.6 / 13.1), K 2 4.8 / 15.4 (4.9 / 15.2), K 1 4.7 / 18.1 (5.1 / 17.9)
+//   2048: K 8 9.1 / 14.6 (9.1 / 14.4), K 2 8.9 / 19.2 (11.5 / 18.9), K 1 11.6 / 21.8 (19.0 / 21.9)
+//   4096: K 8 10.5 / 14.3 (10.8 / 14.1), K 2 14.2 / 18.7 (23.7 / 18.8), K 1 25.2 / 23.9 (52.4 / 23.9)
+// Each of T workgroups counts all pairs, so with K 1 and few experts, whose LDS
+// counters are few too, the last row's border is too far.
+constexpr int kSmallPairs = 4096;
 constexpr int kParts = 16;        // workgroups of the second launch per block of the first
 constexpr int kScanBlocks = 64;   // more blocks are summed in a launch of their own
 

@@ -15,7 +15,7 @@
 // between the one read of its inputs and the writes: what bounds both
 // operators is memory. In us: quantiser T 8192, H 4096, bf16, groups of 128 16.5
 // (6.1 TB/s of reads and writes); joining norm T 4001, H 5003, fp16, post norm
-// and gate, y and E4M3 codes 42.5 to 45.7 (3.9 to 4.2 TB/s: rows start at odd
+// and gate, y and E4M3 codes 43.9 to 45.7 (3.9 to 4.1 TB/s: rows start at odd
 // addresses); at T 8 both 4 to 4.5, a launch and its round trips.
 #include "rowwise.h"
 

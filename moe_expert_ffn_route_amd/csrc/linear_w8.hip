@@ -155,7 +155,9 @@ __device__ __forceinline__ void finish(const LinearW8Args &a, int nt, int kq, in
 // loads leave of that. T 1, N 4096, K 4096 4.6 us (3.6 TB/s), T 64 6.5; odd rows
 // take one shift of the last tile more: T 37, N 5006, K 4251, gated 7.8.
 // More waves or tiles ahead are no faster: T 128, N 1383, K 9470 12.1 us, with 16
-// waves 12.7; T 37, N 5006, K 4251 8.4, with four tiles ahead 9.0.
+// waves 12.7; one / two / four tiles ahead (in a captured graph) T 37, N 5006, K
+// 4251 8.3 / 8.3 / 8.9, T 1, N 4096, K 4096 5.1 / 5.1 / 5.1, T 8, N 2048, K 16384
+// 9.2 / 7.9 / 7.8, T 8, N 28672, K 4096 23.5 / 22.9 / 24.4.
 constexpr int kFewWaves = 8;
 
 // Few tokens: a workgroup takes R tiles of 16 weight rows and ROWS tokens, its
@@ -279,9 +281,10 @@ __global__ __launch_bounds__(kFewWaves *kWave) void linear_w8_few_kernel(LinearW
 // through LDS, where all waves read it, one tile of 128 k (a stage) at a time;
 // weights come packed in operand order and go from memory to the wave's
 // registers, a stage ahead. Per stage a wave reads 2 MT KB of LDS for 2 MT NW
-// products of 16 cycles: four waves take 64 MT of their 32 MT NW cycles at 128
-// bytes a cycle, half of the time with NW = 4. (With both operands in LDS and
-// 64 x 64 sums per wave, reading LDS would take all of it.)
+// products of 16 cycles: four waves take 32 MT of their 32 MT NW cycles at 256
+// bytes a cycle (a loop of such reads alone reached 208), a quarter of the time
+// with NW = 4. (With both operands in LDS and 64 x 64 sums per wave it would be
+// half.)
 //
 // x lies in NB buffers, stage s in buffer s % NB, copied straight to LDS NB - 2
 // stages ahead (into a buffer whose operands every wave has multiplied by the
@@ -291,8 +294,13 @@ __global__ __launch_bounds__(kFewWaves *kWave) void linear_w8_few_kernel(LinearW
 //
 // Measured (T, N, K 8192, bf16 out): 2.44 POP/s, the library's int8 product 2.13;
 // the matrix units are busy 67 % of the cycles, at the 1.75 GHz that the clock
-// falls to under this load; reading LDS takes 18 %, and what is loaded is 30
-// bytes a cycle and CU. 256 tokens a workgroup (one wave per SIMD) was 35 %
+// falls to under this load; LDS is busy 18 % of them (SQ_LDS_IDX_ACTIVE: a
+// quarter of the matrix units' time, and the writes of the end), and what is
+// loaded is 30 bytes a cycle and CU. With one workgroup a CU (T 256, N 8192, K
+// 4096 or T 512, N 4096: 15.3 us, the operations' 8.1) a SIMD has one wave:
+// waves wait for loads and barriers 55 % of their cycles, the matrix units are
+// busy 22 %, and L2 gives 13 TB/s where plain reads by as many waves get 28:
+// latency. 256 tokens a workgroup (one wave per SIMD) was 35 %
 // slower.
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(1))) void glb_void;

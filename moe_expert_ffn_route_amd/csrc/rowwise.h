@@ -95,8 +95,8 @@ __device__ __forceinline__ V join_waves(V v, V *slot, int tr, int waves, V none,
 // Eight codes of a row, quant4's bits: t = (v * Q) * inv, brought to [-Q, Q]
 // (where v * Q leaves fp32) and rounded to nearest even, int8 by an addition
 // whose sum's last bits are the integer, E4M3 by the hardware's conversion,
-// which gives e4m3_code's bits for every fp32 of up to 464 (both compared once,
-// on all). A NaN gives -127 (the median of three is the smaller one then), or
+// which gives e4m3_code's bits for every fp32 of up to 464 (the codes of all
+// fp32 up to a row's largest are checked by tests/test_gpu_conversions.py). A NaN gives -127 (the median of three is the smaller one then), or
 // E4M3's NaN without a sign, for which a lane that has one takes quant4.
 __device__ __forceinline__ uint64_t quant8(const float (&v)[kVec], float inv, bool fp8) {
     uint32_t w[2];
